@@ -1,9 +1,10 @@
-"""Build libtmap.so (gfx950) in-tree with hipcc.
+"""Build libtmap.so and libtkv.so (gfx950) in-tree with hipcc.
 
     python -m tiled_tensor_bulk_amd.build [--jobs N]
 
 Each translation unit is compiled in parallel into tiled_tensor_bulk_amd/_build
-and linked into tiled_tensor_bulk_amd/libtmap.so.  Cross-compiles without a GPU.
+and linked into tiled_tensor_bulk_amd/libtmap.so (the tile copies) or
+libtkv.so (the 4-bit cache and its operators).  Cross-compiles without a GPU.
 """
 from __future__ import annotations
 
@@ -18,12 +19,15 @@ PKG = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libtmap.so")
+TKV_LIB = os.path.join(PKG, "libtkv.so")
 ROOT = os.path.dirname(PKG)
 
 SOURCES = (["tmap_host.cpp"] + [f"tmap_{m}_r{r}.hip" for m in ("load", "store", "roundtrip") for r in (2, 5)]
            + [f"tmap_band_{m}.hip" for m in ("load", "store", "roundtrip")]
            + [f"tmap_corner_{m}.hip" for m in ("load", "store", "roundtrip")]
            + [f"tmap_corner4_{m}.hip" for m in ("load", "store", "roundtrip")] + ["tmap_noalloc.hip"])
+TKV_SOURCES = (["tkv_host.cpp"] + [f"tkv_attend_d{d}.hip" for d in (256, 128, 96, 64)]
+               + ["tkv_combine.hip", "tkv_evict.hip", "tkv_move.hip"])
 ARCH = "gfx950"
 
 
@@ -43,28 +47,25 @@ def common_flags():
 
 def build(jobs: int = 7, verbose: bool = False, incremental: bool = False) -> str:
     """Compile every translation unit (or, with incremental=True, only those
-    older than a source or header) and link libtmap.so."""
+    older than a source or header) and link both libraries."""
     os.makedirs(BUILD, exist_ok=True)
     cc = hipcc()
     procs = []
-    objs = []
     t0 = time.time()
     newest_hdr = max(os.path.getmtime(os.path.join(d, f)) for d in (CSRC, os.path.join(ROOT, "include"))
                      for f in os.listdir(d) if f.endswith(".h"))
     pending = []
-    for src in SOURCES:
+    for src in TKV_SOURCES + SOURCES:
         obj = os.path.join(BUILD, src + ".o")
         if (incremental and os.path.exists(obj)
                 and os.path.getmtime(obj) > max(newest_hdr, os.path.getmtime(os.path.join(CSRC, src)))):
-            objs.append(obj)
-        else:
-            pending.append(src)
+            continue
+        pending.append(src)
     running = []
     while pending or running:
         while pending and len(running) < max(1, jobs):
             src = pending.pop(0)
             obj = os.path.join(BUILD, src + ".o")
-            objs.append(obj)
             cmd = [cc, *common_flags(), "-c", os.path.join(CSRC, src), "-o", obj]
             if verbose:
                 print(" ".join(cmd), flush=True)
@@ -79,12 +80,13 @@ def build(jobs: int = 7, verbose: bool = False, incremental: bool = False) -> st
             raise RuntimeError(f"compiling {src} failed")
         if verbose and lines:
             print("\n".join(lines))
-    tmp = LIB + ".tmp"
-    cmd = [cc, f"--offload-arch={ARCH}", "-shared", "-fPIC", "-o", tmp, *objs]
-    subprocess.check_call(cmd)
-    os.replace(tmp, LIB)
+    for lib, sources in ((LIB, SOURCES), (TKV_LIB, TKV_SOURCES)):
+        tmp = lib + ".tmp"
+        objs = [os.path.join(BUILD, src + ".o") for src in sources]
+        subprocess.check_call([cc, f"--offload-arch={ARCH}", "-shared", "-fPIC", "-o", tmp, *objs])
+        os.replace(tmp, lib)
     if verbose:
-        print(f"built {LIB} in {time.time() - t0:.1f}s", flush=True)
+        print(f"built {LIB} and {TKV_LIB} in {time.time() - t0:.1f}s", flush=True)
     return LIB
 
 

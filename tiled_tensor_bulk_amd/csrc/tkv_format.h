@@ -1,0 +1,173 @@
+// tkv_format.h -- device side of the cache's record format (tkv.h): where
+// things lie, and how 8 codes become a matrix operand.
+#pragma once
+
+#include <hip/hip_runtime.h>
+
+#include "tkv_internal.h"
+
+namespace tkv {
+
+typedef _Float16 h2 __attribute__((ext_vector_type(2)));
+typedef _Float16 h8 __attribute__((ext_vector_type(8)));
+typedef float f4 __attribute__((ext_vector_type(4)));
+
+template <int D, int GROUP>
+struct Format {
+    static constexpr int W = D / 32;            // words of a lane in half a record's K (or V) codes
+    static constexpr int S = W > 4 ? 2 : 1;     // ... in this many runs
+    static constexpr int WV = W / S;            // ... of this many words
+    static constexpr int NG = D / GROUP;        // groups of channels
+    static constexpr int KG = GROUP / 32;       // K words of a group
+    static constexpr int VG = GROUP / 16;       // V words of a group
+    static constexpr int VC = 16 * D;           // byte offsets in a record
+    static constexpr int KP = 32 * D;
+    static constexpr int VP = 32 * D + 128 * NG;
+    static constexpr int REC = 32 * D + 256 * NG;
+};
+
+// N consecutive words (2, 3 or 4), 4-byte aligned at least.
+template <int N>
+struct __attribute__((packed, aligned(4))) Words {
+    uint32_t w[N];
+};
+
+template <int N>
+__device__ __forceinline__ void load_words(const char *p, uint32_t *out) {
+    if constexpr (N == 4) {
+        const uint4 v = *reinterpret_cast<const uint4 *>(p);
+        out[0] = v.x, out[1] = v.y, out[2] = v.z, out[3] = v.w;
+    } else if constexpr (N == 2) {
+        const uint2 v = *reinterpret_cast<const uint2 *>(p);
+        out[0] = v.x, out[1] = v.y;
+    } else {
+        const Words<N> v = *reinterpret_cast<const Words<N> *>(p);
+#pragma unroll
+        for (int i = 0; i < N; ++i) out[i] = v.w[i];
+    }
+}
+
+template <int N>
+__device__ __forceinline__ void store_words(char *p, const uint32_t *in) {
+    if constexpr (N == 4) {
+        *reinterpret_cast<uint4 *>(p) = make_uint4(in[0], in[1], in[2], in[3]);
+    } else if constexpr (N == 2) {
+        *reinterpret_cast<uint2 *>(p) = make_uint2(in[0], in[1]);
+    } else {
+        Words<N> v;
+#pragma unroll
+        for (int i = 0; i < N; ++i) v.w[i] = in[i];
+        *reinterpret_cast<Words<N> *>(p) = v;
+    }
+}
+
+// 8 codes as fp16, exactly.  0x6400 is 1024 in fp16, whose last place is 1:
+// or-ing a code below it gives 1024 + code (or 1024 + 16 * code for the
+// upper nibble of a byte), and the 1024 is taken off again: 1 shift, 4
+// and-ors and 4 packed operations for 8 elements.
+__device__ __forceinline__ h8 codes_to_half(uint32_t w) {
+    const uint32_t x = w >> 8;
+    const h2 low = {(_Float16)1024.0f, (_Float16)1024.0f};
+    const h2 s16 = {(_Float16)0.0625f, (_Float16)0.0625f};
+    const h2 b64 = {(_Float16)64.0f, (_Float16)64.0f};
+    const h2 a0 = __builtin_bit_cast(h2, (w & 0x000F000Fu) | 0x64006400u) - low;
+    const h2 a1 = __builtin_bit_cast(h2, (w & 0x00F000F0u) | 0x64006400u) * s16 - b64;
+    const h2 a2 = __builtin_bit_cast(h2, (x & 0x000F000Fu) | 0x64006400u) - low;
+    const h2 a3 = __builtin_bit_cast(h2, (x & 0x00F000F0u) | 0x64006400u) * s16 - b64;
+    return (h8){a0[0], a0[1], a1[0], a1[1], a2[0], a2[1], a3[0], a3[1]};
+}
+
+// The nibble of code j in its word.
+__device__ __forceinline__ constexpr int nibble_of(int j) { return (j >> 1) + 4 * (j & 1); }
+
+// New tokens of sequence b: their first row and their number.
+__device__ __forceinline__ void new_tokens(const Batch &b, int seq, int64_t &start, int &n) {
+    if (b.starts) {
+        const int64_t s = b.starts[seq], e = b.starts[seq + 1];
+        start = s;
+        int64_t m = e - s;
+        // rows outside the token tensors do not exist, whatever starts says
+        if (s < 0 || m < 0 || e > b.n_tokens) m = 0, start = 0;
+        n = (int)(m < b.max_new ? m : b.max_new);
+    } else {
+        start = (int64_t)seq * b.uniform;
+        n = b.uniform < b.max_new ? b.uniform : b.max_new;
+    }
+}
+
+// The page of a position, or -1 where there is none.
+__device__ __forceinline__ int page_at(const int32_t *row, int width, uint32_t n_pages, int index) {
+    if (index < 0 || index >= width) return -1;
+    const int p = row[index];
+    return p >= 0 && (uint32_t)p < n_pages ? p : -1;
+}
+
+// The record of positions 32 * tile .. 32 * tile + 31 of `head`, in `page`.
+__device__ __forceinline__ char *record_at(const Cache &c, int page, int head, int tile) {
+    const uint32_t in_page = (uint32_t)tile & ((1u << (c.page_shift - 5)) - 1);
+    return (char *)c.pool + (uint64_t)(uint32_t)page * c.page_bytes + (uint64_t)(uint32_t)head * c.head_bytes +
+           in_page * c.record;
+}
+
+__device__ __forceinline__ float bf16_to_float(uint16_t u) { return __builtin_bit_cast(float, (uint32_t)u << 16); }
+
+__device__ __forceinline__ uint16_t float_to_bf16(float f) {  // to nearest, ties to even; NaN stays NaN
+    const uint32_t u = __builtin_bit_cast(uint32_t, f);
+    if ((u & 0x7FFFFFFFu) > 0x7F800000u) return (uint16_t)((u >> 16) | 0x40);
+    return (uint16_t)((u + 0x7FFFu + ((u >> 16) & 1)) >> 16);
+}
+
+__device__ __forceinline__ float elem_to_float(uint16_t u, int type) {
+    return type == kBf16 ? bf16_to_float(u) : (float)__builtin_bit_cast(_Float16, u);
+}
+
+__device__ __forceinline__ uint16_t float_to_elem(float f, int type) {
+    return type == kBf16 ? float_to_bf16(f) : __builtin_bit_cast(uint16_t, (_Float16)f);
+}
+
+// 8 consecutive elements of a row as floats.
+__device__ __forceinline__ void load8(const Tokens &t, int64_t offset, float *out) {
+    uint16_t e[8];
+    const uint16_t *p = (const uint16_t *)t.data + offset;
+    if (t.wide) {
+        const uint4 v = *reinterpret_cast<const uint4 *>(p);
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) e[2 * i] = (uint16_t)w[i], e[2 * i + 1] = (uint16_t)(w[i] >> 16);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) e[i] = p[i];
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) out[i] = elem_to_float(e[i], t.type);
+}
+
+// 8 consecutive elements of a row, rounded to its type.
+__device__ __forceinline__ void store8(const Tokens &t, int64_t offset, const float *in) {
+    if (t.type == kF32) {
+        float *p = (float *)t.data + offset;
+        if (t.wide) {
+            reinterpret_cast<float4 *>(p)[0] = make_float4(in[0], in[1], in[2], in[3]);
+            reinterpret_cast<float4 *>(p)[1] = make_float4(in[4], in[5], in[6], in[7]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) p[i] = in[i];
+        }
+        return;
+    }
+    uint16_t *p = (uint16_t *)t.data + offset;
+    uint16_t e[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) e[i] = float_to_elem(in[i], t.type);
+    if (t.wide) {
+        uint32_t w[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w[i] = e[2 * i] | ((uint32_t)e[2 * i + 1] << 16);
+        *reinterpret_cast<uint4 *>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) p[i] = e[i];
+    }
+}
+
+}  // namespace tkv

@@ -1,0 +1,380 @@
+// tkv_host.cpp -- host half of libtkv: the cache descriptor, the checks of
+// every call's arguments, the gfx950 gate and the split of attention's work.
+// Nothing here throws: details of a failure go into a fixed buffer.
+
+#include <hip/hip_runtime_api.h>
+
+#include <atomic>
+#include <cmath>
+#include <cstdarg>
+#include <cstdio>
+#include <cstring>
+
+#include "tkv_internal.h"
+
+namespace {
+
+using tkv::Cache;
+
+thread_local char g_detail[256];
+
+tmap_status fail(tmap_status st, const char *fmt, ...) __attribute__((format(printf, 2, 3)));
+tmap_status fail(tmap_status st, const char *fmt, ...) {
+    va_list ap;
+    va_start(ap, fmt);
+    vsnprintf(g_detail, sizeof g_detail, fmt, ap);
+    va_end(ap);
+    return st;
+}
+
+tmap_status ok() {
+    g_detail[0] = 0;
+    return TMAP_SUCCESS;
+}
+
+#define TKV_REQUIRE(cond, ...) \
+    do {                       \
+        if (!(cond)) return fail(TMAP_ERROR_INVALID_VALUE, __VA_ARGS__); \
+    } while (0)
+#define TKV_TRY(call)                              \
+    do {                                           \
+        const tmap_status st_ = (call);            \
+        if (st_ != TMAP_SUCCESS) return st_;       \
+    } while (0)
+
+bool decode(const tkv_cache *cache, Cache &c) {
+    if (!cache) return false;
+    std::memcpy(&c, cache, sizeof c);
+    return c.magic == tkv::kMagic;
+}
+
+bool aligned(const void *p, uintptr_t to) { return ((uintptr_t)p & (to - 1)) == 0; }
+
+// Compute units of the current device, which has to be a gfx950 one.
+tmap_status device(int &cus) {
+    static std::atomic<int> seen[64];  // 0: not looked at, -1: another device, else its compute units
+    int dev = -1;
+    if (hipGetDevice(&dev) != hipSuccess || dev < 0 || dev >= 64) {
+        (void)hipGetLastError();
+        return fail(TMAP_ERROR_UNSUPPORTED_DEVICE, "no HIP device is available");
+    }
+    int v = seen[dev].load(std::memory_order_relaxed);
+    if (v == 0) {
+        hipDeviceProp_t p;
+        if (hipGetDeviceProperties(&p, dev) != hipSuccess) {
+            (void)hipGetLastError();
+            return fail(TMAP_ERROR_UNSUPPORTED_DEVICE, "cannot query HIP device %d", dev);
+        }
+        v = std::strncmp(p.gcnArchName, "gfx950", 6) == 0 && p.multiProcessorCount > 0 ? p.multiProcessorCount : -1;
+        seen[dev].store(v, std::memory_order_relaxed);
+    }
+    if (v < 0) return fail(TMAP_ERROR_UNSUPPORTED_DEVICE, "device %d is not gfx950", dev);
+    cus = v;
+    return TMAP_SUCCESS;
+}
+
+tmap_status launched(int rc) {
+    if (rc != 0) return fail(TMAP_ERROR_LAUNCH, "launch failed: %s", hipGetErrorString((hipError_t)rc));
+    return ok();
+}
+
+constexpr int64_t kMostBlocks = 0x7FFFFFFF;
+
+tmap_status check_batch(const tkv_batch *in, tkv::Batch &b, bool tokens) {
+    TKV_REQUIRE(in, "batch is NULL");
+    TKV_REQUIRE(in->n_seq >= 0, "n_seq is negative");
+    TKV_REQUIRE(in->table_width >= 0 && in->table_stride >= in->table_width,
+                "table_width must be >= 0 and at most table_stride");
+    TKV_REQUIRE(in->n_seq == 0 || (in->lens && aligned(in->lens, 4)), "lens is NULL or not 4-byte aligned");
+    TKV_REQUIRE(in->n_seq == 0 || in->table_width == 0 || (in->table && aligned(in->table, 4)),
+                "table is NULL or not 4-byte aligned");
+    b.table = in->table;
+    b.table_stride = in->table_stride;
+    b.lens = in->lens;
+    b.starts = nullptr;
+    b.n_tokens = 0;
+    b.n_seq = in->n_seq;
+    b.table_width = in->table_width;
+    b.max_new = b.uniform = 0;
+    if (!tokens) return TMAP_SUCCESS;
+    TKV_REQUIRE(in->n_tokens >= 0 && in->n_tokens <= 0x7FFFFFFF, "n_tokens must be in [0, 2^31)");
+    TKV_REQUIRE(in->max_new >= 0, "max_new is negative");
+    TKV_REQUIRE(!in->starts || aligned(in->starts, 4), "starts is not 4-byte aligned");
+    if (!in->starts && in->n_seq > 0) {
+        TKV_REQUIRE(in->n_tokens % in->n_seq == 0, "without starts, n_tokens must be a multiple of n_seq");
+        b.uniform = (int32_t)(in->n_tokens / in->n_seq);
+    }
+    b.starts = in->starts;
+    b.n_tokens = in->n_tokens;
+    b.max_new = in->max_new;
+    if (b.max_new > in->n_tokens) b.max_new = (int32_t)in->n_tokens;
+    return TMAP_SUCCESS;
+}
+
+tmap_status check_tokens(const tkv_tokens &in, const char *name, bool fp32_too, bool empty, tkv::Tokens &t) {
+    int size = 2;
+    switch (in.dtype) {
+        case TMAP_F16: t.type = tkv::kF16; break;
+        case TMAP_BF16: t.type = tkv::kBf16; break;
+        case TMAP_F32:
+            if (fp32_too) {
+                t.type = tkv::kF32;
+                size = 4;
+                break;
+            }
+            [[fallthrough]];
+        default: return fail(TMAP_ERROR_INVALID_VALUE, "%s must be fp16 or bf16%s", name, fp32_too ? " or fp32" : "");
+    }
+    TKV_REQUIRE(empty || (in.data && aligned(in.data, (uintptr_t)size)), "%s is NULL or not aligned to its elements", name);
+    TKV_REQUIRE(in.token_stride >= 0 && in.head_stride >= 0, "%s has a negative stride", name);
+    t.data = in.data;
+    t.token_stride = in.token_stride;
+    t.head_stride = in.head_stride;
+    t.wide = aligned(in.data, 16) && in.token_stride % 8 == 0 && in.head_stride % 8 == 0;
+    return TMAP_SUCCESS;
+}
+
+tmap_status move_args(const tkv_cache *cache, const tkv_tokens *k, const tkv_tokens *v, const tkv_batch *batch,
+                      bool fp32_too, tkv::MoveArgs &a) {
+    TKV_REQUIRE(decode(cache, a.c), "cache was never encoded");
+    TKV_REQUIRE(k && v, "k or v is NULL");
+    TKV_TRY(check_batch(batch, a.b, true));
+    TKV_TRY(check_tokens(*k, "k", fp32_too, a.b.n_tokens == 0, a.k));
+    TKV_TRY(check_tokens(*v, "v", fp32_too, a.b.n_tokens == 0, a.v));
+    TKV_REQUIRE(k->dtype == v->dtype, "k and v must have one type");
+    // a run of n positions that starts anywhere touches at most this many records
+    a.tiles = a.b.max_new == 0 ? 0 : (a.b.max_new + 2 * (tkv::kTile - 1)) / tkv::kTile;
+    TKV_REQUIRE((int64_t)a.tiles * a.b.n_seq * a.c.heads < kMostBlocks, "too many sequences, heads and new tokens");
+    return TMAP_SUCCESS;
+}
+
+// How attention is split: see plan().
+struct Split {
+    int row_tile, row_blocks, n_split, chunk, row_tiles;
+    uint64_t part_o, part_ml, frag_q, row_info, total;  // offsets, and bytes in all
+};
+
+uint64_t up(uint64_t v, uint64_t to) { return (v + to - 1) / to * to; }
+
+// Rows of a wave: as many as the registers of head_dim allow, no more than
+// there are.  Chunks: enough workgroups to fill the device, each with at
+// least kLeastChunk positions, as every chunk costs a partial sum.
+constexpr int kLeastChunk = 256;
+constexpr int kBlocksPerCu = 4;
+
+Split plan(const Cache &c, int64_t n_seq, int64_t rows, int64_t max_len, bool scores, int cus) {
+    Split s{};
+    const int most = c.dim <= 128 ? 64 : 32;
+    s.row_tile = rows <= 16 ? 16 : rows <= 32 ? 32 : most;
+    s.row_blocks = (int)((rows + s.row_tile - 1) / s.row_tile);
+    s.row_tiles = (int)((rows + 15) / 16);
+    const int64_t units = n_seq * c.heads * s.row_blocks;
+    const int64_t wanted = units ? ((int64_t)cus * kBlocksPerCu + units - 1) / units : 1;
+    const int64_t possible = (max_len + kLeastChunk - 1) / kLeastChunk;
+    int64_t n = wanted < possible ? wanted : possible;
+    if (n < 1) n = 1;
+    s.chunk = (int)up((uint64_t)((max_len + n - 1) / n), 128);
+    if (s.chunk < 128) s.chunk = 128;
+    s.n_split = (int)((max_len + s.chunk - 1) / s.chunk);
+    if (s.n_split < 1) s.n_split = 1;
+    const uint64_t heads = (uint64_t)n_seq * c.heads;
+    if (s.n_split > 1) {
+        s.part_o = s.total;
+        s.total = up(s.total + heads * s.n_split * rows * c.dim * 4, 256);
+        s.part_ml = s.total;
+        s.total = up(s.total + heads * s.n_split * rows * 8, 256);
+    }
+    if (scores) {
+        s.frag_q = s.total;
+        s.total = up(s.total + heads * s.row_tiles * 32 * c.dim, 256);
+        s.row_info = s.total;
+        s.total = up(s.total + heads * s.row_tiles * 16 * (2 + c.dim / c.group) * 4, 256);
+    }
+    return s;
+}
+
+tmap_status attend_args(const tkv_cache *cache, const tkv_attend_args *in, const tkv_batch *batch, bool pointers,
+                        tkv::AttendArgs &a) {
+    TKV_REQUIRE(decode(cache, a.c), "cache was never encoded");
+    TKV_REQUIRE(in, "args is NULL");
+    TKV_TRY(check_batch(batch, a.b, true));
+    const bool empty = !pointers || a.b.n_tokens == 0;
+    TKV_TRY(check_tokens(in->q, "q", false, empty, a.q));
+    TKV_TRY(check_tokens(in->out, "out", false, empty, a.out));
+    TKV_REQUIRE(in->q.dtype == in->out.dtype, "q and out must have one type");
+    TKV_REQUIRE(empty || (in->lse && aligned(in->lse, 4)), "lse is NULL or not 4-byte aligned");
+    TKV_REQUIRE(in->q_heads > 0 && in->q_heads % (int64_t)a.c.heads == 0, "q_heads must be a multiple of n_heads");
+    TKV_REQUIRE(in->max_len >= 0, "max_len is negative");
+    TKV_REQUIRE(std::isfinite(in->scale), "scale is not finite");
+    TKV_REQUIRE(in->causal == 0 || in->causal == 1, "causal must be 0 or 1");
+    if (in->scores_out) {
+        TKV_REQUIRE(aligned(in->scores_out, 4) && aligned(in->scores_in, 4), "scores are not 4-byte aligned");
+        TKV_REQUIRE(in->score_stride >= in->max_len, "score_stride is less than max_len");
+    } else {
+        TKV_REQUIRE(!in->scores_in, "scores_in without scores_out");
+    }
+    a.lse = in->lse;
+    a.scale_log2 = in->scale * 1.44269504089f;
+    a.causal = in->causal;
+    a.group_heads = in->q_heads / (int32_t)a.c.heads;
+    const int64_t rows = (int64_t)a.b.max_new * a.group_heads;
+    TKV_REQUIRE(rows < (1 << 30), "too many new tokens and query heads");
+    a.rows = (int32_t)rows;
+    a.max_len = in->max_len;
+    // no position lies past the table
+    const int64_t width = (int64_t)a.b.table_width << a.c.page_shift;
+    if (a.max_len > width) a.max_len = (int32_t)width;
+    a.scores_in = in->scores_in;
+    a.scores_out = in->scores_out;
+    a.score_stride = in->score_stride;
+    return TMAP_SUCCESS;
+}
+
+}  // namespace
+
+extern "C" {
+
+tmap_status tkv_encode(tkv_cache *cache, void *pool, int64_t n_pages, uint32_t n_heads, uint32_t head_dim,
+                       uint32_t page_tokens, uint32_t group) {
+    TKV_REQUIRE(cache, "cache is NULL");
+    TKV_REQUIRE(pool && aligned(pool, 16), "pool is NULL or not 16-byte aligned");
+    TKV_REQUIRE(n_pages >= 1 && n_pages < 0x7FFFFFFF, "n_pages must be in [1, 2^31 - 1)");
+    TKV_REQUIRE(n_heads >= 1 && n_heads <= 65535, "n_heads must be in [1, 65535]");
+    TKV_REQUIRE(head_dim == 64 || head_dim == 96 || head_dim == 128 || head_dim == 256,
+                "head_dim must be 64, 96, 128 or 256");
+    TKV_REQUIRE(page_tokens >= 32 && page_tokens <= 1024 && (page_tokens & (page_tokens - 1)) == 0,
+                "page_tokens must be a power of two in [32, 1024]");
+    TKV_REQUIRE((group == 32 || group == 64 || group == 128) && head_dim % group == 0,
+                "group must be 32, 64 or 128 and divide head_dim");
+    Cache c{};
+    c.pool = (uint64_t)(uintptr_t)pool;
+    c.n_pages = (uint32_t)n_pages;
+    c.heads = n_heads;
+    c.dim = head_dim;
+    c.group = group;
+    while ((1u << c.page_shift) < page_tokens) ++c.page_shift;
+    c.record = 32 * head_dim + 256 * (head_dim / group);
+    c.head_bytes = c.record * (page_tokens / tkv::kTile);
+    c.page_bytes = (uint64_t)c.head_bytes * n_heads;
+    c.magic = tkv::kMagic;
+    std::memcpy(cache, &c, sizeof c);
+    return ok();
+}
+
+uint64_t tkv_page_bytes(const tkv_cache *cache) {
+    Cache c;
+    return decode(cache, c) ? c.page_bytes : 0;
+}
+
+tmap_status tkv_append(const tkv_cache *cache, const tkv_tokens *k, const tkv_tokens *v, const tkv_batch *batch,
+                       void *hip_stream) {
+    tkv::MoveArgs a{};
+    TKV_TRY(move_args(cache, k, v, batch, false, a));
+    int cus = 0;
+    TKV_TRY(device(cus));
+    if (a.tiles == 0 || a.b.n_seq == 0) return ok();
+    return launched(tkv::launch_append(a, hip_stream));
+}
+
+tmap_status tkv_read(const tkv_cache *cache, const tkv_tokens *k, const tkv_tokens *v, const tkv_batch *batch,
+                     void *hip_stream) {
+    tkv::MoveArgs a{};
+    TKV_TRY(move_args(cache, k, v, batch, true, a));
+    int cus = 0;
+    TKV_TRY(device(cus));
+    if (a.tiles == 0 || a.b.n_seq == 0) return ok();
+    return launched(tkv::launch_read(a, hip_stream));
+}
+
+tmap_status tkv_attend_workspace(const tkv_cache *cache, const tkv_attend_args *args, const tkv_batch *batch,
+                                 uint64_t *bytes) {
+    tkv::AttendArgs a{};
+    TKV_REQUIRE(bytes, "bytes is NULL");
+    TKV_TRY(attend_args(cache, args, batch, false, a));
+    int cus = 0;
+    TKV_TRY(device(cus));
+    *bytes = a.rows > 0 && a.b.n_seq > 0 ? plan(a.c, a.b.n_seq, a.rows, a.max_len, a.scores_out, cus).total : 0;
+    return ok();
+}
+
+tmap_status tkv_attend(const tkv_cache *cache, const tkv_attend_args *args, const tkv_batch *batch, void *hip_stream) {
+    tkv::AttendArgs a{};
+    TKV_TRY(attend_args(cache, args, batch, true, a));
+    int cus = 0;
+    TKV_TRY(device(cus));
+    if (a.b.n_seq == 0 || a.rows == 0) return ok();
+    const Split s = plan(a.c, a.b.n_seq, a.rows, a.max_len, a.scores_out, cus);
+    TKV_REQUIRE((int64_t)a.b.n_seq * a.c.heads * s.n_split * s.row_blocks < kMostBlocks &&
+                    (int64_t)a.b.n_seq * a.c.heads * (a.max_len / 128 + 1) < kMostBlocks &&
+                    (int64_t)a.b.n_seq * a.c.heads * a.rows < kMostBlocks,
+                "too many sequences, heads and rows");
+    if (s.total) {
+        TKV_REQUIRE(args->workspace && aligned(args->workspace, 16), "workspace is NULL or not 16-byte aligned");
+        TKV_REQUIRE(args->workspace_bytes >= s.total, "workspace holds %llu bytes, %llu are needed",
+                    (unsigned long long)args->workspace_bytes, (unsigned long long)s.total);
+    }
+    char *ws = (char *)args->workspace;
+    a.row_blocks = s.row_blocks;
+    a.row_tiles = s.row_tiles;
+    a.n_split = s.n_split;
+    a.chunk = s.chunk;
+    if (s.n_split > 1) {
+        a.part_o = (float *)(ws + s.part_o);
+        a.part_ml = (float *)(ws + s.part_ml);
+    }
+    if (a.scores_out) {
+        a.frag_q = ws + s.frag_q;
+        a.row_info = (float *)(ws + s.row_info);
+        a.score_chunk = s.chunk < 1024 ? s.chunk : 1024;
+    }
+    switch (a.c.dim) {
+        case 64: return launched(tkv::launch_attend_d64(a, s.row_tile, hip_stream));
+        case 96: return launched(tkv::launch_attend_d96(a, s.row_tile, hip_stream));
+        case 128: return launched(tkv::launch_attend_d128(a, s.row_tile, hip_stream));
+        default: return launched(tkv::launch_attend_d256(a, s.row_tile, hip_stream));
+    }
+}
+
+tmap_status tkv_evict(const tkv_cache *cache, const tkv_evict_args *args, const tkv_batch *batch, void *hip_stream) {
+    tkv::EvictArgs a{};
+    TKV_REQUIRE(decode(cache, a.c), "cache was never encoded");
+    TKV_REQUIRE(args, "args is NULL");
+    TKV_TRY(check_batch(batch, a.b, false));
+    TKV_REQUIRE(args->budget >= 0 && args->recent >= 0, "budget or recent is negative");
+    TKV_REQUIRE(args->max_len >= 0 && args->score_stride >= args->max_len, "score_stride is less than max_len");
+    TKV_REQUIRE(args->dst_width >= 0 && args->dst_stride >= args->dst_width,
+                "dst_width must be >= 0 and at most dst_stride");
+    const bool any = a.b.n_seq > 0;
+    TKV_REQUIRE(!any || (args->lens_out && aligned(args->lens_out, 4)), "lens_out is NULL or not 4-byte aligned");
+    if (any && args->budget > 0) {
+        TKV_REQUIRE(args->kept && args->scores_out && aligned(args->kept, 4) && aligned(args->scores_out, 4),
+                    "kept or scores_out is NULL or not 4-byte aligned");
+        TKV_REQUIRE(args->max_len == 0 || (args->scores && aligned(args->scores, 4)),
+                    "scores is NULL or not 4-byte aligned");
+        TKV_REQUIRE(args->dst_width == 0 || (args->dst_table && aligned(args->dst_table, 4)),
+                    "dst_table is NULL or not 4-byte aligned");
+    }
+    TKV_REQUIRE((int64_t)a.b.n_seq * a.c.heads * ((int64_t)args->budget / tkv::kTile + 1) < kMostBlocks,
+                "too many sequences, heads and positions");
+    a.scores = args->scores;
+    a.scores_out = args->scores_out;
+    a.score_stride = args->score_stride;
+    a.kept = args->kept;
+    a.lens_out = args->lens_out;
+    a.dst_table = args->dst_table;
+    a.dst_stride = args->dst_stride;
+    a.dst_width = args->dst_width;
+    a.budget = args->budget;
+    a.recent = args->recent;
+    a.max_len = args->max_len;
+    const int64_t width = (int64_t)a.b.table_width << a.c.page_shift;
+    if (a.max_len > width) a.max_len = (int32_t)width;
+    int cus = 0;
+    TKV_TRY(device(cus));
+    if (!any) return ok();
+    return launched(tkv::launch_evict(a, hip_stream));
+}
+
+const char *tkv_last_error_detail(void) { return g_detail; }
+
+}  // extern "C"
