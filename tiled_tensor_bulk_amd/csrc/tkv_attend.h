@@ -14,10 +14,18 @@
 // Numbers.  With code c, scale s and zero z of a position and channel group,
 //   q . k = sum over groups of s * (q . c) + z * (sum of q)
 //   p . v = sum over positions of p * (s * c), plus p * z
-// q . c is a product of fp16 numbers, exact up to its fp32 sum (a bf16 row of
-// q is first scaled by a power of two to a largest magnitude in [2^14, 2^15),
-// so what fp16 drops is below 2^-38 of that); s and z come in at fp32.  For V, s * c is
-// rounded to fp16 (half a step is 2^-11 of it, relative), and so is p.
+// q . c is a product of fp16 numbers, exact up to its fp32 sum (a row of q is
+// first scaled by a power of two to a largest magnitude in [2^14, 2^15), and
+// its elements that meet an upper nibble by 2^-4 more, so what fp16 drops is
+// below 2^-35 of that largest); s and z come in at fp32.  For V, s * (c - 8) is
+// rounded to fp16 (half a step is 2^-11 of it, relative; with c itself, whose
+// numbers lie on one side of zero, the error of the sum was 3 times as
+// large), and so is p.  The sums of p * (z + 8 s) are two more rows of the
+// product: the groups' scales and zeros, as they lie, are rows of an operand,
+// and a row of ones gives the sum of the rounded p, by which the output is
+// divided: what rounding adds to a weight it then adds to both.  (256
+// channels in groups of 32 fill all 16 rows, and are divided by the sum of the
+// p before rounding.)  lse goes by the p before rounding.
 //
 // Softmax in one pass: each row keeps a reference m and sums exp2(y - m + 7)
 // of its scaled products y.  m moves only when a y passes m + 8, which keeps
@@ -49,7 +57,8 @@ struct KTile {
 template <int D, int GROUP>
 struct VTile {
     uint32_t w[2 * Format<D, GROUP>::W];
-    h8 scale[Format<D, GROUP>::NG], zero[Format<D, GROUP>::NG];  // of the lane's 8 positions
+    h8 scale[Format<D, GROUP>::NG];  // of the lane's 8 positions
+    h8 row;                          // row n of the operand of scales and zeros
 };
 
 template <int D, int GROUP>
@@ -67,6 +76,18 @@ __device__ __forceinline__ void load_k(const char *rec, int lane, KTile<D, GROUP
     }
 }
 
+// Rows 0, 1, 2, .. of the operand of scales and zeros are scale and zero of
+// each group as they lie in the record; then comes a row of ones, if there is
+// room, then zeros.
+template <int D, int GROUP>
+constexpr bool kOnes = 2 * Format<D, GROUP>::NG < 16;
+
+template <int D, int GROUP>
+__device__ __forceinline__ h8 one_row(int lane) {
+    const _Float16 x = (lane & 15) == 2 * Format<D, GROUP>::NG ? (_Float16)1.0f : (_Float16)0.0f;
+    return (h8){x, x, x, x, x, x, x, x};
+}
+
 template <int D, int GROUP>
 __device__ __forceinline__ void load_v(const char *rec, int lane, VTile<D, GROUP> &v) {
     using F = Format<D, GROUP>;
@@ -74,11 +95,11 @@ __device__ __forceinline__ void load_v(const char *rec, int lane, VTile<D, GROUP
     for (int hs = 0; hs < 2 * F::S; ++hs)
         load_words<F::WV>(rec + F::VC + ((hs * 64 + lane) * F::WV) * 4, &v.w[hs * F::WV]);
 #pragma unroll
-    for (int grp = 0; grp < F::NG; ++grp) {
-        const char *p = rec + F::VP + grp * 128 + (lane >> 4) * 16;
-        v.scale[grp] = *reinterpret_cast<const h8 *>(p);
-        v.zero[grp] = *reinterpret_cast<const h8 *>(p + 64);
-    }
+    for (int grp = 0; grp < F::NG; ++grp)
+        v.scale[grp] = *reinterpret_cast<const h8 *>(rec + F::VP + grp * 128 + (lane >> 4) * 16);
+    v.row = one_row<D, GROUP>(lane);
+    if ((lane & 15) < 2 * F::NG)
+        v.row = *reinterpret_cast<const h8 *>(rec + F::VP + (lane & 15) * 64 + (lane >> 4) * 16);
 }
 
 // A sequence's extent and the rows of one block.
@@ -112,7 +133,7 @@ struct Pages {
 };
 
 // Products of a record's 32 positions with the wave's rows, in fp32:
-// x[nt][4 * half + i] for position 16 half + 4 g + i.
+// x[nt][4 * half + i] for position 16 half + 4 g + i, times 2^-kCodeBits as qsum is.
 template <int D, int GROUP, int NT>
 __device__ __forceinline__ void products(const KTile<D, GROUP> &k, const h8 (&q)[NT][D / 32],
                                          const float (&qsum)[NT][D / GROUP], float (&x)[NT][8]) {
@@ -126,7 +147,7 @@ __device__ __forceinline__ void products(const KTile<D, GROUP> &k, const h8 (&q)
             for (int nt = 0; nt < NT; ++nt) acc[nt] = (f4){0, 0, 0, 0};
 #pragma unroll
             for (int c = 0; c < F::KG; ++c) {
-                const h8 key = codes_to_half(k.w[half][grp * F::KG + c]);
+                const h8 key = codes_as_bits(k.w[half][grp * F::KG + c]);
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
                     acc[nt] = __builtin_amdgcn_mfma_f32_16x16x32_f16(key, q[nt][grp * F::KG + c], acc[nt], 0, 0, 0);
@@ -146,117 +167,200 @@ __device__ __forceinline__ float over_groups_sum(float v) {  // over the four la
     v += __shfl_xor(v, 16);
     return v + __shfl_xor(v, 32);
 }
+__device__ __forceinline__ float over_rows_sum(float v) {  // over 16 neighbouring lanes, by rotations
+    v += __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), 0x128, 15, 15, true));
+    v += __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), 0x124, 15, 15, true));
+    v += __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), 0x122, 15, 15, true));
+    return v + __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), 0x121, 15, 15, true));
+}
 __device__ __forceinline__ float over_groups_max(float v) {
     v = fmaxf(v, __shfl_xor(v, 16));
     return fmaxf(v, __shfl_xor(v, 32));
 }
 
+// Four channels of an output row, and with the first ones its lse.
+__device__ __forceinline__ void write_row(const AttendArgs &a, const Extent &e, int seq, int head, int row, int channel,
+                                          f4 y, float best, float sum) {
+    const float inv = sum > 0.0f || sum != sum ? 1.0f / sum : 0.0f;
+    const int i = row / a.group_heads, hq = head * a.group_heads + row % a.group_heads;
+    store4(a.out, (e.start + i) * a.out.token_stride + hq * a.out.head_stride + channel, y * inv);
+    if (channel == 0) {
+        const float log_sum = best - kLift + log2f(sum);  // log2(0) = -inf: nothing seen
+        a.lse[(e.start + i) * (a.c.heads * a.group_heads) + hq] = log_sum * 0.69314718056f;
+        if (a.frag_q && (sum > 0.0f || sum != sum)) {
+            const int64_t tile = ((int64_t)seq * a.c.heads + head) * a.row_tiles + row / 16;
+            a.row_info[(tile * 16 + row % 16) * (2 + a.c.dim / a.c.group) + 1] = log_sum;
+        }
+    }
+}
+
+// Rows of one (sequence, head) as the right operand: lane (g, n) of a tile
+// holds channels 32 c + 8 g .. of row r.
+template <int D, int GROUP>
+struct Row {
+    uint4 raw[D / 32];
+    __device__ __forceinline__ void load(const AttendArgs &a, const Extent &e, int head, int r, int g, bool live) {
+        const int i = live ? r / a.group_heads : 0, hq = head * a.group_heads + (live ? r - i * a.group_heads : 0);
+        const int64_t row = (e.start + i) * a.q.token_stride + hq * a.q.head_stride + 8 * g;
+#pragma unroll
+        for (int c = 0; c < D / 32; ++c) raw[c] = live ? load8_raw(a.q, row + 32 * c) : make_uint4(0, 0, 0, 0);
+    }
+    // q, its sums over the groups of channels (times 2^-kCodeBits), and what
+    // turns products into logarithms to base 2: at least the smallest normal
+    // number, as masked products are -inf.
+    __device__ __forceinline__ void operand(const AttendArgs &a, h8 (&q)[D / 32], float (&qsum)[D / GROUP],
+                                            float &factor) const {
+        using F = Format<D, GROUP>;
+        float x[F::W][8], top = 0.0f;
+#pragma unroll
+        for (int c = 0; c < F::W; ++c) {
+            raw_to_float(raw[c], a.q.type, x[c]);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) top = fmaxf(top, fabsf(x[c][j]));
+        }
+        top = over_groups_max(top);
+        int power = 0;
+        if (top > 0.0f && top < __builtin_inff()) {
+            (void)frexpf(top, &power);  // top = m * 2^power, m in [0.5, 1)
+            power = 15 - power;
+        }
+        const float f = fabsf(ldexpf(a.scale_log2, kCodeBits - power));
+        factor = fminf(fmaxf(f, 0x1p-126f), 0x1.fffffep127f);
+        const float sign = a.scale_log2 < 0.0f ? -1.0f : 1.0f;
+#pragma unroll
+        for (int grp = 0; grp < F::NG; ++grp) qsum[grp] = 0.0f;
+#pragma unroll
+        for (int c = 0; c < F::W; ++c)
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const _Float16 v = (_Float16)ldexpf(sign * x[c][j], power - code_shift(j));
+                q[c][j] = v;
+                qsum[c / F::KG] = fmaf((float)v, (float)(1 << code_shift(j)), qsum[c / F::KG]);
+            }
+#pragma unroll
+        for (int grp = 0; grp < F::NG; ++grp) qsum[grp] = over_groups_sum(qsum[grp]) * (1.0f / (1 << kCodeBits));
+    }
+};
+
+// Where the scores kernel finds a tile of 16 rows and what belongs to it.
+template <int D, int GROUP>
+__device__ __forceinline__ void keep_rows(const AttendArgs &a, int64_t tile, int lane, const h8 (&q)[D / 32],
+                                          const float (&qsum)[D / GROUP], float factor) {
+    using F = Format<D, GROUP>;
+    h8 *to = (h8 *)a.frag_q + tile * (F::W * 64);
+#pragma unroll
+    for (int c = 0; c < F::W; ++c) to[c * 64 + lane] = q[c];
+    if (lane < 16) {
+        float *info = a.row_info + (tile * 16 + lane) * (2 + F::NG);
+        info[0] = factor;
+        info[1] = __builtin_inff();  // a row without positions weighs nothing
+#pragma unroll
+        for (int grp = 0; grp < F::NG; ++grp) info[2 + grp] = qsum[grp];
+    }
+}
+
+// What a row's running softmax holds, and one step of it: x (32 positions'
+// products) become weights p; o and z are scaled where the reference moves.
+template <int D, int GROUP>
+struct Softmax {
+    float m, l;
+    f4 o[D / 16], z;
+    __device__ __forceinline__ void clear() {
+        m = kFar;
+        l = 0.0f;
+        z = (f4){0, 0, 0, 0};
+#pragma unroll
+        for (int c = 0; c < D / 16; ++c) o[c] = (f4){0, 0, 0, 0};
+    }
+    static __device__ __forceinline__ float top(const float (&x)[8]) {
+        return fmaxf(fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])), fmaxf(fmaxf(x[4], x[5]), fmaxf(x[6], x[7])));
+    }
+    __device__ __forceinline__ void grow(float y) {  // y: the largest logarithm of the lane's 8
+        const float t = over_groups_max(y);
+        const float m1 = t > m + kSlack ? t : m;
+        const float f = exp2f(m - m1);
+        m = m1;
+        l *= f;
+        z *= f;
+#pragma unroll
+        for (int c = 0; c < D / 16; ++c) o[c] *= f;
+    }
+    __device__ __forceinline__ h8 weights(const float (&x)[8], float factor) {
+        const float lift = kLift - m;
+        h8 p;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const float w = __builtin_amdgcn_exp2f(fmaf(x[j], factor, lift));
+            l += w;
+            p[j] = (_Float16)w;
+        }
+        return p;
+    }
+    // after the last position: l whole in every lane, o what a division by l makes the output
+    __device__ __forceinline__ void finish(int lane) {
+        using F = Format<D, GROUP>;
+        l = over_groups_sum(l);
+        float ratio = 1.0f;
+        if constexpr (kOnes<D, GROUP>) {
+            const float rounded = __shfl(z[(2 * F::NG) & 3], 16 * (2 * F::NG / 4) + (lane & 15));
+            ratio = rounded > 0.0f ? l / rounded : 1.0f;
+        }
+#pragma unroll
+        for (int grp = 0; grp < F::NG; ++grp) {
+            const int from = 16 * (grp / 2) + (lane & 15);
+            const float zero = fmaf(8.0f, __shfl(z[(2 * grp) & 3], from), __shfl(z[(2 * grp + 1) & 3], from));
+#pragma unroll
+            for (int c = grp * F::VG; c < (grp + 1) * F::VG; ++c) o[c] = (o[c] + zero) * ratio;
+        }
+    }
+};
+
+// Waves of a SIMD that the registers of a wave leave room for: queries, sums
+// and logits of its rows, a record on its way, and what is being worked on.
 template <int D, int GROUP, int NT>
-__global__ void __launch_bounds__(64 * kAttendWaves) attend_kernel(const AttendArgs a) {
+struct FewRows {
+    using F = Format<D, GROUP>;
+    static constexpr int kRegs = NT * (4 * F::W + 8 * F::W + 4 + 8 + 8) + 4 * F::W + 4 + 12 * F::NG + 32;
+    static constexpr int kWaves = kRegs <= 128 ? 4 : kRegs <= 168 ? 3 : kRegs <= 256 ? 2 : 1;
+};
+
+// Few rows: the four waves share them and take every fourth record.
+template <int D, int GROUP, int NT>
+__global__ void __launch_bounds__(64 * kAttendWaves, (FewRows<D, GROUP, NT>::kWaves)) attend_kernel(const AttendArgs a) {
     using F = Format<D, GROUP>;
     constexpr int R = 16 * NT;
-    constexpr int CH = NT >= 4 ? 2 : NT == 2 ? (D == 96 ? 3 : 4) : (D / 16 < 8 ? D / 16 : 8);  // V words joined in a round
+    constexpr int CH = NT == 2 ? (D == 96 ? 3 : 4) : (D / 16 < 8 ? D / 16 : 8);  // V words joined in a round
     constexpr int ROUNDS = (2 * F::W) / CH;
     static_assert(ROUNDS * CH == 2 * F::W, "rounds cover the channels");
     __shared__ float join[kAttendWaves][CH * NT][64][4];
     __shared__ float join_m[kAttendWaves][R], join_l[kAttendWaves][R];
 
-    const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, g = lane >> 4, n = lane & 15;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int lane = threadIdx.x & 63, g = lane >> 4, n = lane & 15;
     int at = blockIdx.x;
     const int block = at % a.row_blocks;
     at /= a.row_blocks;
     const int split = at % a.n_split;
     at /= a.n_split;
     const int head = at % (int)a.c.heads, seq = at / (int)a.c.heads;
+    const int t0 = split * a.chunk;
+    const int shift = a.c.page_shift;
+    const int32_t *table = a.b.table + seq * a.b.table_stride;
+    Pages pages;
+    pages.load(a, table, t0 >> shift, lane);  // before what depends on lengths
     const Extent e(a, seq);
     const int r0 = block * R;
     if (r0 >= e.rows) return;
-    const int t0 = split * a.chunk;
     if (split > 0 && t0 >= e.len) return;
 
-    // ---- the queries
-    h8 q[NT][F::W];
-    float qsum[NT][F::NG], factor[NT];
-    int limit[NT];
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-        const int r = r0 + 16 * nt + n;
-        const bool live = r < e.rows;
-        const int i = r / a.group_heads, hq = head * a.group_heads + r % a.group_heads;
-        limit[nt] = live ? e.limit(a, i) : 0;
-        float x[F::W][8], top = 0.0f;
-        const int64_t row = (e.start + i) * a.q.token_stride + hq * a.q.head_stride + 8 * g;
-#pragma unroll
-        for (int c = 0; c < F::W; ++c) {
-            if (live) {
-                load8(a.q, row + 32 * c, x[c]);
-            } else {
-#pragma unroll
-                for (int j = 0; j < 8; ++j) x[c][j] = 0.0f;
-            }
-#pragma unroll
-            for (int j = 0; j < 8; ++j) top = fmaxf(top, fabsf(x[c][j]));
-        }
-        int power = 0;
-        if (a.q.type == kBf16) {
-            top = over_groups_max(top);
-            int ex;
-            (void)frexpf(top, &ex);  // top = m * 2^ex, m in [0.5, 1)
-            if (top > 0.0f && top < __builtin_inff()) power = 15 - ex;
-        }
-        factor[nt] = ldexpf(a.scale_log2, -power);
-#pragma unroll
-        for (int grp = 0; grp < F::NG; ++grp) qsum[nt][grp] = 0.0f;
-#pragma unroll
-        for (int c = 0; c < F::W; ++c)
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const _Float16 v = (_Float16)ldexpf(x[c][j], power);
-                q[nt][c][j] = v;
-                qsum[nt][c / F::KG] += (float)v;
-            }
-#pragma unroll
-        for (int grp = 0; grp < F::NG; ++grp) qsum[nt][grp] = over_groups_sum(qsum[nt][grp]);
-        if (a.frag_q && split == 0 && wave == 0) {
-            const int64_t tile = ((int64_t)seq * a.c.heads + head) * a.row_tiles + r0 / 16 + nt;
-            if (r0 / 16 + nt < a.row_tiles) {
-                h8 *to = (h8 *)a.frag_q + tile * (F::W * 64);
-#pragma unroll
-                for (int c = 0; c < F::W; ++c) to[c * 64 + lane] = q[nt][c];
-                if (g == 0) {
-                    float *info = a.row_info + (tile * 16 + n) * (2 + F::NG);
-                    info[0] = factor[nt];
-                    info[1] = __builtin_inff();  // a row without positions weighs nothing
-#pragma unroll
-                    for (int grp = 0; grp < F::NG; ++grp) info[2 + grp] = qsum[nt][grp];
-                }
-            }
-        }
-    }
-
-    // ---- the positions
     const int rows_here = e.rows - r0 < R ? e.rows - r0 : R;
     const int all_see = e.limit(a, r0 / a.group_heads);                  // below this no row is masked
     int end = e.limit(a, (r0 + rows_here - 1) / a.group_heads);          // at this and above every row is
     end = end < t0 + a.chunk ? end : t0 + a.chunk;
 
-    f4 o[NT][2 * F::W];
-    float m[NT], l[NT], zsum[NT][F::NG];
+    Row<D, GROUP> raw[NT];
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-        m[nt] = kFar;
-        l[nt] = 0.0f;
-#pragma unroll
-        for (int c = 0; c < 2 * F::W; ++c) o[nt][c] = (f4){0, 0, 0, 0};
-#pragma unroll
-        for (int grp = 0; grp < F::NG; ++grp) zsum[nt][grp] = 0.0f;
-    }
-
-    const int32_t *table = a.b.table + seq * a.b.table_stride;
-    const int shift = a.c.page_shift;
-    const int page_first = t0 >> shift;
-    Pages pages;
-    pages.load(a, table, page_first, lane);
+    for (int nt = 0; nt < NT; ++nt) raw[nt].load(a, e, head, r0 + 16 * nt + n, g, r0 + 16 * nt + n < e.rows);
     KTile<D, GROUP> k;
     VTile<D, GROUP> v;
     int p0 = t0 + kTile * wave;
@@ -267,6 +371,22 @@ __global__ void __launch_bounds__(64 * kAttendWaves) attend_kernel(const AttendA
         load_k<D, GROUP>(rec, lane, k);
         load_v<D, GROUP>(rec, lane, v);
     }
+
+    h8 q[NT][F::W];
+    float qsum[NT][F::NG], factor[NT];
+    int limit[NT];
+    Softmax<D, GROUP> s[NT];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+        const int r = r0 + 16 * nt + n;
+        limit[nt] = r < e.rows ? e.limit(a, r / a.group_heads) : 0;
+        raw[nt].operand(a, q[nt], qsum[nt], factor[nt]);
+        s[nt].clear();
+        if (a.frag_q && split == 0 && wave == 0 && r0 / 16 + nt < a.row_tiles)
+            keep_rows<D, GROUP>(a, ((int64_t)seq * a.c.heads + head) * a.row_tiles + r0 / 16 + nt, lane, q[nt],
+                                qsum[nt], factor[nt]);
+    }
+
     while (p0 < end) {
         const int next = p0 + kTile * kAttendWaves;
         const int page_now = page;
@@ -281,18 +401,15 @@ __global__ void __launch_bounds__(64 * kAttendWaves) attend_kernel(const AttendA
 
         if (p0 + kTile > all_see || page_now < 0) {  // some position is not seen by some row
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const int pos = p0 + 16 * (j >> 2) + 4 * g + (j & 3);
-                    if (pos >= limit[nt] || page_now < 0) x[nt][j] = -__builtin_inff();
-                }
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {  // what lies past the sequence's end may be anything
+            for (int j = 0; j < 8; ++j) {
                 const int pos = p0 + 16 * (j >> 2) + 4 * g + (j & 3);
-                if (pos >= e.len || page_now < 0) {
 #pragma unroll
-                    for (int grp = 0; grp < F::NG; ++grp) v.scale[grp][j] = (_Float16)0.0f, v.zero[grp][j] = (_Float16)0.0f;
+                for (int nt = 0; nt < NT; ++nt)
+                    if (pos >= limit[nt] || page_now < 0) x[nt][j] = -__builtin_inff();
+                if (pos >= e.len || page_now < 0) {  // what lies past the sequence's end may be anything
+#pragma unroll
+                    for (int grp = 0; grp < F::NG; ++grp) v.scale[grp][j] = (_Float16)0.0f;
+                    v.row[j] = (_Float16)0.0f;
                 }
             }
         }
@@ -300,45 +417,25 @@ __global__ void __launch_bounds__(64 * kAttendWaves) attend_kernel(const AttendA
         float top[NT];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-#pragma unroll
-            for (int j = 0; j < 8; ++j) x[nt][j] *= factor[nt];
-            top[nt] = fmaxf(fmaxf(fmaxf(x[nt][0], x[nt][1]), fmaxf(x[nt][2], x[nt][3])),
-                            fmaxf(fmaxf(x[nt][4], x[nt][5]), fmaxf(x[nt][6], x[nt][7])));
-            grown |= top[nt] > m[nt] + kSlack;
+            top[nt] = Softmax<D, GROUP>::top(x[nt]) * factor[nt];
+            grown |= top[nt] > s[nt].m + kSlack;
         }
         if (__any(grown)) {
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-                const float t = over_groups_max(top[nt]);
-                const float m1 = t > m[nt] + kSlack ? t : m[nt];
-                const float f = exp2f(m[nt] - m1);
-                m[nt] = m1;
-                l[nt] *= f;
-#pragma unroll
-                for (int grp = 0; grp < F::NG; ++grp) zsum[nt][grp] *= f;
-#pragma unroll
-                for (int c = 0; c < 2 * F::W; ++c) o[nt][c] *= f;
-            }
+            for (int nt = 0; nt < NT; ++nt) s[nt].grow(top[nt]);
         }
         h8 p[NT];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-            const float lift = kLift - m[nt];
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const float w = __builtin_amdgcn_exp2f(x[nt][j] + lift);
-                l[nt] += w;
-                p[nt][j] = (_Float16)w;
-#pragma unroll
-                for (int grp = 0; grp < F::NG; ++grp) zsum[nt][grp] = fmaf(w, (float)v.zero[grp][j], zsum[nt][grp]);
-            }
+            p[nt] = s[nt].weights(x[nt], factor[nt]);
+            s[nt].z = __builtin_amdgcn_mfma_f32_16x16x32_f16(v.row, p[nt], s[nt].z, 0, 0, 0);
         }
 #pragma unroll
         for (int c = 0; c < 2 * F::W; ++c) {
-            const h8 value = codes_to_half(v.w[c]) * v.scale[c / F::VG];
+            const h8 value = codes_minus_8(v.w[c]) * v.scale[c / F::VG];
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
-                o[nt][c] = __builtin_amdgcn_mfma_f32_16x16x32_f16(value, p[nt], o[nt][c], 0, 0, 0);
+                s[nt].o[c] = __builtin_amdgcn_mfma_f32_16x16x32_f16(value, p[nt], s[nt].o[c], 0, 0, 0);
         }
         if (rec) load_v<D, GROUP>(rec, lane, v);
         p0 = next;
@@ -347,14 +444,8 @@ __global__ void __launch_bounds__(64 * kAttendWaves) attend_kernel(const AttendA
     // ---- join the waves
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-        l[nt] = over_groups_sum(l[nt]);
-#pragma unroll
-        for (int grp = 0; grp < F::NG; ++grp) {
-            const float z = over_groups_sum(zsum[nt][grp]);
-#pragma unroll
-            for (int c = 0; c < F::VG; ++c) o[nt][grp * F::VG + c] += z;
-        }
-        if (g == 0) join_m[wave][16 * nt + n] = m[nt], join_l[wave][16 * nt + n] = l[nt];
+        s[nt].finish(lane);
+        if (g == 0) join_m[wave][16 * nt + n] = s[nt].m, join_l[wave][16 * nt + n] = s[nt].l;
     }
     __syncthreads();
 #pragma unroll
@@ -362,9 +453,9 @@ __global__ void __launch_bounds__(64 * kAttendWaves) attend_kernel(const AttendA
         float best = join_m[0][16 * nt + n];
 #pragma unroll
         for (int w = 1; w < kAttendWaves; ++w) best = fmaxf(best, join_m[w][16 * nt + n]);
-        const float f = exp2f(m[nt] - best);
+        const float f = exp2f(s[nt].m - best);
 #pragma unroll
-        for (int c = 0; c < 2 * F::W; ++c) o[nt][c] *= f;
+        for (int c = 0; c < 2 * F::W; ++c) s[nt].o[c] *= f;
     }
     const int64_t unit = ((int64_t)seq * a.c.heads + head) * a.n_split + split;
 #pragma unroll
@@ -374,7 +465,7 @@ __global__ void __launch_bounds__(64 * kAttendWaves) attend_kernel(const AttendA
         for (int c = 0; c < CH; ++c)
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
-                *reinterpret_cast<f4 *>(join[wave][c * NT + nt][lane]) = o[nt][round * CH + c];
+                *reinterpret_cast<f4 *>(join[wave][c * NT + nt][lane]) = s[nt].o[round * CH + c];
         __syncthreads();
         for (int item = threadIdx.x; item < CH * NT * 64; item += 64 * kAttendWaves) {
             const int cn = item >> 6, ln = item & 63;
@@ -397,20 +488,7 @@ __global__ void __launch_bounds__(64 * kAttendWaves) attend_kernel(const AttendA
                 *reinterpret_cast<f4 *>(a.part_o + to * D + channel) = y;
                 if (channel == 0) a.part_ml[2 * to] = best, a.part_ml[2 * to + 1] = sum;
             } else {
-                const float inv = sum > 0.0f || sum != sum ? 1.0f / sum : 0.0f;
-                const int i = row / a.group_heads, hq = head * a.group_heads + row % a.group_heads;
-                uint16_t *to = (uint16_t *)a.out.data + (e.start + i) * a.out.token_stride + hq * a.out.head_stride + channel;
-#pragma unroll
-                for (int j = 0; j < 4; ++j) to[j] = float_to_elem(y[j] * inv, a.out.type);
-                if (channel == 0) {
-                    const float log_sum = best - kLift + log2f(sum);  // log2(0) = -inf: nothing seen
-                    a.lse[(e.start + i) * (a.c.heads * a.group_heads) + hq] = log_sum * 0.69314718056f;
-                    if (a.frag_q) {
-                        const int64_t tile = ((int64_t)seq * a.c.heads + head) * a.row_tiles + row / 16;
-                        if (sum > 0.0f || sum != sum)
-                            a.row_info[(tile * 16 + row % 16) * (2 + F::NG) + 1] = log_sum;
-                    }
-                }
+                write_row(a, e, seq, head, row, channel, y, best, sum);
             }
         }
     }
@@ -423,7 +501,8 @@ __global__ void __launch_bounds__(64 * kAttendWaves) attend_kernel(const AttendA
 template <int D, int GROUP>
 __global__ void __launch_bounds__(64 * kAttendWaves) scores_kernel(const AttendArgs a) {
     using F = Format<D, GROUP>;
-    const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, g = lane >> 4, n = lane & 15;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int lane = threadIdx.x & 63, g = lane >> 4, n = lane & 15;
     const int splits = (a.max_len + a.score_chunk - 1) / a.score_chunk;
     int at = blockIdx.x;
     const int split = at % splits;
@@ -476,9 +555,7 @@ __global__ void __launch_bounds__(64 * kAttendWaves) scores_kernel(const AttendA
             }
         }
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-#pragma unroll
-            for (int mask = 1; mask < 16; mask <<= 1) sum[j] += __shfl_xor(sum[j], mask);
+        for (int j = 0; j < 8; ++j) sum[j] = over_rows_sum(sum[j]);
         if (n == 0) {
             const int64_t row = ((int64_t)seq * a.c.heads + head) * a.score_stride;
 #pragma unroll
@@ -499,8 +576,6 @@ static int launch_group(const AttendArgs &a, int row_tile, void *stream) {
         attend_kernel<D, GROUP, 1><<<grid, block, 0, s>>>(a);
     else if (row_tile == 32)
         attend_kernel<D, GROUP, 2><<<grid, block, 0, s>>>(a);
-    else if constexpr (D <= 128)
-        attend_kernel<D, GROUP, 4><<<grid, block, 0, s>>>(a);
     else
         return (int)hipErrorInvalidValue;
     int rc = (int)hipGetLastError();

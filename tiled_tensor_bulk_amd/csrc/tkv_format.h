@@ -61,21 +61,34 @@ __device__ __forceinline__ void store_words(char *p, const uint32_t *in) {
     }
 }
 
-// 8 codes as fp16, exactly.  0x6400 is 1024 in fp16, whose last place is 1:
-// or-ing a code below it gives 1024 + code (or 1024 + 16 * code for the
-// upper nibble of a byte), and the 1024 is taken off again: 1 shift, 4
+// 8 codes minus 8 as fp16, exactly.  0x6400 is 1024 in fp16, whose last place
+// is 1: or-ing a code below it gives 1024 + code (or 1024 + 16 * code for the
+// upper nibble of a byte), and the rest is taken off again: 1 shift, 4
 // and-ors and 4 packed operations for 8 elements.
-__device__ __forceinline__ h8 codes_to_half(uint32_t w) {
+__device__ __forceinline__ h8 codes_minus_8(uint32_t w) {
     const uint32_t x = w >> 8;
-    const h2 low = {(_Float16)1024.0f, (_Float16)1024.0f};
+    const h2 low = {(_Float16)1032.0f, (_Float16)1032.0f};
     const h2 s16 = {(_Float16)0.0625f, (_Float16)0.0625f};
-    const h2 b64 = {(_Float16)64.0f, (_Float16)64.0f};
+    const h2 b72 = {(_Float16)72.0f, (_Float16)72.0f};
     const h2 a0 = __builtin_bit_cast(h2, (w & 0x000F000Fu) | 0x64006400u) - low;
-    const h2 a1 = __builtin_bit_cast(h2, (w & 0x00F000F0u) | 0x64006400u) * s16 - b64;
+    const h2 a1 = __builtin_bit_cast(h2, (w & 0x00F000F0u) | 0x64006400u) * s16 - b72;
     const h2 a2 = __builtin_bit_cast(h2, (x & 0x000F000Fu) | 0x64006400u) - low;
-    const h2 a3 = __builtin_bit_cast(h2, (x & 0x00F000F0u) | 0x64006400u) * s16 - b64;
+    const h2 a3 = __builtin_bit_cast(h2, (x & 0x00F000F0u) | 0x64006400u) * s16 - b72;
     return (h8){a0[0], a0[1], a1[0], a1[1], a2[0], a2[1], a3[0], a3[1]};
 }
+
+// 8 codes as they lie: the bits of a code are those of the subnormal fp16
+// number code * 2^-24, or 16 times that in the upper nibble of a byte (codes 2,
+// 3, 6 and 7), so a mask is all it takes; the matrix unit takes subnormal
+// numbers as they are.  1 shift and 4 ands for 8 elements.
+__device__ __forceinline__ h8 codes_as_bits(uint32_t w) {
+    typedef uint32_t u4 __attribute__((ext_vector_type(4)));
+    const uint32_t x = w >> 8;
+    return __builtin_bit_cast(h8, (u4){w & 0x000F000Fu, w & 0x00F000F0u, x & 0x000F000Fu, x & 0x00F000F0u});
+}
+// ... and so a query's element j is held divided by this
+__device__ __forceinline__ constexpr int code_shift(int j) { return j & 2 ? 4 : 0; }
+constexpr int kCodeBits = 24;
 
 // The nibble of code j in its word.
 __device__ __forceinline__ constexpr int nibble_of(int j) { return (j >> 1) + 4 * (j & 1); }
@@ -125,21 +138,38 @@ __device__ __forceinline__ uint16_t float_to_elem(float f, int type) {
     return type == kBf16 ? float_to_bf16(f) : __builtin_bit_cast(uint16_t, (_Float16)f);
 }
 
-// 8 consecutive elements of a row as floats.
-__device__ __forceinline__ void load8(const Tokens &t, int64_t offset, float *out) {
-    uint16_t e[8];
+// 8 consecutive elements of a row as they lie, and as floats.
+__device__ __forceinline__ uint4 load8_raw(const Tokens &t, int64_t offset) {
     const uint16_t *p = (const uint16_t *)t.data + offset;
-    if (t.wide) {
-        const uint4 v = *reinterpret_cast<const uint4 *>(p);
-        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    if (t.wide) return *reinterpret_cast<const uint4 *>(p);
+    uint32_t w[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) e[2 * i] = (uint16_t)w[i], e[2 * i + 1] = (uint16_t)(w[i] >> 16);
+    for (int i = 0; i < 4; ++i) w[i] = p[2 * i] | ((uint32_t)p[2 * i + 1] << 16);
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+__device__ __forceinline__ void raw_to_float(const uint4 &v, int type, float *out) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) out[i] = elem_to_float((uint16_t)(w[i / 2] >> (16 * (i & 1))), type);
+}
+
+__device__ __forceinline__ void load8(const Tokens &t, int64_t offset, float *out) {
+    raw_to_float(load8_raw(t, offset), t.type, out);
+}
+
+// 4 consecutive elements of a row, rounded to its type, which is 16 bits wide.
+__device__ __forceinline__ void store4(const Tokens &t, int64_t offset, f4 in) {
+    uint16_t *p = (uint16_t *)t.data + offset;
+    uint16_t e[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) e[i] = float_to_elem(in[i], t.type);
+    if (t.wide) {
+        *reinterpret_cast<uint2 *>(p) = make_uint2(e[0] | ((uint32_t)e[1] << 16), e[2] | ((uint32_t)e[3] << 16));
     } else {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) e[i] = p[i];
+        for (int i = 0; i < 4; ++i) p[i] = e[i];
     }
-#pragma unroll
-    for (int i = 0; i < 8; ++i) out[i] = elem_to_float(e[i], t.type);
 }
 
 // 8 consecutive elements of a row, rounded to its type.

@@ -65,7 +65,7 @@ struct AttendArgs {
     int32_t rows;          // max_new * group_heads
     int32_t row_blocks;
     int32_t max_len;
-    int32_t chunk;         // positions of a workgroup, a multiple of 128
+    int32_t chunk;         // positions of a workgroup, a power of two
     int32_t n_split;
     float *part_o;         // [n_seq][heads][n_split][rows][dim]
     float *part_ml;        // [n_seq][heads][n_split][rows][2]
@@ -96,7 +96,7 @@ struct EvictArgs {
 // Launchers, one translation unit each; they return a hipError_t as int.
 int launch_append(const MoveArgs &a, void *stream);
 int launch_read(const MoveArgs &a, void *stream);
-// row_tile: rows of a wave, 16, 32 or 64
+// row_tile: rows of a wave, 16 or 32
 int launch_attend_d64(const AttendArgs &a, int row_tile, void *stream);
 int launch_attend_d96(const AttendArgs &a, int row_tile, void *stream);
 int launch_attend_d128(const AttendArgs &a, int row_tile, void *stream);
