@@ -44,6 +44,8 @@
 namespace tkv {
 
 constexpr int kAttendWaves = 4;
+template <int D>
+constexpr int kScoreRecords = D <= 128 ? 2 : 1;  // records of a wave of the scores kernel
 constexpr float kFar = -1e30f;  // reference of a row that has seen nothing
 constexpr float kLift = 7.0f;   // weights are held times 2^7
 constexpr float kSlack = 8.0f;
@@ -189,7 +191,7 @@ __device__ __forceinline__ void write_row(const AttendArgs &a, const Extent &e, 
         a.lse[(e.start + i) * (a.c.heads * a.group_heads) + hq] = log_sum * 0.69314718056f;
         if (a.frag_q && (sum > 0.0f || sum != sum)) {
             const int64_t tile = ((int64_t)seq * a.c.heads + head) * a.row_tiles + row / 16;
-            a.row_info[(tile * 16 + row % 16) * (2 + a.c.dim / a.c.group) + 1] = log_sum;
+            a.row_info[(tile * 16 + row % 16) * 2 + 1] = log_sum;
         }
     }
 }
@@ -242,21 +244,41 @@ struct Row {
     }
 };
 
+// The sums of a row's q over the groups of channels as an operand: three fp16
+// numbers that add up to a sum, in units of 2^kSumBits, in the lanes of g = 0, 1
+// and 2, group j in place j.  Its left operand is the zeros of a position.
+constexpr int kSumBits = 8;
+
+template <int D, int GROUP>
+__device__ __forceinline__ h8 sum_parts(const float (&qsum)[D / GROUP], int g) {
+    h8 r = {0, 0, 0, 0, 0, 0, 0, 0};
+#pragma unroll
+    for (int grp = 0; grp < D / GROUP; ++grp) {
+        float y = qsum[grp] * (float)(1 << (kCodeBits - kSumBits));
+        const _Float16 a = (_Float16)y;
+        y -= (float)a;
+        const _Float16 b = (_Float16)y;
+        const _Float16 c = (_Float16)(y - (float)b);
+        r[grp] = g == 0 ? a : g == 1 ? b : g == 2 ? c : (_Float16)0.0f;
+    }
+    return r;
+}
+// what turns products in those units into logarithms
+__device__ __forceinline__ float sums_factor(float factor) {
+    return fmaxf(factor * (1.0f / (1 << (kCodeBits - kSumBits))), 0x1p-126f);
+}
+
 // Where the scores kernel finds a tile of 16 rows and what belongs to it.
 template <int D, int GROUP>
-__device__ __forceinline__ void keep_rows(const AttendArgs &a, int64_t tile, int lane, const h8 (&q)[D / 32],
-                                          const float (&qsum)[D / GROUP], float factor) {
+__device__ __forceinline__ void keep_rows(const AttendArgs &a, int64_t tile, int lane, const h8 (&q)[D / 32], h8 sums,
+                                          float factor) {
     using F = Format<D, GROUP>;
-    h8 *to = (h8 *)a.frag_q + tile * (F::W * 64);
+    h8 *to = (h8 *)a.frag_q + tile * ((F::W + 1) * 64);
 #pragma unroll
     for (int c = 0; c < F::W; ++c) to[c * 64 + lane] = q[c];
-    if (lane < 16) {
-        float *info = a.row_info + (tile * 16 + lane) * (2 + F::NG);
-        info[0] = factor;
-        info[1] = __builtin_inff();  // a row without positions weighs nothing
-#pragma unroll
-        for (int grp = 0; grp < F::NG; ++grp) info[2 + grp] = qsum[grp];
-    }
+    to[F::W * 64 + lane] = sums;
+    // a row without positions weighs nothing: its logarithm stays at inf
+    if (lane < 16) *reinterpret_cast<float2 *>(a.row_info + (tile * 16 + lane) * 2) = make_float2(factor, __builtin_inff());
 }
 
 // What a row's running softmax holds, and one step of it: x (32 positions'
@@ -384,7 +406,7 @@ __global__ void __launch_bounds__(64 * kAttendWaves, (FewRows<D, GROUP, NT>::kWa
         s[nt].clear();
         if (a.frag_q && split == 0 && wave == 0 && r0 / 16 + nt < a.row_tiles)
             keep_rows<D, GROUP>(a, ((int64_t)seq * a.c.heads + head) * a.row_tiles + r0 / 16 + nt, lane, q[nt],
-                                qsum[nt], factor[nt]);
+                                sum_parts<D, GROUP>(qsum[nt], g), sums_factor(factor[nt]));
     }
 
     while (p0 < end) {
@@ -492,100 +514,6 @@ __global__ void __launch_bounds__(64 * kAttendWaves, (FewRows<D, GROUP, NT>::kWa
             }
         }
     }
-}
-
-// scores_out = scores_in + the weights of each position, summed over rows:
-// exp2(y - lse2), with y computed again from the K codes (half of a record)
-// rather than kept in memory by the first kernel, which would be 4 bytes for
-// each position and row.  One wave owns a record, so sums have one order.
-template <int D, int GROUP>
-__global__ void __launch_bounds__(64 * kAttendWaves) scores_kernel(const AttendArgs a) {
-    using F = Format<D, GROUP>;
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int lane = threadIdx.x & 63, g = lane >> 4, n = lane & 15;
-    const int splits = (a.max_len + a.score_chunk - 1) / a.score_chunk;
-    int at = blockIdx.x;
-    const int split = at % splits;
-    at /= splits;
-    const int head = at % (int)a.c.heads, seq = at / (int)a.c.heads;
-    const Extent e(a, seq);
-    const int t0 = split * a.score_chunk;
-    if (t0 >= e.len) return;
-    const int end = e.len < t0 + a.score_chunk ? e.len : t0 + a.score_chunk;
-    const int32_t *table = a.b.table + seq * a.b.table_stride;
-    const int64_t first_tile = ((int64_t)seq * a.c.heads + head) * a.row_tiles;
-    const h8 *frags = (const h8 *)a.frag_q + first_tile * (F::W * 64);
-    const float *infos = a.row_info + first_tile * 16 * (2 + F::NG);
-    const int tiles = (e.rows + 15) / 16;
-    h8 q[1][F::W];
-    float qsum[1][F::NG], factor = 0.0f, lse2 = 0.0f;
-    int limit = 0;
-    auto load_rows = [&](int t) {
-#pragma unroll
-        for (int c = 0; c < F::W; ++c) q[0][c] = frags[(t * F::W + c) * 64 + lane];
-        const float *info = infos + (t * 16 + n) * (2 + F::NG);
-        factor = info[0];
-        lse2 = info[1];
-#pragma unroll
-        for (int grp = 0; grp < F::NG; ++grp) qsum[0][grp] = info[2 + grp];
-        const int r = t * 16 + n;
-        limit = r < e.rows ? e.limit(a, r / a.group_heads) : 0;
-    };
-    if (tiles == 1) load_rows(0);
-    for (int p0 = t0 + kTile * wave; p0 < end; p0 += kTile * kAttendWaves) {
-        const int page = page_at(table, a.b.table_width, a.c.n_pages, p0 >> a.c.page_shift);
-        KTile<D, GROUP> k;
-        load_k<D, GROUP>(record_at(a.c, page < 0 ? 0 : page, head, p0 / kTile), lane, k);
-        float sum[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-        // the first row that sees the record
-        int t = 0;
-        if (a.causal) {
-            const int i = p0 - (e.len - e.n);
-            if (i > 0) t = i * a.group_heads / 16;
-        }
-        for (; t < tiles; ++t) {
-            if (tiles > 1) load_rows(t);
-            float x[1][8];
-            products<D, GROUP, 1>(k, q, qsum, x);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const int pos = p0 + 16 * (j >> 2) + 4 * g + (j & 3);
-                const float w = __builtin_amdgcn_exp2f(fmaf(x[0][j], factor, -lse2));
-                sum[j] += pos < limit && page >= 0 ? w : 0.0f;
-            }
-        }
-#pragma unroll
-        for (int j = 0; j < 8; ++j) sum[j] = over_rows_sum(sum[j]);
-        if (n == 0) {
-            const int64_t row = ((int64_t)seq * a.c.heads + head) * a.score_stride;
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const int pos = p0 + 16 * (j >> 2) + 4 * g + (j & 3);
-                if (pos < e.len) a.scores_out[row + pos] = (a.scores_in ? a.scores_in[row + pos] : 0.0f) + sum[j];
-            }
-        }
-    }
-}
-
-template <int D, int GROUP>
-static int launch_group(const AttendArgs &a, int row_tile, void *stream) {
-    const dim3 block(64 * kAttendWaves);
-    const dim3 grid((uint32_t)((int64_t)a.b.n_seq * a.c.heads * a.n_split * a.row_blocks));
-    hipStream_t s = (hipStream_t)stream;
-    if (row_tile == 16)
-        attend_kernel<D, GROUP, 1><<<grid, block, 0, s>>>(a);
-    else if (row_tile == 32)
-        attend_kernel<D, GROUP, 2><<<grid, block, 0, s>>>(a);
-    else
-        return (int)hipErrorInvalidValue;
-    int rc = (int)hipGetLastError();
-    if (rc == 0 && a.n_split > 1) rc = launch_combine(a, stream);
-    if (rc == 0 && a.scores_out && a.max_len > 0) {
-        const int64_t splits = (a.max_len + a.score_chunk - 1) / a.score_chunk;
-        scores_kernel<D, GROUP><<<dim3((uint32_t)(splits * a.c.heads * a.b.n_seq)), block, 0, s>>>(a);
-        rc = (int)hipGetLastError();
-    }
-    return rc;
 }
 
 }  // namespace tkv

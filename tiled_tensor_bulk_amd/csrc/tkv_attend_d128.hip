@@ -1,5 +1,5 @@
 // tkv_attend_d128.hip -- attention over the 4-bit cache, head_dim 128.
-#include "tkv_attend.h"
+#include "tkv_launch.h"
 
 namespace tkv {
 int launch_attend_d128(const AttendArgs &a, int row_tile, void *stream) {

@@ -1,5 +1,5 @@
 // tkv_attend_d256.hip -- attention over the 4-bit cache, head_dim 256.
-#include "tkv_attend.h"
+#include "tkv_launch.h"
 
 namespace tkv {
 int launch_attend_d256(const AttendArgs &a, int row_tile, void *stream) {

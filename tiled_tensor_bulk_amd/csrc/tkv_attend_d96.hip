@@ -1,5 +1,5 @@
 // tkv_attend_d96.hip -- attention over the 4-bit cache, head_dim 96.
-#include "tkv_attend.h"
+#include "tkv_launch.h"
 
 namespace tkv {
 int launch_attend_d96(const AttendArgs &a, int row_tile, void *stream) {

@@ -166,15 +166,17 @@ uint64_t up(uint64_t v, uint64_t to) { return (v + to - 1) / to * to; }
 constexpr int kLeastChunk = 512;
 constexpr int kMostChunk = 1 << 16;
 constexpr int kBlocksPerCu = 8;
+constexpr int kRowBlocksPerCu = 2;
 
 Split plan(const Cache &c, int64_t n_seq, int64_t rows, int64_t max_len, bool scores, int cus) {
     Split s{};
-    s.row_tile = rows <= 16 ? 16 : 32;
+    s.row_tile = rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 || c.dim > 128 ? 64 : 128;
     s.row_blocks = (int)((rows + s.row_tile - 1) / s.row_tile);
     s.row_tiles = (int)((rows + 15) / 16);
     const int64_t units = n_seq * c.heads * s.row_blocks;
     s.chunk = kLeastChunk;
-    while (s.chunk < kMostChunk && units * ((max_len + s.chunk - 1) / s.chunk) > (int64_t)cus * kBlocksPerCu) s.chunk *= 2;
+    const int64_t most = (int64_t)cus * (s.row_tile <= 32 ? kBlocksPerCu : kRowBlocksPerCu);
+    while (s.chunk < kMostChunk && units * ((max_len + s.chunk - 1) / s.chunk) > most) s.chunk *= 2;
     s.n_split = (int)((max_len + s.chunk - 1) / s.chunk);
     if (s.n_split < 1) s.n_split = 1;
     const uint64_t heads = (uint64_t)n_seq * c.heads;
@@ -186,9 +188,9 @@ Split plan(const Cache &c, int64_t n_seq, int64_t rows, int64_t max_len, bool sc
     }
     if (scores) {
         s.frag_q = s.total;
-        s.total = up(s.total + heads * s.row_tiles * 32 * c.dim, 256);
+        s.total = up(s.total + heads * s.row_tiles * (32 * c.dim + 1024), 256);
         s.row_info = s.total;
-        s.total = up(s.total + heads * s.row_tiles * 16 * (2 + c.dim / c.group) * 4, 256);
+        s.total = up(s.total + heads * s.row_tiles * 16 * 8, 256);
     }
     return s;
 }
@@ -325,7 +327,6 @@ tmap_status tkv_attend(const tkv_cache *cache, const tkv_attend_args *args, cons
     if (a.scores_out) {
         a.frag_q = ws + s.frag_q;
         a.row_info = (float *)(ws + s.row_info);
-        a.score_chunk = s.chunk < 1024 ? s.chunk : 1024;
     }
     switch (a.c.dim) {
         case 64: return launched(tkv::launch_attend_d64(a, s.row_tile, hip_stream));

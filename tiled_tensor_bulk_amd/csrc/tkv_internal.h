@@ -71,10 +71,9 @@ struct AttendArgs {
     float *part_ml;        // [n_seq][heads][n_split][rows][2]
     // with scores: the queries as the matrix unit takes them, and what turns
     // their products into weights
-    void *frag_q;          // fp16 [n_seq][heads][row tiles][dim/32][64 lanes][8]
-    float *row_info;       // [n_seq][heads][row tiles][16][2 + groups]: factor, lse2, channel sums
+    void *frag_q;          // fp16 [n_seq][heads][row tiles][dim/32 + 1][64 lanes][8]: q, and its sums over groups
+    float *row_info;       // [n_seq][heads][row tiles][16][2]: factor, lse2
     int32_t row_tiles;
-    int32_t score_chunk;   // positions of a workgroup of the scores kernel
     const float *scores_in;
     float *scores_out;
     int64_t score_stride;
@@ -96,7 +95,8 @@ struct EvictArgs {
 // Launchers, one translation unit each; they return a hipError_t as int.
 int launch_append(const MoveArgs &a, void *stream);
 int launch_read(const MoveArgs &a, void *stream);
-// row_tile: rows of a wave, 16 or 32
+// row_tile: rows of a workgroup, 16 or 32 (its waves share the positions), 64
+// or 128 (its waves share the rows)
 int launch_attend_d64(const AttendArgs &a, int row_tile, void *stream);
 int launch_attend_d96(const AttendArgs &a, int row_tile, void *stream);
 int launch_attend_d128(const AttendArgs &a, int row_tile, void *stream);

@@ -1,0 +1,37 @@
+// tkv_launch.h -- the launches of one attention call, for one head_dim.
+#pragma once
+
+#include "tkv_rows.h"
+#include "tkv_scores.h"
+
+namespace tkv {
+
+template <int D, int GROUP>
+static int launch_group(const AttendArgs &a, int row_tile, void *stream) {
+    const dim3 block(64 * kAttendWaves);
+    const dim3 grid((uint32_t)((int64_t)a.b.n_seq * a.c.heads * a.n_split * a.row_blocks));
+    hipStream_t s = (hipStream_t)stream;
+    if (row_tile == 16) {
+        attend_kernel<D, GROUP, 1><<<grid, block, 0, s>>>(a);
+    } else if (row_tile == 32) {
+        attend_kernel<D, GROUP, 2><<<grid, block, 0, s>>>(a);
+    } else if (row_tile == 64) {
+        rows_kernel<D, GROUP, 1><<<grid, block, 0, s>>>(a);
+    } else {
+        if constexpr (D > 128)
+            return (int)hipErrorInvalidValue;
+        else
+            rows_kernel<D, GROUP, 2><<<grid, block, 0, s>>>(a);
+    }
+    int rc = (int)hipGetLastError();
+    if (rc == 0 && a.n_split > 1) rc = launch_combine(a, stream);
+    if (rc == 0 && a.scores_out && a.max_len > 0) {
+        constexpr int kPositions = kTile * kAttendWaves * kScoreRecords<D>;
+        const int64_t splits = (a.max_len + kPositions - 1) / kPositions;
+        scores_kernel<D, GROUP><<<dim3((uint32_t)(splits * a.c.heads * a.b.n_seq)), block, 0, s>>>(a);
+        rc = (int)hipGetLastError();
+    }
+    return rc;
+}
+
+}  // namespace tkv

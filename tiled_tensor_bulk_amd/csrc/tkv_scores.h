@@ -1,0 +1,143 @@
+// tkv_scores.h -- attention weights summed over rows:
+//   scores_out = scores_in + sum over rows of exp2(y - lse2)
+// with the logarithms y computed again from the K codes (half of a record)
+// rather than kept in memory by the first kernel, which would be 4 bytes for
+// each position and row.
+//
+// A wave owns RECS records, unpacked in registers with their scales and zeros,
+// and goes over the tiles of 16 rows that see them; a workgroup's waves go over
+// the same tiles at about the same time, so those come from the first level of
+// cache.  One wave adds up a position, in the order of the rows.
+#pragma once
+
+#include "tkv_attend.h"
+
+namespace tkv {
+
+template <int D, int GROUP>
+struct ScoreRows {  // a tile of 16 rows
+    h8 q[D / 32], sums;
+    float factor, lse2;
+    __device__ __forceinline__ void load(const AttendArgs &a, int64_t tile, int lane) {
+        const h8 *from = (const h8 *)a.frag_q + tile * ((D / 32 + 1) * 64);
+#pragma unroll
+        for (int c = 0; c < D / 32; ++c) q[c] = from[c * 64 + lane];
+        sums = from[D / 32 * 64 + lane];
+        const float2 info = *reinterpret_cast<const float2 *>(a.row_info + (tile * 16 + (lane & 15)) * 2);
+        factor = info.x;
+        lse2 = info.y;
+    }
+};
+
+template <int D, int GROUP>
+struct ScoreKeys {  // 32 positions
+    using F = Format<D, GROUP>;
+    h8 k[2][F::W], zero[2];
+    float scale[F::NG][8], sum[8];
+    __device__ __forceinline__ void load(const char *rec, int lane) {
+        const int g = lane >> 4, m = lane & 15;
+        uint32_t w[2][F::W];
+#pragma unroll
+        for (int hs = 0; hs < 2 * F::S; ++hs)
+            load_words<F::WV>(rec + (hs * 64 + lane) * F::WV * 4, &w[hs / F::S][(hs % F::S) * F::WV]);
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+            zero[half] = (h8){0, 0, 0, 0, 0, 0, 0, 0};
+#pragma unroll
+            for (int grp = 0; grp < F::NG; ++grp) {
+                const _Float16 *pairs = reinterpret_cast<const _Float16 *>(rec + F::KP) + (grp * kTile + 16 * half) * 2;
+                zero[half][grp] = pairs[2 * m + 1];
+                const h8 mine = *reinterpret_cast<const h8 *>(pairs + 8 * g);
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    scale[grp][4 * half + i] = (float)mine[2 * i] * (float)(1 << (kCodeBits - kSumBits));
+            }
+#pragma unroll
+            for (int c = 0; c < F::W; ++c) k[half][c] = codes_as_bits(w[half][c]);
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) sum[j] = 0.0f;
+    }
+    // add the rows' weights; `masked`: some row does not see some position
+    __device__ __forceinline__ void add(const ScoreRows<D, GROUP> &r, bool masked, int p0, int limit, int lane) {
+        const int g = lane >> 4;
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+            f4 y = __builtin_amdgcn_mfma_f32_16x16x32_f16(zero[half], r.sums, (f4){0, 0, 0, 0}, 0, 0, 0);
+#pragma unroll
+            for (int grp = 0; grp < F::NG; ++grp) {
+                f4 acc = {0, 0, 0, 0};
+#pragma unroll
+                for (int c = grp * F::KG; c < (grp + 1) * F::KG; ++c)
+                    acc = __builtin_amdgcn_mfma_f32_16x16x32_f16(k[half][c], r.q[c], acc, 0, 0, 0);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) y[i] = fmaf(scale[grp][4 * half + i], acc[i], y[i]);
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                float w = __builtin_amdgcn_exp2f(fmaf(y[i], r.factor, -r.lse2));
+                if (masked) w = p0 + 16 * half + 4 * g + i < limit ? w : 0.0f;
+                sum[4 * half + i] += w;
+            }
+        }
+    }
+};
+
+template <int D, int GROUP>
+__global__ void __launch_bounds__(64 * kAttendWaves) scores_kernel(const AttendArgs a) {
+    constexpr int RECS = kScoreRecords<D>;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int lane = threadIdx.x & 63, g = lane >> 4, n = lane & 15;
+    const int splits = (a.max_len + kTile * RECS * kAttendWaves - 1) / (kTile * RECS * kAttendWaves);
+    int at = blockIdx.x;
+    const int split = at % splits;
+    at /= splits;
+    const int head = at % (int)a.c.heads, seq = at / (int)a.c.heads;
+    const Extent e(a, seq);
+    const int p0 = (split * kAttendWaves + wave) * kTile * RECS;
+    if (p0 >= e.len) return;
+    const int32_t *table = a.b.table + seq * a.b.table_stride;
+    const int64_t first_tile = ((int64_t)seq * a.c.heads + head) * a.row_tiles;
+    const int tiles = (e.rows + 15) / 16;
+    ScoreKeys<D, GROUP> keys[RECS];
+    int page[RECS];
+#pragma unroll
+    for (int i = 0; i < RECS; ++i) {
+        const int pr = p0 + kTile * i;
+        page[i] = page_at(table, a.b.table_width, a.c.n_pages, pr >> a.c.page_shift);
+        // of a page that does not exist another one's are read, and dropped
+        keys[i].load(record_at(a.c, page[i] < 0 ? 0 : page[i], head, pr / kTile), lane);
+    }
+    int t = 0;  // the first tile with a row that sees the first position
+    if (a.causal) {
+        const int i = p0 - (e.len - e.n);
+        if (i > 0) t = (int)((int64_t)i * a.group_heads / 16);
+    }
+    ScoreRows<D, GROUP> rows;
+    if (t < tiles) rows.load(a, first_tile + t, lane);
+    for (; t < tiles; ++t) {
+        const ScoreRows<D, GROUP> now = rows;
+        if (t + 1 < tiles) rows.load(a, first_tile + t + 1, lane);
+        const int r = t * 16 + n;
+        const int limit = r < e.rows ? e.limit(a, r / a.group_heads) : 0;
+        const bool masked = t * 16 + 16 > e.rows || p0 + kTile * RECS > e.limit(a, t * 16 / a.group_heads);
+#pragma unroll
+        for (int i = 0; i < RECS; ++i) keys[i].add(now, masked, p0 + kTile * i, limit, lane);
+    }
+    const int64_t row = ((int64_t)seq * a.c.heads + head) * a.score_stride;
+#pragma unroll
+    for (int i = 0; i < RECS; ++i) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) keys[i].sum[j] = over_rows_sum(keys[i].sum[j]);
+        if (n < 8) {  // lane n of a group has position n of its 8
+            float mine = keys[i].sum[0];
+#pragma unroll
+            for (int j = 1; j < 8; ++j) mine = n == j ? keys[i].sum[j] : mine;
+            const int pos = p0 + kTile * i + 16 * (n >> 2) + 4 * g + (n & 3);
+            if (pos < e.len)
+                a.scores_out[row + pos] = (a.scores_in ? a.scores_in[row + pos] : 0.0f) + (page[i] < 0 ? 0.0f : mine);
+        }
+    }
+}
+
+}  // namespace tkv
