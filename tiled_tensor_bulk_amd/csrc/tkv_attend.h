@@ -121,6 +121,18 @@ struct Extent {
     __device__ __forceinline__ int limit(const AttendArgs &a, int i) const { return a.causal ? len - n + 1 + i : len; }
 };
 
+// A sequence's chunks: as few as the launch's chunk allows, of equal length up
+// to whole steps of the workgroup.
+struct Chunks {
+    int size, n;
+    __device__ __forceinline__ Chunks(const AttendArgs &a, int len) {
+        constexpr int kStep = kTile * kAttendWaves;
+        const int parts = (len + a.chunk - 1) / a.chunk;
+        size = parts > 1 ? ((len + parts - 1) / parts + kStep - 1) / kStep * kStep : a.chunk;
+        n = len > 0 ? (len + size - 1) / size : 1;
+    }
+};
+
 // Table entries of up to 64 neighbouring pages, one in each lane.
 struct Pages {
     int mine, base;
@@ -294,10 +306,17 @@ struct Softmax {
 #pragma unroll
         for (int c = 0; c < D / 16; ++c) o[c] = (f4){0, 0, 0, 0};
     }
-    static __device__ __forceinline__ float top(const float (&x)[8]) {
-        return fmaxf(fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])), fmaxf(fmaxf(x[4], x[5]), fmaxf(x[6], x[7])));
+    template <int N>
+    static __device__ __forceinline__ float top(const float (&x)[N]) {
+        float t[2] = {x[0], x[1]};  // maxima of three
+#pragma unroll
+        for (int j = 2; j < N; j += 4) {
+            t[0] = fmaxf(fmaxf(t[0], x[j]), x[j + 1]);
+            if (j + 2 < N) t[1] = fmaxf(fmaxf(t[1], x[j + 2]), x[j + 3]);
+        }
+        return fmaxf(t[0], t[1]);
     }
-    __device__ __forceinline__ void grow(float y) {  // y: the largest logarithm of the lane's 8
+    __device__ __forceinline__ void grow(float y) {  // y: the largest logarithm of the lane's positions
         const float t = over_groups_max(y);
         const float m1 = t > m + kSlack ? t : m;
         const float f = exp2f(m - m1);
@@ -307,16 +326,17 @@ struct Softmax {
 #pragma unroll
         for (int c = 0; c < D / 16; ++c) o[c] *= f;
     }
-    __device__ __forceinline__ h8 weights(const float (&x)[8], float factor) {
+    template <int RECS>
+    __device__ __forceinline__ void weights(const float (&x)[8 * RECS], float factor, h8 (&p)[RECS]) {
         const float lift = kLift - m;
-        h8 p;
+        float sum = 0.0f;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
+        for (int j = 0; j < 8 * RECS; ++j) {
             const float w = __builtin_amdgcn_exp2f(fmaf(x[j], factor, lift));
-            l += w;
-            p[j] = (_Float16)w;
+            sum += w;
+            p[j >> 3][j & 7] = (_Float16)w;
         }
-        return p;
+        l += sum;
     }
     // after the last position: l whole in every lane, o what a division by l makes the output
     __device__ __forceinline__ void finish(int lane) {
@@ -365,20 +385,20 @@ __global__ void __launch_bounds__(64 * kAttendWaves, (FewRows<D, GROUP, NT>::kWa
     const int split = at % a.n_split;
     at /= a.n_split;
     const int head = at % (int)a.c.heads, seq = at / (int)a.c.heads;
-    const int t0 = split * a.chunk;
     const int shift = a.c.page_shift;
     const int32_t *table = a.b.table + seq * a.b.table_stride;
-    Pages pages;
-    pages.load(a, table, t0 >> shift, lane);  // before what depends on lengths
     const Extent e(a, seq);
+    const Chunks chunks(a, e.len);
     const int r0 = block * R;
-    if (r0 >= e.rows) return;
-    if (split > 0 && t0 >= e.len) return;
+    if (r0 >= e.rows || split >= chunks.n) return;
+    const int t0 = split * chunks.size;
+    Pages pages;
+    pages.load(a, table, t0 >> shift, lane);
 
     const int rows_here = e.rows - r0 < R ? e.rows - r0 : R;
     const int all_see = e.limit(a, r0 / a.group_heads);                  // below this no row is masked
     int end = e.limit(a, (r0 + rows_here - 1) / a.group_heads);          // at this and above every row is
-    end = end < t0 + a.chunk ? end : t0 + a.chunk;
+    end = end < t0 + chunks.size ? end : t0 + chunks.size;
 
     Row<D, GROUP> raw[NT];
 #pragma unroll
@@ -446,18 +466,18 @@ __global__ void __launch_bounds__(64 * kAttendWaves, (FewRows<D, GROUP, NT>::kWa
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) s[nt].grow(top[nt]);
         }
-        h8 p[NT];
+        h8 p[NT][1];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-            p[nt] = s[nt].weights(x[nt], factor[nt]);
-            s[nt].z = __builtin_amdgcn_mfma_f32_16x16x32_f16(v.row, p[nt], s[nt].z, 0, 0, 0);
+            s[nt].weights(x[nt], factor[nt], p[nt]);
+            s[nt].z = __builtin_amdgcn_mfma_f32_16x16x32_f16(v.row, p[nt][0], s[nt].z, 0, 0, 0);
         }
 #pragma unroll
         for (int c = 0; c < 2 * F::W; ++c) {
             const h8 value = codes_minus_8(v.w[c]) * v.scale[c / F::VG];
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
-                s[nt].o[c] = __builtin_amdgcn_mfma_f32_16x16x32_f16(value, p[nt], s[nt].o[c], 0, 0, 0);
+                s[nt].o[c] = __builtin_amdgcn_mfma_f32_16x16x32_f16(value, p[nt][0], s[nt].o[c], 0, 0, 0);
         }
         if (rec) load_v<D, GROUP>(rec, lane, v);
         p0 = next;

@@ -24,8 +24,7 @@ __global__ void __launch_bounds__(kCombineThreads) combine_kernel(const AttendAr
     const int seq = (int)(unit / a.c.heads);
     const Extent e(a, seq);
     if (row >= e.rows) return;
-    int parts = (e.len + a.chunk - 1) / a.chunk;
-    parts = parts < 1 ? 1 : parts;
+    const int parts = Chunks(a, e.len).n;
     const int64_t first = (unit * a.n_split) * a.rows + row;
     float best = kFar, sum = 0.0f;
     f4 y = (f4){0, 0, 0, 0};

@@ -67,13 +67,17 @@ __device__ __forceinline__ void store_words(char *p, const uint32_t *in) {
 // and-ors and 4 packed operations for 8 elements.
 __device__ __forceinline__ h8 codes_minus_8(uint32_t w) {
     const uint32_t x = w >> 8;
+    // from a register, as an and-or takes one number that is not: the compiler
+    // makes an and and an or of two that it knows
+    uint32_t magic;
+    asm("v_mov_b32 %0, 0x64006400" : "=v"(magic));
     const h2 low = {(_Float16)1032.0f, (_Float16)1032.0f};
     const h2 s16 = {(_Float16)0.0625f, (_Float16)0.0625f};
     const h2 b72 = {(_Float16)72.0f, (_Float16)72.0f};
-    const h2 a0 = __builtin_bit_cast(h2, (w & 0x000F000Fu) | 0x64006400u) - low;
-    const h2 a1 = __builtin_bit_cast(h2, (w & 0x00F000F0u) | 0x64006400u) * s16 - b72;
-    const h2 a2 = __builtin_bit_cast(h2, (x & 0x000F000Fu) | 0x64006400u) - low;
-    const h2 a3 = __builtin_bit_cast(h2, (x & 0x00F000F0u) | 0x64006400u) * s16 - b72;
+    const h2 a0 = __builtin_bit_cast(h2, (w & 0x000F000Fu) | magic) - low;
+    const h2 a1 = __builtin_bit_cast(h2, (w & 0x00F000F0u) | magic) * s16 - b72;
+    const h2 a2 = __builtin_bit_cast(h2, (x & 0x000F000Fu) | magic) - low;
+    const h2 a3 = __builtin_bit_cast(h2, (x & 0x00F000F0u) | magic) * s16 - b72;
     return (h8){a0[0], a0[1], a1[0], a1[1], a2[0], a2[1], a3[0], a3[1]};
 }
 

@@ -125,20 +125,19 @@ __global__ void __launch_bounds__(64 * kAttendWaves, 2) rows_kernel(const Attend
     const int split = at % a.n_split;
     at /= a.n_split;
     const int head = at % (int)a.c.heads, seq = at / (int)a.c.heads;
-    const int t0 = split * a.chunk;
-    const int shift = a.c.page_shift;
     const int32_t *table = a.b.table + seq * a.b.table_stride;
-    Pages pages;
-    pages.load(a, table, t0 >> shift, lane);
     const Extent e(a, seq);
-    if (block * R >= e.rows) return;
-    if (split > 0 && t0 >= e.len) return;
+    const Chunks chunks(a, e.len);
+    if (block * R >= e.rows || split >= chunks.n) return;
+    const int t0 = split * chunks.size;
+    Pages pages;
+    pages.load(a, table, t0 >> a.c.page_shift, lane);
     const int r0 = block * R + wave * 16 * NT;
 
     // positions that some row of the workgroup sees, and of the wave
     const int last = block * R + R < e.rows ? block * R + R - 1 : e.rows - 1;
     int end = e.limit(a, last / a.group_heads);
-    end = end < t0 + a.chunk ? end : t0 + a.chunk;
+    end = end < t0 + chunks.size ? end : t0 + chunks.size;
     const int wave_last = r0 + 16 * NT < e.rows ? r0 + 16 * NT - 1 : e.rows - 1;
     const int wave_end = r0 < e.rows ? e.limit(a, wave_last / a.group_heads) : 0;
     const int all_see = r0 < e.rows ? e.limit(a, r0 / a.group_heads) : 0;
@@ -180,45 +179,49 @@ __global__ void __launch_bounds__(64 * kAttendWaves, 2) rows_kernel(const Attend
     int now = 0;
     for (int p0 = t0; p0 < end; p0 += STEP, now ^= 1) {
         const Stage<D, GROUP, RECS> &from = stage[now];
+        if (p0 < wave_end) {
+            float x[NT][8 * RECS];
 #pragma unroll
-        for (int i = 0; i < RECS; ++i) {
-            const int pr = p0 + kTile * i;
-            if (pr >= wave_end) break;
-            float x[NT][8];
+            for (int i = 0; i < RECS; ++i)
 #pragma unroll
-            for (int half = 0; half < 2; ++half) {
-                f4 acc[NT][F::NG], zero[NT];
-                const h8 kz = from.kz[i][16 * half + n];
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-                    zero[nt] = __builtin_amdgcn_mfma_f32_16x16x32_f16(kz, sums[nt], (f4){0, 0, 0, 0}, 0, 0, 0);
-#pragma unroll
-                for (int c = 0; c < F::W; ++c) {
-                    const h8 key = from.k[i][half][c][lane];
+                for (int half = 0; half < 2; ++half) {
+                    f4 acc[NT][F::NG], y[NT];
+                    const h8 kz = from.kz[i][16 * half + n];
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt)
-                        acc[nt][c / F::KG] = __builtin_amdgcn_mfma_f32_16x16x32_f16(
-                            key, q[nt][c], c % F::KG ? acc[nt][c / F::KG] : (f4){0, 0, 0, 0}, 0, 0, 0);
-                }
+                        y[nt] = __builtin_amdgcn_mfma_f32_16x16x32_f16(kz, sums[nt], (f4){0, 0, 0, 0}, 0, 0, 0);
 #pragma unroll
-                for (int grp = 0; grp < F::NG; ++grp) {
-                    const f4 ks = *reinterpret_cast<const f4 *>(&from.ks[i][grp][16 * half + 4 * g]);
+                    for (int c = 0; c < F::W; ++c) {
+                        const h8 key = from.k[i][half][c][lane];
 #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                        for (int j = 0; j < 4; ++j)
-                            x[nt][4 * half + j] = fmaf(ks[j], acc[nt][grp][j], grp ? x[nt][4 * half + j] : zero[nt][j]);
-                }
-            }
-            const bool missing = step_now.page[i] < 0;
-            if (pr + kTile > all_see || missing) {  // some position is not seen by some row
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        const int pos = pr + 16 * (j >> 2) + 4 * g + (j & 3);
-                        if (pos >= limit[nt] || missing) x[nt][j] = -__builtin_inff();
+                        for (int nt = 0; nt < NT; ++nt)
+                            acc[nt][c / F::KG] = __builtin_amdgcn_mfma_f32_16x16x32_f16(
+                                key, q[nt][c], c % F::KG ? acc[nt][c / F::KG] : (f4){0, 0, 0, 0}, 0, 0, 0);
                     }
+#pragma unroll
+                    for (int grp = 0; grp < F::NG; ++grp) {
+                        const f4 ks = *reinterpret_cast<const f4 *>(&from.ks[i][grp][16 * half + 4 * g]);
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) y[nt][j] = fmaf(ks[j], acc[nt][grp][j], y[nt][j]);
+                    }
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) x[nt][8 * i + 4 * half + j] = y[nt][j];
+                }
+            bool missing = false;
+#pragma unroll
+            for (int i = 0; i < RECS; ++i) missing |= step_now.page[i] < 0;
+            if (p0 + STEP > all_see || missing) {  // some position is not seen by some row
+#pragma unroll
+                for (int j = 0; j < 8 * RECS; ++j) {
+                    const int pos = p0 + kTile * (j >> 3) + 16 * ((j >> 2) & 1) + 4 * g + (j & 3);
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+                        if (pos >= limit[nt] || step_now.page[j >> 3] < 0) x[nt][j] = -__builtin_inff();
+                }
             }
             bool grown = false;
             float top[NT];
@@ -231,20 +234,23 @@ __global__ void __launch_bounds__(64 * kAttendWaves, 2) rows_kernel(const Attend
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) s[nt].grow(top[nt]);
             }
-            h8 p[NT];
-            h8 row = one_row<D, GROUP>(lane);
-            if (n < 2 * F::NG) row = *reinterpret_cast<const h8 *>(&from.zs[i][n][4 * g]);
+            h8 p[NT][RECS];
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-                p[nt] = s[nt].weights(x[nt], factor[nt]);
-                s[nt].z = __builtin_amdgcn_mfma_f32_16x16x32_f16(row, p[nt], s[nt].z, 0, 0, 0);
-            }
+            for (int nt = 0; nt < NT; ++nt) s[nt].weights(x[nt], factor[nt], p[nt]);
 #pragma unroll
-            for (int c = 0; c < 2 * F::W; ++c) {
-                const h8 value = from.v[i][c][lane];
+            for (int i = 0; i < RECS; ++i) {
+                h8 row = one_row<D, GROUP>(lane);
+                if (n < 2 * F::NG) row = *reinterpret_cast<const h8 *>(&from.zs[i][n][4 * g]);
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
-                    s[nt].o[c] = __builtin_amdgcn_mfma_f32_16x16x32_f16(value, p[nt], s[nt].o[c], 0, 0, 0);
+                    s[nt].z = __builtin_amdgcn_mfma_f32_16x16x32_f16(row, p[nt][i], s[nt].z, 0, 0, 0);
+#pragma unroll
+                for (int c = 0; c < 2 * F::W; ++c) {
+                    const h8 value = from.v[i][c][lane];
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+                        s[nt].o[c] = __builtin_amdgcn_mfma_f32_16x16x32_f16(value, p[nt][i], s[nt].o[c], 0, 0, 0);
+                }
             }
         }
         share.unpack(stage[now ^ 1], rec, hs, lane, e.len);

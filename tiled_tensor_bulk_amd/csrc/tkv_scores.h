@@ -58,8 +58,9 @@ struct ScoreKeys {  // 32 positions
 #pragma unroll
         for (int j = 0; j < 8; ++j) sum[j] = 0.0f;
     }
-    // add the rows' weights; `masked`: some row does not see some position
-    __device__ __forceinline__ void add(const ScoreRows<D, GROUP> &r, bool masked, int p0, int limit, int lane) {
+    // add the rows' weights; MASKED: some row does not see some position
+    template <bool MASKED>
+    __device__ __forceinline__ void add(const ScoreRows<D, GROUP> &r, int p0, int limit, int lane) {
         const int g = lane >> 4;
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
@@ -76,7 +77,7 @@ struct ScoreKeys {  // 32 positions
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 float w = __builtin_amdgcn_exp2f(fmaf(y[i], r.factor, -r.lse2));
-                if (masked) w = p0 + 16 * half + 4 * g + i < limit ? w : 0.0f;
+                if (MASKED) w = p0 + 16 * half + 4 * g + i < limit ? w : 0.0f;
                 sum[4 * half + i] += w;
             }
         }
@@ -113,16 +114,33 @@ __global__ void __launch_bounds__(64 * kAttendWaves) scores_kernel(const AttendA
         const int i = p0 - (e.len - e.n);
         if (i > 0) t = (int)((int64_t)i * a.group_heads / 16);
     }
-    ScoreRows<D, GROUP> rows;
-    if (t < tiles) rows.load(a, first_tile + t, lane);
-    for (; t < tiles; ++t) {
-        const ScoreRows<D, GROUP> now = rows;
-        if (t + 1 < tiles) rows.load(a, first_tile + t + 1, lane);
-        const int r = t * 16 + n;
-        const int limit = r < e.rows ? e.limit(a, r / a.group_heads) : 0;
-        const bool masked = t * 16 + 16 > e.rows || p0 + kTile * RECS > e.limit(a, t * 16 / a.group_heads);
+    // tiles whose every row sees all positions, and, before and after, others
+    int full = tiles, last_full = e.rows / 16;
+    if (!a.causal) {
+        if (p0 + kTile * RECS <= e.len) full = 0;
+    } else {
+        const int i = p0 + kTile * RECS - 1 - (e.len - e.n);  // the first new token that does
+        const int64_t r = i > 0 ? (int64_t)i * a.group_heads : 0;
+        if (p0 + kTile * RECS <= e.len && r <= e.rows) full = (int)((r + 15) / 16);
+    }
+    full = full < t ? t : full;
+    ScoreRows<D, GROUP> even, odd;
+    const auto go = [&](ScoreRows<D, GROUP> &now, ScoreRows<D, GROUP> &next) {
+        if (t + 1 < tiles) next.load(a, first_tile + t + 1, lane);
+        if (t >= full && t < last_full) {
 #pragma unroll
-        for (int i = 0; i < RECS; ++i) keys[i].add(now, masked, p0 + kTile * i, limit, lane);
+            for (int i = 0; i < RECS; ++i) keys[i].template add<false>(now, 0, 0, lane);
+        } else {
+            const int r = t * 16 + n, limit = r < e.rows ? e.limit(a, r / a.group_heads) : 0;
+#pragma unroll
+            for (int i = 0; i < RECS; ++i) keys[i].template add<true>(now, p0 + kTile * i, limit, lane);
+        }
+        ++t;
+    };
+    if (t < tiles) even.load(a, first_tile + t, lane);
+    while (t < tiles) {
+        go(even, odd);
+        if (t < tiles) go(odd, even);
     }
     const int64_t row = ((int64_t)seq * a.c.heads + head) * a.score_stride;
 #pragma unroll
