@@ -14,10 +14,11 @@
 // Numbers.  With code c, scale s and zero z of a position and channel group,
 //   q . k = sum over groups of s * (q . c) + z * (sum of q)
 //   p . v = sum over positions of p * (s * c), plus p * z
-// q . c is a product of fp16 numbers, exact up to its fp32 sum (a row of q is
-// first scaled by a power of two to a largest magnitude in [2^14, 2^15), and
-// its elements that meet an upper nibble by 2^-4 more, so what fp16 drops is
-// below 2^-35 of that largest); s and z come in at fp32.  For V, s * (c - 8) is
+// q . c is a product of fp16 numbers, exact up to its fp32 sum (a bf16 row of
+// q is first scaled by a power of two to a largest magnitude in [2^14, 2^15),
+// so what fp16 drops is below 2^-38 of that largest); s and z come in at fp32.
+// Where a record is unpacked for few rows, its codes are 64 too large, and the
+// sum starts at -64 * (sum of q).  For V, s * (c - 8) is
 // rounded to fp16 (half a step is 2^-11 of it, relative; with c itself, whose
 // numbers lie on one side of zero, the error of the sum was 3 times as
 // large), and so is p.  The sums of p * (z + 8 s) are two more rows of the
@@ -50,34 +51,6 @@ constexpr float kFar = -1e30f;  // reference of a row that has seen nothing
 constexpr float kLift = 7.0f;   // weights are held times 2^7
 constexpr float kSlack = 8.0f;
 
-template <int D, int GROUP>
-struct KTile {
-    uint32_t w[2][Format<D, GROUP>::W];
-    h8 pair[2][Format<D, GROUP>::NG];  // (scale, zero) of positions 16 half + 4 g + 0..3
-};
-
-template <int D, int GROUP>
-struct VTile {
-    uint32_t w[2 * Format<D, GROUP>::W];
-    h8 scale[Format<D, GROUP>::NG];  // of the lane's 8 positions
-    h8 row;                          // row n of the operand of scales and zeros
-};
-
-template <int D, int GROUP>
-__device__ __forceinline__ void load_k(const char *rec, int lane, KTile<D, GROUP> &k) {
-    using F = Format<D, GROUP>;
-#pragma unroll
-    for (int half = 0; half < 2; ++half) {
-#pragma unroll
-        for (int s = 0; s < F::S; ++s)
-            load_words<F::WV>(rec + (((half * F::S + s) * 64 + lane) * F::WV) * 4, &k.w[half][s * F::WV]);
-#pragma unroll
-        for (int grp = 0; grp < F::NG; ++grp)
-            k.pair[half][grp] =
-                *reinterpret_cast<const h8 *>(rec + F::KP + (grp * kTile + 16 * half + 4 * (lane >> 4)) * 4);
-    }
-}
-
 // Rows 0, 1, 2, .. of the operand of scales and zeros are scale and zero of
 // each group as they lie in the record; then comes a row of ones, if there is
 // room, then zeros.
@@ -88,20 +61,6 @@ template <int D, int GROUP>
 __device__ __forceinline__ h8 one_row(int lane) {
     const _Float16 x = (lane & 15) == 2 * Format<D, GROUP>::NG ? (_Float16)1.0f : (_Float16)0.0f;
     return (h8){x, x, x, x, x, x, x, x};
-}
-
-template <int D, int GROUP>
-__device__ __forceinline__ void load_v(const char *rec, int lane, VTile<D, GROUP> &v) {
-    using F = Format<D, GROUP>;
-#pragma unroll
-    for (int hs = 0; hs < 2 * F::S; ++hs)
-        load_words<F::WV>(rec + F::VC + ((hs * 64 + lane) * F::WV) * 4, &v.w[hs * F::WV]);
-#pragma unroll
-    for (int grp = 0; grp < F::NG; ++grp)
-        v.scale[grp] = *reinterpret_cast<const h8 *>(rec + F::VP + grp * 128 + (lane >> 4) * 16);
-    v.row = one_row<D, GROUP>(lane);
-    if ((lane & 15) < 2 * F::NG)
-        v.row = *reinterpret_cast<const h8 *>(rec + F::VP + (lane & 15) * 64 + (lane >> 4) * 16);
 }
 
 // A sequence's extent and the rows of one block.
@@ -147,39 +106,59 @@ struct Pages {
 };
 
 // Products of a record's 32 positions with the wave's rows, in fp32:
-// x[nt][4 * half + i] for position 16 half + 4 g + i, times 2^-kCodeBits as qsum is.
+// x[nt][4 * half + i] for position 16 half + 4 g + i.  first: -kPlus * qsum, four times.
 template <int D, int GROUP, int NT>
-__device__ __forceinline__ void products(const KTile<D, GROUP> &k, const h8 (&q)[NT][D / 32],
-                                         const float (&qsum)[NT][D / GROUP], float (&x)[NT][8]) {
+__device__ __forceinline__ void products(const char *rec, int lane, const h8 (&q)[NT][D / 32],
+                                         const float (&qsum)[NT][D / GROUP], const f4 (&first)[NT][D / GROUP],
+                                         float (&x)[NT][8]) {
     using F = Format<D, GROUP>;
 #pragma unroll
-    for (int half = 0; half < 2; ++half)
+    for (int half = 0; half < 2; ++half) {
+        uint32_t w[F::W];
+#pragma unroll
+        for (int s = 0; s < F::S; ++s)
+            load_words<F::WV>(rec + ((half * F::S + s) * 64 + lane) * (F::WV * 4), &w[s * F::WV]);
+        f4 acc[NT][F::NG];
+#pragma unroll
+        for (int c = 0; c < F::W; ++c) {
+            const h8 key = codes_plus(w[c]);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+                acc[nt][c / F::KG] = __builtin_amdgcn_mfma_f32_16x16x32_f16(
+                    key, q[nt][c], c % F::KG ? acc[nt][c / F::KG] : first[nt][c / F::KG], 0, 0, 0);
+        }
 #pragma unroll
         for (int grp = 0; grp < F::NG; ++grp) {
-            f4 acc[NT];
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) acc[nt] = (f4){0, 0, 0, 0};
-#pragma unroll
-            for (int c = 0; c < F::KG; ++c) {
-                const h8 key = codes_as_bits(k.w[half][grp * F::KG + c]);
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-                    acc[nt] = __builtin_amdgcn_mfma_f32_16x16x32_f16(key, q[nt][grp * F::KG + c], acc[nt], 0, 0, 0);
-            }
+            // (scale, zero) of positions 16 half + 4 g + 0..3
+            const h8 pair = *reinterpret_cast<const h8 *>(rec + F::KP + (grp * kTile + 16 * half + 4 * (lane >> 4)) * 4);
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    const float s = (float)k.pair[half][grp][2 * i], z = (float)k.pair[half][grp][2 * i + 1];
-                    const float y = grp == 0 ? z * qsum[nt][grp] : fmaf(z, qsum[nt][grp], x[nt][4 * half + i]);
-                    x[nt][4 * half + i] = fmaf(s, acc[nt][i], y);
+                    const float y = fmaf((float)pair[2 * i + 1], qsum[nt][grp], grp ? x[nt][4 * half + i] : 0.0f);
+                    x[nt][4 * half + i] = fmaf((float)pair[2 * i], acc[nt][grp][i], y);
                 }
         }
+    }
 }
 
-__device__ __forceinline__ float over_groups_sum(float v) {  // over the four lanes of a row
-    v += __shfl_xor(v, 16);
-    return v + __shfl_xor(v, 32);
+// Sum and maximum over the four lanes of a row: each swap of lanes leaves a
+// lane with its own number and that of the one 16, or 32, away.
+// (From assembly: given one number twice, the compiler takes the builtin's two
+// results for one.  The swap waits for what a VALU has just written.)
+template <class Op>
+__device__ __forceinline__ float over_groups(float v, Op op) {
+    float a = v, b = v;
+    asm("s_nop 1\n\tv_permlane16_swap_b32 %0, %1" : "+v"(a), "+v"(b));
+    a = b = op(a, b);
+    asm("s_nop 1\n\tv_permlane32_swap_b32 %0, %1" : "+v"(a), "+v"(b));
+    return op(a, b);
+}
+__device__ __forceinline__ float over_groups_sum(float v) {
+    return over_groups(v, [](float a, float b) { return a + b; });
+}
+__device__ __forceinline__ float over_groups_max(float v) {
+    return over_groups(v, [](float a, float b) { return fmaxf(a, b); });
 }
 __device__ __forceinline__ float over_rows_sum(float v) {  // over 16 neighbouring lanes, by rotations
     v += __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), 0x128, 15, 15, true));
@@ -187,11 +166,6 @@ __device__ __forceinline__ float over_rows_sum(float v) {  // over 16 neighbouri
     v += __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), 0x122, 15, 15, true));
     return v + __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), 0x121, 15, 15, true));
 }
-__device__ __forceinline__ float over_groups_max(float v) {
-    v = fmaxf(v, __shfl_xor(v, 16));
-    return fmaxf(v, __shfl_xor(v, 32));
-}
-
 // Four channels of an output row, and with the first ones its lse.
 __device__ __forceinline__ void write_row(const AttendArgs &a, const Extent &e, int seq, int head, int row, int channel,
                                           f4 y, float best, float sum) {
@@ -214,45 +188,55 @@ template <int D, int GROUP>
 struct Row {
     uint4 raw[D / 32];
     __device__ __forceinline__ void load(const AttendArgs &a, const Extent &e, int head, int r, int g, bool live) {
-        const int i = live ? r / a.group_heads : 0, hq = head * a.group_heads + (live ? r - i * a.group_heads : 0);
+        r = live ? r : 0;  // the first row is read for one that is not there, and dropped
+        const int i = r / a.group_heads, hq = head * a.group_heads + r - i * a.group_heads;
         const int64_t row = (e.start + i) * a.q.token_stride + hq * a.q.head_stride + 8 * g;
 #pragma unroll
-        for (int c = 0; c < D / 32; ++c) raw[c] = live ? load8_raw(a.q, row + 32 * c) : make_uint4(0, 0, 0, 0);
+        for (int c = 0; c < D / 32; ++c) raw[c] = load8_raw(a.q, row + 32 * c);
+#pragma unroll
+        for (int c = 0; c < D / 32; ++c)
+            raw[c] = live ? raw[c] : make_uint4(0, 0, 0, 0);
     }
-    // q, its sums over the groups of channels (times 2^-kCodeBits), and what
-    // turns products into logarithms to base 2: at least the smallest normal
-    // number, as masked products are -inf.
+    __device__ __forceinline__ void wait() {
+#pragma unroll
+        for (int c = 0; c < D / 32; ++c) asm volatile("" : "+v"(raw[c].x), "+v"(raw[c].y), "+v"(raw[c].z), "+v"(raw[c].w));
+    }
+    // q, its sums over the groups of channels, and what turns products into
+    // logarithms to base 2: at least the smallest normal number, as masked
+    // products are -inf.
+    template <bool BF16>
     __device__ __forceinline__ void operand(const AttendArgs &a, h8 (&q)[D / 32], float (&qsum)[D / GROUP],
                                             float &factor) const {
         using F = Format<D, GROUP>;
+        const uint32_t sign = a.scale_log2 < 0.0f ? 0x80008000u : 0;  // moves into q
         float x[F::W][8], top = 0.0f;
 #pragma unroll
         for (int c = 0; c < F::W; ++c) {
-            raw_to_float(raw[c], a.q.type, x[c]);
+            raw_to_float<BF16>(make_uint4(raw[c].x ^ sign, raw[c].y ^ sign, raw[c].z ^ sign, raw[c].w ^ sign), x[c]);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) top = fmaxf(top, fabsf(x[c][j]));
+            for (int j = 0; j < 8; ++j)
+                if (BF16) top = fmaxf(top, fabsf(x[c][j]));
         }
-        top = over_groups_max(top);
         int power = 0;
-        if (top > 0.0f && top < __builtin_inff()) {
-            (void)frexpf(top, &power);  // top = m * 2^power, m in [0.5, 1)
-            power = 15 - power;
+        if constexpr (BF16) {
+            top = over_groups_max(top);
+            if (top > 0.0f && top < __builtin_inff()) power = 15 - __builtin_amdgcn_frexp_expf(top);
         }
-        const float f = fabsf(ldexpf(a.scale_log2, kCodeBits - power));
+        const float f = fabsf(ldexpf(a.scale_log2, -power));
         factor = fminf(fmaxf(f, 0x1p-126f), 0x1.fffffep127f);
-        const float sign = a.scale_log2 < 0.0f ? -1.0f : 1.0f;
-#pragma unroll
-        for (int grp = 0; grp < F::NG; ++grp) qsum[grp] = 0.0f;
 #pragma unroll
         for (int c = 0; c < F::W; ++c)
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const _Float16 v = (_Float16)ldexpf(sign * x[c][j], power - code_shift(j));
-                q[c][j] = v;
-                qsum[c / F::KG] = fmaf((float)v, (float)(1 << code_shift(j)), qsum[c / F::KG]);
-            }
+            for (int j = 0; j < 8; ++j) q[c][j] = (_Float16)(BF16 ? ldexpf(x[c][j], power) : x[c][j]);
+        const h8 ones = {1, 1, 1, 1, 1, 1, 1, 1};
 #pragma unroll
-        for (int grp = 0; grp < F::NG; ++grp) qsum[grp] = over_groups_sum(qsum[grp]) * (1.0f / (1 << kCodeBits));
+        for (int grp = 0; grp < F::NG; ++grp) {
+            f4 sum = {0, 0, 0, 0};
+#pragma unroll
+            for (int c = 0; c < F::KG; ++c)
+                sum = __builtin_amdgcn_mfma_f32_16x16x32_f16(ones, q[grp * F::KG + c], sum, 0, 0, 0);
+            qsum[grp] = sum[0];
+        }
     }
 };
 
@@ -266,7 +250,7 @@ __device__ __forceinline__ h8 sum_parts(const float (&qsum)[D / GROUP], int g) {
     h8 r = {0, 0, 0, 0, 0, 0, 0, 0};
 #pragma unroll
     for (int grp = 0; grp < D / GROUP; ++grp) {
-        float y = qsum[grp] * (float)(1 << (kCodeBits - kSumBits));
+        float y = qsum[grp] * (1.0f / (1 << kSumBits));
         const _Float16 a = (_Float16)y;
         y -= (float)a;
         const _Float16 b = (_Float16)y;
@@ -277,7 +261,7 @@ __device__ __forceinline__ h8 sum_parts(const float (&qsum)[D / GROUP], int g) {
 }
 // what turns products in those units into logarithms
 __device__ __forceinline__ float sums_factor(float factor) {
-    return fmaxf(factor * (1.0f / (1 << (kCodeBits - kSumBits))), 0x1p-126f);
+    return fminf(factor * (float)(1 << kSumBits), 0x1.fffffep127f);
 }
 
 // Where the scores kernel finds a tile of 16 rows and what belongs to it.
@@ -319,7 +303,7 @@ struct Softmax {
     __device__ __forceinline__ void grow(float y) {  // y: the largest logarithm of the lane's positions
         const float t = over_groups_max(y);
         const float m1 = t > m + kSlack ? t : m;
-        const float f = exp2f(m - m1);
+        const float f = __builtin_amdgcn_exp2f(m - m1);
         m = m1;
         l *= f;
         z *= f;
@@ -357,25 +341,32 @@ struct Softmax {
     }
 };
 
-// Waves of a SIMD that the registers of a wave leave room for: queries, sums
-// and logits of its rows, a record on its way, and what is being worked on.
+// Few rows: the four waves share them and take every fourth record.  A wave
+// has a ring of two records in LDS, which its loads fill without passing
+// through registers: while it works on one, the other is on its way, and the
+// registers leave room for four waves on a SIMD.
 template <int D, int GROUP, int NT>
 struct FewRows {
     using F = Format<D, GROUP>;
-    static constexpr int kRegs = NT * (4 * F::W + 8 * F::W + 4 + 8 + 8) + 4 * F::W + 4 + 12 * F::NG + 32;
+    static constexpr int kLoads = (F::REC + 1023) / 1024;  // of a record
+    static constexpr int kSlot = kLoads * 1024;
+    static constexpr int kDepth = 2;
+    static constexpr int kRing = kDepth * kSlot;  // a wave's; later CH words of its sums, and its references and sums
+    static constexpr int CH = D == 96 ? 3 : D == 64 && NT == 2 ? 2 : 4;
+    static constexpr int kRounds = 2 * F::W / CH;
+    static_assert(kRounds * CH == 2 * F::W, "rounds cover the channels");
+    static constexpr int kJoinM = kRing - 32 * 4 * NT, kJoinL = kRing - 16 * 4 * NT;
+    static_assert(CH * NT * 1024 <= kJoinM, "both fit");
+    static constexpr int kRegs = NT * (12 * F::W + 20) + 8 * F::NG + 2 * F::W + 28;
     static constexpr int kWaves = kRegs <= 128 ? 4 : kRegs <= 168 ? 3 : kRegs <= 256 ? 2 : 1;
 };
 
-// Few rows: the four waves share them and take every fourth record.
-template <int D, int GROUP, int NT>
+template <int D, int GROUP, int NT, bool BF16>
 __global__ void __launch_bounds__(64 * kAttendWaves, (FewRows<D, GROUP, NT>::kWaves)) attend_kernel(const AttendArgs a) {
     using F = Format<D, GROUP>;
+    using K = FewRows<D, GROUP, NT>;
     constexpr int R = 16 * NT;
-    constexpr int CH = NT == 2 ? (D == 96 ? 3 : 4) : (D / 16 < 8 ? D / 16 : 8);  // V words joined in a round
-    constexpr int ROUNDS = (2 * F::W) / CH;
-    static_assert(ROUNDS * CH == 2 * F::W, "rounds cover the channels");
-    __shared__ float join[kAttendWaves][CH * NT][64][4];
-    __shared__ float join_m[kAttendWaves][R], join_l[kAttendWaves][R];
+    __shared__ __attribute__((aligned(1024))) char ring[kAttendWaves * K::kRing];
 
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int lane = threadIdx.x & 63, g = lane >> 4, n = lane & 15;
@@ -402,56 +393,76 @@ __global__ void __launch_bounds__(64 * kAttendWaves, (FewRows<D, GROUP, NT>::kWa
 
     Row<D, GROUP> raw[NT];
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) raw[nt].load(a, e, head, r0 + 16 * nt + n, g, r0 + 16 * nt + n < e.rows);
-    KTile<D, GROUP> k;
-    VTile<D, GROUP> v;
-    int p0 = t0 + kTile * wave;
-    int page = -1;
-    if (p0 < end) {
-        page = pages.get(a, table, p0 >> shift, lane);
-        const char *rec = record_at(a.c, page < 0 ? 0 : page, head, p0 / kTile);
-        load_k<D, GROUP>(rec, lane, k);
-        load_v<D, GROUP>(rec, lane, v);
+    for (int nt = 0; nt < NT; ++nt) {
+        raw[nt].load(a, e, head, r0 + 16 * nt + n, g, r0 + 16 * nt + n < e.rows);
+        raw[nt].wait();  // no wait for them later, which would be one for the records too
     }
+    char *const mine = ring + wave * K::kRing;
+    const uint32_t mine_at = lds_address(mine);
+    int missing = 0;  // bit s: the record in slot s has no page
+    const auto fetch = [&](int pos, int slot) {
+        const int page = pages.get(a, table, pos >> shift, lane);
+        const char *rec = record_at(a.c, page < 0 ? 0 : page, head, pos / kTile);
+        missing = (missing & ~(1 << slot)) | ((page < 0 ? 1 : 0) << slot);
+#pragma unroll
+        for (int i = 0; i < K::kLoads; ++i)
+            load_to_lds(rec, page < 0 ? 0 : F::REC, mine_at + slot * K::kSlot + i * 1024, i * 1024 + lane * 16);
+    };
+    constexpr int kStride = kTile * kAttendWaves;
+    int p0 = t0 + kTile * wave;
+#pragma unroll
+    for (int i = 0; i < K::kDepth; ++i)
+        if (p0 + i * kStride < end) fetch(p0 + i * kStride, i);
 
     h8 q[NT][F::W];
     float qsum[NT][F::NG], factor[NT];
+    f4 first[NT][F::NG];
     int limit[NT];
     Softmax<D, GROUP> s[NT];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
         const int r = r0 + 16 * nt + n;
         limit[nt] = r < e.rows ? e.limit(a, r / a.group_heads) : 0;
-        raw[nt].operand(a, q[nt], qsum[nt], factor[nt]);
+        raw[nt].template operand<BF16>(a, q[nt], qsum[nt], factor[nt]);
+#pragma unroll
+        for (int grp = 0; grp < F::NG; ++grp) {
+            const float f = -kPlus * qsum[nt][grp];
+            first[nt][grp] = (f4){f, f, f, f};
+        }
         s[nt].clear();
         if (a.frag_q && split == 0 && wave == 0 && r0 / 16 + nt < a.row_tiles)
             keep_rows<D, GROUP>(a, ((int64_t)seq * a.c.heads + head) * a.row_tiles + r0 / 16 + nt, lane, q[nt],
                                 sum_parts<D, GROUP>(qsum[nt], g), sums_factor(factor[nt]));
     }
 
-    while (p0 < end) {
-        const int next = p0 + kTile * kAttendWaves;
-        const int page_now = page;
-        const char *rec = nullptr;
-        if (next < end) {
-            page = pages.get(a, table, next >> shift, lane);
-            rec = record_at(a.c, page < 0 ? 0 : page, head, next / kTile);
-        }
+    for (int slot = 0; p0 < end; p0 += kStride, slot ^= 1) {
+        static_assert(K::kDepth == 2, "slots alternate");
+        if (p0 + kStride < end)
+            wait_loads<K::kLoads>();
+        else
+            wait_loads<0>();
+        const char *rec = mine + slot * K::kSlot;
+        const bool gone = (missing >> slot) & 1;
         float x[NT][8];
-        products<D, GROUP, NT>(k, q, qsum, x);
-        if (rec) load_k<D, GROUP>(rec, lane, k);
+        products<D, GROUP, NT>(rec, lane, q, qsum, first, x);
+        h8 scale[F::NG];  // of the lane's 8 positions
+#pragma unroll
+        for (int grp = 0; grp < F::NG; ++grp)
+            scale[grp] = *reinterpret_cast<const h8 *>(rec + F::VP + grp * 128 + g * 16);
+        h8 row = one_row<D, GROUP>(lane);
+        if (n < 2 * F::NG) row = *reinterpret_cast<const h8 *>(rec + F::VP + n * 64 + g * 16);
 
-        if (p0 + kTile > all_see || page_now < 0) {  // some position is not seen by some row
+        if (p0 + kTile > all_see || gone) {  // some position is not seen by some row
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
                 const int pos = p0 + 16 * (j >> 2) + 4 * g + (j & 3);
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
-                    if (pos >= limit[nt] || page_now < 0) x[nt][j] = -__builtin_inff();
-                if (pos >= e.len || page_now < 0) {  // what lies past the sequence's end may be anything
+                    if (pos >= limit[nt] || gone) x[nt][j] = -__builtin_inff();
+                if (pos >= e.len) {  // what lies past the sequence's end may be anything
 #pragma unroll
-                    for (int grp = 0; grp < F::NG; ++grp) v.scale[grp][j] = (_Float16)0.0f;
-                    v.row[j] = (_Float16)0.0f;
+                    for (int grp = 0; grp < F::NG; ++grp) scale[grp][j] = (_Float16)0.0f;
+                    row[j] = (_Float16)0.0f;
                 }
             }
         }
@@ -470,61 +481,62 @@ __global__ void __launch_bounds__(64 * kAttendWaves, (FewRows<D, GROUP, NT>::kWa
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
             s[nt].weights(x[nt], factor[nt], p[nt]);
-            s[nt].z = __builtin_amdgcn_mfma_f32_16x16x32_f16(v.row, p[nt][0], s[nt].z, 0, 0, 0);
+            s[nt].z = __builtin_amdgcn_mfma_f32_16x16x32_f16(row, p[nt][0], s[nt].z, 0, 0, 0);
         }
 #pragma unroll
-        for (int c = 0; c < 2 * F::W; ++c) {
-            const h8 value = codes_minus_8(v.w[c]) * v.scale[c / F::VG];
+        for (int hs = 0; hs < 2 * F::S; ++hs) {
+            uint32_t w[F::WV];
+            load_words<F::WV>(rec + F::VC + (hs * 64 + lane) * (F::WV * 4), w);
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-                s[nt].o[c] = __builtin_amdgcn_mfma_f32_16x16x32_f16(value, p[nt][0], s[nt].o[c], 0, 0, 0);
+            for (int i = 0; i < F::WV; ++i) {
+                const int c = hs * F::WV + i;
+                const h8 value = codes_minus<8>(w[i]) * scale[c / F::VG];
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+                    s[nt].o[c] = __builtin_amdgcn_mfma_f32_16x16x32_f16(value, p[nt][0], s[nt].o[c], 0, 0, 0);
+            }
         }
-        if (rec) load_v<D, GROUP>(rec, lane, v);
-        p0 = next;
+        if (p0 + K::kDepth * kStride < end) {
+            wait_lds();  // the slot has been read
+            fetch(p0 + K::kDepth * kStride, slot);
+        }
     }
 
     // ---- join the waves
+    wait_lds();
+    const auto m_of = [&](int w, int r) -> float & { return reinterpret_cast<float *>(ring + w * K::kRing + K::kJoinM)[r]; };
+    const auto l_of = [&](int w, int r) -> float & { return reinterpret_cast<float *>(ring + w * K::kRing + K::kJoinL)[r]; };
+    const auto o_of = [&](int w, int item) -> f4 & { return reinterpret_cast<f4 *>(ring + w * K::kRing)[item]; };
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
         s[nt].finish(lane);
-        if (g == 0) join_m[wave][16 * nt + n] = s[nt].m, join_l[wave][16 * nt + n] = s[nt].l;
-    }
-    __syncthreads();
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-        float best = join_m[0][16 * nt + n];
-#pragma unroll
-        for (int w = 1; w < kAttendWaves; ++w) best = fmaxf(best, join_m[w][16 * nt + n]);
-        const float f = exp2f(s[nt].m - best);
-#pragma unroll
-        for (int c = 0; c < 2 * F::W; ++c) s[nt].o[c] *= f;
+        if (g == 0) m_of(wave, 16 * nt + n) = s[nt].m, l_of(wave, 16 * nt + n) = s[nt].l;
     }
     const int64_t unit = ((int64_t)seq * a.c.heads + head) * a.n_split + split;
 #pragma unroll
-    for (int round = 0; round < ROUNDS; ++round) {
+    for (int round = 0; round < K::kRounds; ++round) {
         if (round) __syncthreads();
 #pragma unroll
-        for (int c = 0; c < CH; ++c)
+        for (int c = 0; c < K::CH; ++c)
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-                *reinterpret_cast<f4 *>(join[wave][c * NT + nt][lane]) = s[nt].o[round * CH + c];
+            for (int nt = 0; nt < NT; ++nt) o_of(wave, (c * NT + nt) * 64 + lane) = s[nt].o[round * K::CH + c];
         __syncthreads();
-        for (int item = threadIdx.x; item < CH * NT * 64; item += 64 * kAttendWaves) {
+        for (int item = threadIdx.x; item < K::CH * NT * 64; item += 64 * kAttendWaves) {
             const int cn = item >> 6, ln = item & 63;
-            const int row = r0 + 16 * (cn % NT) + (ln & 15);
+            const int rl = 16 * (cn % NT) + (ln & 15), row = r0 + rl;
             if (row >= e.rows) continue;
-            const int rl = 16 * (cn % NT) + (ln & 15);
-            float best = join_m[0][rl];
+            float best = m_of(0, rl);
 #pragma unroll
-            for (int w = 1; w < kAttendWaves; ++w) best = fmaxf(best, join_m[w][rl]);
+            for (int w = 1; w < kAttendWaves; ++w) best = fmaxf(best, m_of(w, rl));
             float sum = 0.0f;
             f4 y = (f4){0, 0, 0, 0};
 #pragma unroll
             for (int w = 0; w < kAttendWaves; ++w) {
-                sum += join_l[w][rl] * exp2f(join_m[w][rl] - best);
-                y += *reinterpret_cast<const f4 *>(join[w][cn][ln]);
+                const float f = __builtin_amdgcn_exp2f(m_of(w, rl) - best);
+                sum += l_of(w, rl) * f;
+                y += o_of(w, item) * f;
             }
-            const int channel = 16 * (round * CH + cn / NT) + 4 * (ln >> 4);
+            const int channel = 16 * (round * K::CH + cn / NT) + 4 * (ln >> 4);
             if (a.n_split > 1) {
                 const int64_t to = unit * a.rows + row;
                 *reinterpret_cast<f4 *>(a.part_o + to * D + channel) = y;

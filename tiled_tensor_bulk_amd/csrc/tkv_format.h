@@ -61,38 +61,40 @@ __device__ __forceinline__ void store_words(char *p, const uint32_t *in) {
     }
 }
 
-// 8 codes minus 8 as fp16, exactly.  0x6400 is 1024 in fp16, whose last place
-// is 1: or-ing a code below it gives 1024 + code (or 1024 + 16 * code for the
-// upper nibble of a byte), and the rest is taken off again: 1 shift, 4
+// 8 codes minus BIAS as fp16, exactly.  0x6400 is 1024 in fp16, whose last
+// place is 1: or-ing a code below it gives 1024 + code (or 1024 + 16 * code for
+// the upper nibble of a byte), and the rest is taken off again: 1 shift, 4
 // and-ors and 4 packed operations for 8 elements.
-__device__ __forceinline__ h8 codes_minus_8(uint32_t w) {
+template <int BIAS>
+__device__ __forceinline__ h8 codes_minus(uint32_t w) {
     const uint32_t x = w >> 8;
     // from a register, as an and-or takes one number that is not: the compiler
     // makes an and and an or of two that it knows
     uint32_t magic;
     asm("v_mov_b32 %0, 0x64006400" : "=v"(magic));
-    const h2 low = {(_Float16)1032.0f, (_Float16)1032.0f};
+    const h2 low = {(_Float16)(1024.0f + BIAS), (_Float16)(1024.0f + BIAS)};
     const h2 s16 = {(_Float16)0.0625f, (_Float16)0.0625f};
-    const h2 b72 = {(_Float16)72.0f, (_Float16)72.0f};
+    const h2 high = {(_Float16)(64.0f + BIAS), (_Float16)(64.0f + BIAS)};
     const h2 a0 = __builtin_bit_cast(h2, (w & 0x000F000Fu) | magic) - low;
-    const h2 a1 = __builtin_bit_cast(h2, (w & 0x00F000F0u) | magic) * s16 - b72;
+    const h2 a1 = __builtin_bit_cast(h2, (w & 0x00F000F0u) | magic) * s16 - high;
     const h2 a2 = __builtin_bit_cast(h2, (x & 0x000F000Fu) | magic) - low;
-    const h2 a3 = __builtin_bit_cast(h2, (x & 0x00F000F0u) | magic) * s16 - b72;
+    const h2 a3 = __builtin_bit_cast(h2, (x & 0x00F000F0u) | magic) * s16 - high;
     return (h8){a0[0], a0[1], a1[0], a1[1], a2[0], a2[1], a3[0], a3[1]};
 }
 
-// 8 codes as they lie: the bits of a code are those of the subnormal fp16
-// number code * 2^-24, or 16 times that in the upper nibble of a byte (codes 2,
-// 3, 6 and 7), so a mask is all it takes; the matrix unit takes subnormal
-// numbers as they are.  1 shift and 4 ands for 8 elements.
-__device__ __forceinline__ h8 codes_as_bits(uint32_t w) {
+// 8 codes plus 64: bits 4..7 of 64 in fp16 count by 1, so 3 shifts and 4
+// and-ors are all.  (As the subnormal numbers that their bits are codes would
+// cost only 4 ands, but the matrix unit adds up products by the exponents of
+// their factors, and 10 bits of its sums would go.)
+constexpr float kPlus = 64.0f;
+__device__ __forceinline__ h8 codes_plus(uint32_t w) {
     typedef uint32_t u4 __attribute__((ext_vector_type(4)));
-    const uint32_t x = w >> 8;
-    return __builtin_bit_cast(h8, (u4){w & 0x000F000Fu, w & 0x00F000F0u, x & 0x000F000Fu, x & 0x00F000F0u});
+    uint32_t magic;
+    asm("v_mov_b32 %0, 0x54005400" : "=v"(magic));
+    constexpr uint32_t mask = 0x00F000F0u;
+    return __builtin_bit_cast(h8, (u4){((w << 4) & mask) | magic, (w & mask) | magic, ((w >> 4) & mask) | magic,
+                                       ((w >> 8) & mask) | magic});
 }
-// ... and so a query's element j is held divided by this
-__device__ __forceinline__ constexpr int code_shift(int j) { return j & 2 ? 4 : 0; }
-constexpr int kCodeBits = 24;
 
 // The nibble of code j in its word.
 __device__ __forceinline__ constexpr int nibble_of(int j) { return (j >> 1) + 4 * (j & 1); }
@@ -152,14 +154,25 @@ __device__ __forceinline__ uint4 load8_raw(const Tokens &t, int64_t offset) {
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-__device__ __forceinline__ void raw_to_float(const uint4 &v, int type, float *out) {
+template <bool BF16>
+__device__ __forceinline__ void raw_to_float(const uint4 &v, float *out) {
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-    for (int i = 0; i < 8; ++i) out[i] = elem_to_float((uint16_t)(w[i / 2] >> (16 * (i & 1))), type);
+    for (int i = 0; i < 8; ++i) {
+        if constexpr (BF16) {
+            out[i] = __builtin_bit_cast(float, i & 1 ? w[i / 2] & 0xFFFF0000u : w[i / 2] << 16);
+        } else {
+            out[i] = (float)__builtin_bit_cast(_Float16, (uint16_t)(w[i / 2] >> (16 * (i & 1))));
+        }
+    }
 }
 
 __device__ __forceinline__ void load8(const Tokens &t, int64_t offset, float *out) {
-    raw_to_float(load8_raw(t, offset), t.type, out);
+    const uint4 v = load8_raw(t, offset);
+    if (t.type == kBf16)
+        raw_to_float<true>(v, out);
+    else
+        raw_to_float<false>(v, out);
 }
 
 // 4 consecutive elements of a row, rounded to its type, which is 16 bits wide.
@@ -202,6 +215,45 @@ __device__ __forceinline__ void store8(const Tokens &t, int64_t offset, const fl
 #pragma unroll
         for (int i = 0; i < 8; ++i) p[i] = e[i];
     }
+}
+
+// One wave-wide load of 1 KiB straight into LDS: lane l's 16 bytes at
+// voff, or zeros where they end past `bytes`, land at lds + 16 l.  From
+// assembly, as the compiler would wait for it before every later access to
+// LDS; wait_loads() waits.  (M0 holds the LDS address and is put back, since
+// the compiler reserves it; the nops are for the hazards of M0 and of an SGPR
+// just written.)
+typedef int i4 __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(3))) void lds_void;
+
+__device__ __forceinline__ uint32_t lds_address(const void *p) { return (uint32_t)(uintptr_t)(lds_void *)p; }
+
+__device__ __forceinline__ void load_to_lds(const char *base, uint32_t bytes, uint32_t lds, uint32_t voff) {
+    const i4 d = {__builtin_amdgcn_readfirstlane((int)(uint32_t)(uint64_t)base),
+                  __builtin_amdgcn_readfirstlane((int)((uint32_t)((uint64_t)base >> 32) & 0xFFFFu)),
+                  __builtin_amdgcn_readfirstlane((int)bytes), 0x00020000};
+    const uint32_t m0 = __builtin_amdgcn_readfirstlane((int)lds);
+    uint32_t saved;
+    asm volatile(
+        "s_mov_b32 %0, m0\n\ts_mov_b32 m0, %1\n\ts_nop 4\n\t"
+        "buffer_load_dwordx4 %2, %3, 0 offen lds\n\ts_nop 0\n\ts_mov_b32 m0, %0"
+        : "=&s"(saved)
+        : "s"(m0), "v"(voff), "s"(d)
+        : "memory");
+}
+
+// At most N of this wave's loads and stores are on their way: they end in the
+// order of their issue.
+template <int N>
+__device__ __forceinline__ void wait_loads() {
+    static_assert(N < 64, "the counter's range");
+    __builtin_amdgcn_s_waitcnt((N & 0xF) | ((N >> 4) << 14) | 0x70 | 0xF00);
+    asm volatile("" ::: "memory");
+}
+// Every LDS access of this wave has ended.
+__device__ __forceinline__ void wait_lds() {
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_waitcnt(0xC07F);
 }
 
 }  // namespace tkv

@@ -6,24 +6,32 @@
 
 namespace tkv {
 
-template <int D, int GROUP>
-static int launch_group(const AttendArgs &a, int row_tile, void *stream) {
+template <int D, int GROUP, bool BF16>
+static int launch_type(const AttendArgs &a, int row_tile, void *stream) {
     const dim3 block(64 * kAttendWaves);
     const dim3 grid((uint32_t)((int64_t)a.b.n_seq * a.c.heads * a.n_split * a.row_blocks));
     hipStream_t s = (hipStream_t)stream;
     if (row_tile == 16) {
-        attend_kernel<D, GROUP, 1><<<grid, block, 0, s>>>(a);
+        attend_kernel<D, GROUP, 1, BF16><<<grid, block, 0, s>>>(a);
     } else if (row_tile == 32) {
-        attend_kernel<D, GROUP, 2><<<grid, block, 0, s>>>(a);
+        attend_kernel<D, GROUP, 2, BF16><<<grid, block, 0, s>>>(a);
     } else if (row_tile == 64) {
-        rows_kernel<D, GROUP, 1><<<grid, block, 0, s>>>(a);
+        rows_kernel<D, GROUP, 1, BF16><<<grid, block, 0, s>>>(a);
     } else {
         if constexpr (D > 128)
             return (int)hipErrorInvalidValue;
         else
-            rows_kernel<D, GROUP, 2><<<grid, block, 0, s>>>(a);
+            rows_kernel<D, GROUP, 2, BF16><<<grid, block, 0, s>>>(a);
     }
-    int rc = (int)hipGetLastError();
+    return (int)hipGetLastError();
+}
+
+template <int D, int GROUP>
+static int launch_group(const AttendArgs &a, int row_tile, void *stream) {
+    const dim3 block(64 * kAttendWaves);
+    hipStream_t s = (hipStream_t)stream;
+    int rc = a.q.type == kBf16 ? launch_type<D, GROUP, true>(a, row_tile, stream)
+                               : launch_type<D, GROUP, false>(a, row_tile, stream);
     if (rc == 0 && a.n_split > 1) rc = launch_combine(a, stream);
     if (rc == 0 && a.scores_out && a.max_len > 0) {
         constexpr int kPositions = kTile * kAttendWaves * kScoreRecords<D>;

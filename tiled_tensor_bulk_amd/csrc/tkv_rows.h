@@ -20,8 +20,7 @@
 
 namespace tkv {
 
-// Products of the matrix unit are in units of 2^-kCodeBits, z * (sum of q) in
-// units of 2^-kSumBits; scales are held times the quotient.
+// z * (sum of q) is in units of 2^kSumBits, and so scales are held divided by that.
 template <int D, int GROUP, int RECS>
 struct Stage {
     using F = Format<D, GROUP>;
@@ -63,12 +62,12 @@ struct Share {
         const int g = lane >> 4;
         if (there) {
 #pragma unroll
-            for (int i = 0; i < F::WV; ++i) to.k[rec][hs / F::S][(hs % F::S) * F::WV + i][lane] = codes_as_bits(k[i]);
+            for (int i = 0; i < F::WV; ++i) to.k[rec][hs / F::S][(hs % F::S) * F::WV + i][lane] = codes_minus<0>(k[i]);
         }
         const int live = there ? len - p0 : 0;  // what lies past the sequence's end may be anything
         if (live >= kTile) {
 #pragma unroll
-            for (int i = 0; i < F::WV; ++i) to.v[rec][hs * F::WV + i][lane] = codes_minus_8(v[i]) * scale[i];
+            for (int i = 0; i < F::WV; ++i) to.v[rec][hs * F::WV + i][lane] = codes_minus<8>(v[i]) * scale[i];
         } else {
 #pragma unroll
             for (int i = 0; i < F::WV; ++i) {
@@ -76,7 +75,7 @@ struct Share {
 #pragma unroll
                 for (int j = 0; j < 8; ++j)
                     if (4 * g + (j & 3) + 16 * (j >> 2) >= live) s[j] = (_Float16)0.0f;
-                to.v[rec][hs * F::WV + i][lane] = codes_minus_8(there ? v[i] : 0) * s;
+                to.v[rec][hs * F::WV + i][lane] = codes_minus<8>(there ? v[i] : 0) * s;
             }
         }
         const int at = hs * 64 + lane;
@@ -84,7 +83,7 @@ struct Share {
             const int grp = at >> 5, pos = at & 31, slot = 2 * (at & 15);
             if (there) {
                 const h2 pair = __builtin_bit_cast(h2, kpair);
-                to.ks[rec][grp][pos] = (float)pair[0] * (float)(1 << (kCodeBits - kSumBits));
+                to.ks[rec][grp][pos] = (float)pair[0] * (1.0f / (1 << kSumBits));
                 reinterpret_cast<_Float16 *>(&to.kz[rec][pos])[grp] = pair[1];
             }
             const int first = 4 * (slot >> 3) + (slot & 3) + 16 * ((slot >> 2) & 1);  // position of that slot
@@ -109,7 +108,7 @@ struct StepPages {
     __device__ __forceinline__ int of(int rec) const { return RECS == 1 || rec == 0 ? page[0] : page[RECS - 1]; }
 };
 
-template <int D, int GROUP, int NT>
+template <int D, int GROUP, int NT, bool BF16>
 __global__ void __launch_bounds__(64 * kAttendWaves, 2) rows_kernel(const AttendArgs a) {
     using F = Format<D, GROUP>;
     constexpr int R = 16 * NT * kAttendWaves;
@@ -160,7 +159,7 @@ __global__ void __launch_bounds__(64 * kAttendWaves, 2) rows_kernel(const Attend
         const int r = r0 + 16 * nt + n;
         limit[nt] = r < e.rows ? e.limit(a, r / a.group_heads) : 0;
         float qsum[F::NG], f;
-        raw[nt].operand(a, q[nt], qsum, f);
+        raw[nt].template operand<BF16>(a, q[nt], qsum, f);
         sums[nt] = sum_parts<D, GROUP>(qsum, g);
         factor[nt] = sums_factor(f);
         s[nt].clear();

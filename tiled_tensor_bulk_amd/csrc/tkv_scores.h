@@ -50,10 +50,10 @@ struct ScoreKeys {  // 32 positions
                 const h8 mine = *reinterpret_cast<const h8 *>(pairs + 8 * g);
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
-                    scale[grp][4 * half + i] = (float)mine[2 * i] * (float)(1 << (kCodeBits - kSumBits));
+                    scale[grp][4 * half + i] = (float)mine[2 * i] * (1.0f / (1 << kSumBits));
             }
 #pragma unroll
-            for (int c = 0; c < F::W; ++c) k[half][c] = codes_as_bits(w[half][c]);
+            for (int c = 0; c < F::W; ++c) k[half][c] = codes_minus<0>(w[half][c]);
         }
 #pragma unroll
         for (int j = 0; j < 8; ++j) sum[j] = 0.0f;
