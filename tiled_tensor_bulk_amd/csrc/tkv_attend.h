@@ -357,7 +357,7 @@ struct FewRows {
     static_assert(kRounds * CH == 2 * F::W, "rounds cover the channels");
     static constexpr int kJoinM = kRing - 32 * 4 * NT, kJoinL = kRing - 16 * 4 * NT;
     static_assert(CH * NT * 1024 <= kJoinM, "both fit");
-    static constexpr int kRegs = NT * (12 * F::W + 20) + 8 * F::NG + 2 * F::W + 28;
+    static constexpr int kRegs = NT * (12 * F::W + 4 * F::NG + 20) + 8 * F::NG + 2 * F::W + 28;
     static constexpr int kWaves = kRegs <= 128 ? 4 : kRegs <= 168 ? 3 : kRegs <= 256 ? 2 : 1;
 };
 
@@ -404,9 +404,7 @@ __global__ void __launch_bounds__(64 * kAttendWaves, (FewRows<D, GROUP, NT>::kWa
         const int page = pages.get(a, table, pos >> shift, lane);
         const char *rec = record_at(a.c, page < 0 ? 0 : page, head, pos / kTile);
         missing = (missing & ~(1 << slot)) | ((page < 0 ? 1 : 0) << slot);
-#pragma unroll
-        for (int i = 0; i < K::kLoads; ++i)
-            load_to_lds(rec, page < 0 ? 0 : F::REC, mine_at + slot * K::kSlot + i * 1024, i * 1024 + lane * 16);
+        load_run_to_lds<K::kLoads>(rec, page < 0 ? 0 : F::REC, mine_at + slot * K::kSlot, lane * 16);
     };
     constexpr int kStride = kTile * kAttendWaves;
     int p0 = t0 + kTile * wave;
@@ -445,25 +443,14 @@ __global__ void __launch_bounds__(64 * kAttendWaves, (FewRows<D, GROUP, NT>::kWa
         const bool gone = (missing >> slot) & 1;
         float x[NT][8];
         products<D, GROUP, NT>(rec, lane, q, qsum, first, x);
-        h8 scale[F::NG];  // of the lane's 8 positions
-#pragma unroll
-        for (int grp = 0; grp < F::NG; ++grp)
-            scale[grp] = *reinterpret_cast<const h8 *>(rec + F::VP + grp * 128 + g * 16);
-        h8 row = one_row<D, GROUP>(lane);
-        if (n < 2 * F::NG) row = *reinterpret_cast<const h8 *>(rec + F::VP + n * 64 + g * 16);
-
-        if (p0 + kTile > all_see || gone) {  // some position is not seen by some row
+        const bool masked = p0 + kTile > all_see || gone;  // some position is not seen by some row
+        if (masked) {
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
                 const int pos = p0 + 16 * (j >> 2) + 4 * g + (j & 3);
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
                     if (pos >= limit[nt] || gone) x[nt][j] = -__builtin_inff();
-                if (pos >= e.len) {  // what lies past the sequence's end may be anything
-#pragma unroll
-                    for (int grp = 0; grp < F::NG; ++grp) scale[grp][j] = (_Float16)0.0f;
-                    row[j] = (_Float16)0.0f;
-                }
             }
         }
         bool grown = false;
@@ -479,10 +466,25 @@ __global__ void __launch_bounds__(64 * kAttendWaves, (FewRows<D, GROUP, NT>::kWa
         }
         h8 p[NT][1];
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-            s[nt].weights(x[nt], factor[nt], p[nt]);
-            s[nt].z = __builtin_amdgcn_mfma_f32_16x16x32_f16(row, p[nt][0], s[nt].z, 0, 0, 0);
+        for (int nt = 0; nt < NT; ++nt) s[nt].weights(x[nt], factor[nt], p[nt]);
+        h8 scale[F::NG];  // of the lane's 8 positions
+#pragma unroll
+        for (int grp = 0; grp < F::NG; ++grp)
+            scale[grp] = *reinterpret_cast<const h8 *>(rec + F::VP + grp * 128 + g * 16);
+        h8 row = one_row<D, GROUP>(lane);
+        if (n < 2 * F::NG) row = *reinterpret_cast<const h8 *>(rec + F::VP + n * 64 + g * 16);
+        if (masked) {  // what lies past the sequence's end may be anything
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                if (p0 + 16 * (j >> 2) + 4 * g + (j & 3) >= e.len) {
+#pragma unroll
+                    for (int grp = 0; grp < F::NG; ++grp) scale[grp][j] = (_Float16)0.0f;
+                    row[j] = (_Float16)0.0f;
+                }
         }
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+            s[nt].z = __builtin_amdgcn_mfma_f32_16x16x32_f16(row, p[nt][0], s[nt].z, 0, 0, 0);
 #pragma unroll
         for (int hs = 0; hs < 2 * F::S; ++hs) {
             uint32_t w[F::WV];

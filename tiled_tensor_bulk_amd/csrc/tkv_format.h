@@ -217,29 +217,51 @@ __device__ __forceinline__ void store8(const Tokens &t, int64_t offset, const fl
     }
 }
 
-// One wave-wide load of 1 KiB straight into LDS: lane l's 16 bytes at
-// voff, or zeros where they end past `bytes`, land at lds + 16 l.  From
-// assembly, as the compiler would wait for it before every later access to
-// LDS; wait_loads() waits.  (M0 holds the LDS address and is put back, since
-// the compiler reserves it; the nops are for the hazards of M0 and of an SGPR
-// just written.)
+// Wave-wide loads straight into LDS, N times 1 KiB (1 to 4): lane l's 16 bytes
+// at base + 1024 i + 16 l, or zeros where they end past `bytes`, land at
+// lds + 1024 i + 16 l (a load's offset counts for both).  From assembly, as the
+// compiler would wait for them before every later access to LDS; wait_loads()
+// waits.  (M0 holds the LDS address and is put back, since the compiler
+// reserves it; the nops are for the hazards of M0 and of an SGPR just written.)
 typedef int i4 __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) void lds_void;
 
 __device__ __forceinline__ uint32_t lds_address(const void *p) { return (uint32_t)(uintptr_t)(lds_void *)p; }
 
-__device__ __forceinline__ void load_to_lds(const char *base, uint32_t bytes, uint32_t lds, uint32_t voff) {
+template <int N>
+__device__ __forceinline__ void load_to_lds(const char *base, uint32_t bytes, uint32_t lds, uint32_t lane16) {
+    static_assert(N >= 1 && N <= 4, "an offset has 12 bits");
     const i4 d = {__builtin_amdgcn_readfirstlane((int)(uint32_t)(uint64_t)base),
                   __builtin_amdgcn_readfirstlane((int)((uint32_t)((uint64_t)base >> 32) & 0xFFFFu)),
                   __builtin_amdgcn_readfirstlane((int)bytes), 0x00020000};
     const uint32_t m0 = __builtin_amdgcn_readfirstlane((int)lds);
     uint32_t saved;
-    asm volatile(
-        "s_mov_b32 %0, m0\n\ts_mov_b32 m0, %1\n\ts_nop 4\n\t"
-        "buffer_load_dwordx4 %2, %3, 0 offen lds\n\ts_nop 0\n\ts_mov_b32 m0, %0"
-        : "=&s"(saved)
-        : "s"(m0), "v"(voff), "s"(d)
-        : "memory");
+#define TKV_LOADS(more)                                                     \
+    asm volatile("s_mov_b32 %0, m0\n\ts_mov_b32 m0, %1\n\ts_nop 4\n\t"      \
+                 "buffer_load_dwordx4 %2, %3, 0 offen lds\n\t" more         \
+                 "s_nop 0\n\ts_mov_b32 m0, %0"                              \
+                 : "=&s"(saved)                                             \
+                 : "s"(m0), "v"(lane16), "s"(d)                             \
+                 : "memory")
+    if constexpr (N == 1)
+        TKV_LOADS("");
+    else if constexpr (N == 2)
+        TKV_LOADS("buffer_load_dwordx4 %2, %3, 0 offen offset:1024 lds\n\t");
+    else if constexpr (N == 3)
+        TKV_LOADS("buffer_load_dwordx4 %2, %3, 0 offen offset:1024 lds\n\t"
+                  "buffer_load_dwordx4 %2, %3, 0 offen offset:2048 lds\n\t");
+    else
+        TKV_LOADS("buffer_load_dwordx4 %2, %3, 0 offen offset:1024 lds\n\t"
+                  "buffer_load_dwordx4 %2, %3, 0 offen offset:2048 lds\n\t"
+                  "buffer_load_dwordx4 %2, %3, 0 offen offset:3072 lds\n\t");
+#undef TKV_LOADS
+}
+
+// The same for up to 12 KiB.
+template <int N>
+__device__ __forceinline__ void load_run_to_lds(const char *base, uint32_t bytes, uint32_t lds, uint32_t lane16) {
+    load_to_lds<(N < 4 ? N : 4)>(base, bytes, lds, lane16);
+    if constexpr (N > 4) load_run_to_lds<N - 4>(base + 4096, bytes ? bytes - 4096 : 0, lds + 4096, lane16);
 }
 
 // At most N of this wave's loads and stores are on their way: they end in the
