@@ -7,7 +7,9 @@
 // with a histogram in LDS.  A last pass writes the kept positions in order:
 // each wave owns a run of positions, counts its keys above and equal to that
 // key, and takes its places from the other waves' counts; of the equal keys
-// the lowest positions stay.
+// the lowest positions stay.  The scores are read once, 16 bytes a lane, and
+// stay in registers as far as kHeld for a lane go (32768 positions); only a
+// longer row is read anew in each pass.
 //
 // Moving.  One wave takes one record of the destination.  K words and pairs
 // move as they are, 16 bytes a lane; a V word is put together from 8 nibbles
@@ -19,6 +21,7 @@ namespace tkv {
 constexpr int kSelectThreads = 1024;
 constexpr int kSelectWaves = kSelectThreads / 64;
 constexpr int kBins = 2048;
+constexpr int kHeld = 8;  // rows of 4 scores that a lane holds
 constexpr int kEvictWaves = 4;
 
 __device__ __forceinline__ uint32_t key_of(float f) {
@@ -40,6 +43,55 @@ __device__ __forceinline__ int evict_len(const EvictArgs &a, int seq) {
     return (int64_t)l < width ? l : (int)width;
 }
 
+// The candidates as the waves own them: wave w has positions w * run .., row r
+// of its run is 256 of them, 4 in a lane.  HELD rows stay in registers; with
+// HELD 0 every pass reads them.
+template <int HELD>
+struct Scores {
+    const float *from;
+    int run, count, base, lane;
+    bool wide;
+    float held[HELD ? HELD : 1][4];
+    __device__ __forceinline__ Scores(const float *scores, int n, int wave, int lane_) {
+        from = scores;
+        count = n;
+        lane = lane_;
+        run = ((n + kSelectWaves - 1) / kSelectWaves + 255) & ~255;
+        base = wave * run;
+        wide = ((uintptr_t)scores & 15) == 0;
+#pragma unroll
+        for (int r = 0; r < HELD; ++r)
+            if (r * 256 < run) read(r, held[r]);
+    }
+    __device__ __forceinline__ int at(int r) const { return base + 256 * r + 4 * lane; }
+    __device__ __forceinline__ void read(int r, float (&x)[4]) const {
+        const int i = at(r);
+        if (wide && i + 4 <= count) {
+            const float4 v = *reinterpret_cast<const float4 *>(from + i);
+            x[0] = v.x, x[1] = v.y, x[2] = v.z, x[3] = v.w;
+        } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) x[e] = i + e < count ? from[i + e] : 0.0f;
+        }
+    }
+    // f(position of x[0], x, how many of the 4 are there), in order
+    template <class Fn>
+    __device__ __forceinline__ void each(Fn f) const {
+        if constexpr (HELD > 0) {
+#pragma unroll
+            for (int r = 0; r < HELD; ++r)
+                if (r * 256 < run) f(at(r), held[r], count - at(r));
+        } else {
+            for (int r = 0; r * 256 < run; ++r) {
+                float x[4];
+                read(r, x);
+                f(at(r), x, count - at(r));
+            }
+        }
+    }
+};
+
+template <int HELD>
 __global__ void __launch_bounds__(kSelectThreads) select_kernel(const EvictArgs a) {
     __shared__ uint32_t bins[kBins];
     __shared__ uint32_t found[2];  // digit, and how many are still wanted below it
@@ -59,55 +111,69 @@ __global__ void __launch_bounds__(kSelectThreads) select_kernel(const EvictArgs 
         return;
     }
     const int recent = a.recent < a.budget ? a.recent : a.budget;
-    const int old = len - recent;               // candidates
+    const int old = len - recent;                   // candidates
     uint32_t want = (uint32_t)(a.budget - recent);  // of which so many stay; want < old
+    for (int i = tid; i < recent; i += kSelectThreads) {
+        kept[a.budget - recent + i] = old + i;
+        scores_out[a.budget - recent + i] = scores[old + i];
+    }
+    if (want == 0) return;
+    const Scores<HELD> mine(scores, old, wave, lane);
     uint32_t prefix = 0, prefix_mask = 0;
-    if (want > 0) {
-        for (int pass = 0; pass < 3; ++pass) {
-            const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
-            const uint32_t digit_mask = pass == 2 ? 1023u : 2047u;
-            for (int i = tid; i < kBins; i += kSelectThreads) bins[i] = 0;
-            __syncthreads();
-            for (int i = tid; i < old; i += kSelectThreads) {
-                const uint32_t key = key_of(scores[i]);
-                if ((key & prefix_mask) == prefix) atomicAdd(&bins[(key >> shift) & digit_mask], 1u);
+    for (int pass = 0; pass < 3; ++pass) {
+        const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
+        const uint32_t digit_mask = pass == 2 ? 1023u : 2047u;
+        for (int i = tid; i < kBins; i += kSelectThreads) bins[i] = 0;
+        __syncthreads();
+        mine.each([&](int, const float (&x)[4], int there) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const uint32_t key = key_of(x[e]);
+                if (e < there && (key & prefix_mask) == prefix) atomicAdd(&bins[(key >> shift) & digit_mask], 1u);
             }
-            __syncthreads();
-            if (wave == 0) {
-                // lane i owns bins 32 i .. 32 i + 31; from the top
-                uint32_t mine = 0;
-                for (int j = 0; j < kBins / 64; ++j) mine += bins[lane * (kBins / 64) + ((j + lane) & 31)];
-                uint32_t above = mine;  // inclusive sum from this lane up
-                for (int d = 1; d < 64; d <<= 1) {
-                    const uint32_t y = __shfl_down(above, d);
-                    if (lane + d < 64) above += y;
-                }
-                above -= mine;
-                if (above < want && above + mine >= want) {
-                    uint32_t left = want - above;
-                    int j = kBins / 64 - 1;
-                    while (j > 0 && bins[lane * (kBins / 64) + j] < left) left -= bins[lane * (kBins / 64) + j], --j;
-                    found[0] = lane * (kBins / 64) + j;
-                    found[1] = left;
-                }
+        });
+        __syncthreads();
+        if (wave == 0) {
+            // lane i owns bins 32 i .. 32 i + 31; from the top
+            uint32_t own = 0;
+#pragma unroll
+            for (int j = 0; j < kBins / 64; ++j) own += bins[lane * (kBins / 64) + ((j + lane) & 31)];
+            uint32_t above = own;  // inclusive sum from this lane up
+            for (int d = 1; d < 64; d <<= 1) {
+                const uint32_t y = __shfl_down(above, d);
+                if (lane + d < 64) above += y;
             }
-            __syncthreads();
-            prefix |= found[0] << shift;
-            prefix_mask |= digit_mask << shift;
-            want = found[1];
+            above -= own;
+            // the lane whose bins hold the last one wanted, and then its bin, again by sums from the top
+            const bool here = above < want && above + own >= want;
+            const int who = __ffsll((long long)__ballot(here)) - 1;
+            const uint32_t left = want - __shfl(above, who);
+            const uint32_t bin = lane < 32 ? bins[who * 32 + lane] : 0;
+            uint32_t sum = bin;
+            for (int d = 1; d < 32; d <<= 1) {
+                const uint32_t y = __shfl_down(sum, d);
+                if (lane + d < 32) sum += y;
+            }
+            if (lane < 32 && sum - bin < left && sum >= left) {
+                found[0] = who * 32 + lane;
+                found[1] = left - (sum - bin);
+            }
         }
+        __syncthreads();
+        prefix |= found[0] << shift;
+        prefix_mask |= digit_mask << shift;
+        want = found[1];
     }
     // keys above `prefix` stay, and the first `want` of those equal to it
-    const bool any = a.budget > recent;
-    const int run = ((old + kSelectWaves - 1) / kSelectWaves + 63) & ~63;
-    const int from = wave * run, to = from + run < old ? from + run : old;
     int above = 0, equal = 0;
-    if (any)
-        for (int i = from; i < to; i += 64) {
-            const uint32_t key = i + lane < to ? key_of(scores[i + lane]) : 0;
-            above += __popcll(__ballot(i + lane < to && key > prefix));
-            equal += __popcll(__ballot(i + lane < to && key == prefix));
+    mine.each([&](int, const float (&x)[4], int there) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const uint32_t key = key_of(x[e]);
+            above += __popcll(__ballot(e < there && key > prefix));
+            equal += __popcll(__ballot(e < there && key == prefix));
         }
+    });
     if (lane == 0) count_above[wave] = above, count_equal[wave] = equal;
     __syncthreads();
     int out = 0, equal_before = 0;
@@ -116,26 +182,37 @@ __global__ void __launch_bounds__(kSelectThreads) select_kernel(const EvictArgs 
         out += count_above[w] + (count_equal[w] < left ? count_equal[w] : left > 0 ? left : 0);
         equal_before += count_equal[w];
     }
-    if (any)
-        for (int i = from; i < to; i += 64) {
-            const bool in = i + lane < to;
-            const float s = in ? scores[i + lane] : 0.0f;
-            const uint32_t key = key_of(s);
-            const uint64_t same = __ballot(in && key == prefix);
-            const bool stay = in && (key > prefix || (key == prefix && equal_before + below(same) < (int)want));
-            const uint64_t all = __ballot(stay);
-            if (stay) {
-                const int at = out + below(all);
-                kept[at] = i + lane;
-                scores_out[at] = s;
-            }
-            out += __popcll(all);
-            equal_before += __popcll(same);
+    mine.each([&](int i, const float (&x)[4], int there) {
+        uint32_t key[4];
+        int before = equal_before, all_equal = 0;
+        uint64_t same[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            key[e] = key_of(x[e]);
+            same[e] = __ballot(e < there && key[e] == prefix);
+            before += below(same[e]);  // equal ones of lower lanes
+            all_equal += __popcll(same[e]);
         }
-    for (int i = tid; i < recent; i += kSelectThreads) {
-        kept[a.budget - recent + i] = old + i;
-        scores_out[a.budget - recent + i] = scores[old + i];
-    }
+        bool stay[4];
+        int at = out;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const bool equal_here = e < there && key[e] == prefix;
+            stay[e] = (e < there && key[e] > prefix) || (equal_here && before < (int)want);
+            before += equal_here;
+            const uint64_t staying = __ballot(stay[e]);
+            at += below(staying);
+            out += __popcll(staying);
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            if (stay[e]) {
+                kept[at] = i + e;
+                scores_out[at] = x[e];
+                ++at;
+            }
+        equal_before += all_equal;
+    });
 }
 
 template <int D, int GROUP>
@@ -234,7 +311,15 @@ static int launch_moves(const EvictArgs &a, void *stream) {
 }
 
 int launch_evict(const EvictArgs &a, void *stream) {
-    select_kernel<<<dim3((uint32_t)(a.b.n_seq * (int64_t)a.c.heads)), dim3(kSelectThreads), 0, (hipStream_t)stream>>>(a);
+    const dim3 grid((uint32_t)(a.b.n_seq * (int64_t)a.c.heads)), block(kSelectThreads);
+    hipStream_t s = (hipStream_t)stream;
+    constexpr int kRow = 256 * kSelectWaves;  // positions of a row of every wave
+    if (a.max_len <= kRow)
+        select_kernel<1><<<grid, block, 0, s>>>(a);
+    else if (a.max_len <= kHeld * kRow)
+        select_kernel<kHeld><<<grid, block, 0, s>>>(a);
+    else
+        select_kernel<0><<<grid, block, 0, s>>>(a);
     const int rc = (int)hipGetLastError();
     if (rc) return rc;
     switch (a.c.dim * 1000 + a.c.group) {

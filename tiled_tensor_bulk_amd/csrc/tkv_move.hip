@@ -16,22 +16,41 @@
 namespace tkv {
 
 constexpr int kMoveWaves = 4;
+constexpr int kFewTokens = 4;
 
-// Nearest whole number to (x - z) / s, ties to even.  The quotient in fp32 is
-// within 1e-5 of the true one, so only one that close to a border needs the
-// exact comparison, in fp64, where products of an fp16 number and a small
-// integer, and differences of fp16 and bf16 numbers, are exact.
-__device__ __forceinline__ int code_of(float x, float z, float s, float inv) {
-    const float t = (x - z) * inv;
-    float c = rintf(t);
-    const float low = floorf(t);
-    if (fabsf(t - low - 0.5f) < 1e-4f && t > 0.0f && t < 15.0f) {
-        const double twice = 2.0 * ((double)x - (double)z);
-        const double border = (2.0 * (double)low + 1.0) * (double)s;
-        const int k = (int)low;
-        c = (float)(twice > border ? k + 1 : twice < border ? k : k + (k & 1));
+// Nearest whole numbers to (x - z) / s within 0..15, ties to even.  The
+// quotient in fp32 is within 1e-5 of the true one, so only one that close to a
+// border needs the exact comparison, in fp64, where products of an fp16 number
+// and a small integer, and differences of fp16 and bf16 numbers, are exact; a
+// lane goes there when one of its N is.
+template <int N>
+__device__ __forceinline__ void codes_of(const float *x, float z, float s, uint8_t *code) {
+    const float inv = s > 0.0f ? 1.0f / s : 0.0f;
+    float c[N], off = 0.0f;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        const float t = (x[i] - z) * inv;
+        c[i] = rintf(t);
+        off = fmaxf(off, fabsf(t - c[i]));
     }
-    return (int)fminf(fmaxf(c, 0.0f), 15.0f);
+    if (off > 0.4999f) {
+        for (int i = 0; i < N; ++i) {
+            const float t = (x[i] - z) * inv, low = floorf(t);
+            if (fabsf(t - low - 0.5f) < 1e-4f && t > 0.0f && t < 15.0f) {
+                const double twice = 2.0 * ((double)x[i] - (double)z);
+                const double border = (2.0 * (double)low + 1.0) * (double)s;
+                const int k = (int)low;
+                c[i] = (float)(twice > border ? k + 1 : twice < border ? k : k + (k & 1));
+            }
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < N; ++i) code[i] = (uint8_t)fminf(fmaxf(c[i], 0.0f), 15.0f);
+}
+
+__device__ __forceinline__ void scale_of(float lo, float hi, _Float16 &scale, _Float16 &zero) {
+    scale = (_Float16)((hi - lo) / 15.0f);
+    zero = (_Float16)lo;
 }
 
 // Quantise one position's channels: lane group g holds channels 32 i + 8 g + j
@@ -50,14 +69,14 @@ __device__ __forceinline__ void quantise(const float *x, _Float16 *scale, _Float
             lo = fminf(lo, __shfl_xor(lo, mask));
             hi = fmaxf(hi, __shfl_xor(hi, mask));
         }
-        const _Float16 s16 = (_Float16)((hi - lo) / 15.0f), z16 = (_Float16)lo;
-        const float s = (float)s16, z = (float)z16, inv = s > 0.0f ? 1.0f / s : 0.0f;
-        scale[grp] = s16;
-        zero[grp] = z16;
+        scale_of(lo, hi, scale[grp], zero[grp]);
 #pragma unroll
-        for (int i = 0; i < F::KG * 8; ++i) code[grp * F::KG * 8 + i] = (uint8_t)code_of(y[i], z, s, inv);
+        for (int i = 0; i < F::KG; ++i)
+            codes_of<8>(y + 8 * i, (float)zero[grp], (float)scale[grp], code + (grp * F::KG + i) * 8);
     }
 }
+
+__device__ __forceinline__ float limited(float y) { return y != y ? 0.0f : fminf(fmaxf(y, -kLimit), kLimit); }
 
 template <int D>
 __device__ __forceinline__ void load_row(const Tokens &t, int64_t row, int head, int g, float *x) {
@@ -66,10 +85,7 @@ __device__ __forceinline__ void load_row(const Tokens &t, int64_t row, int head,
     for (int i = 0; i < D / 32; ++i) {
         load8(t, at + 32 * i, x + 8 * i);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const float y = x[8 * i + j];
-            x[8 * i + j] = y != y ? 0.0f : fminf(fmaxf(y, -kLimit), kLimit);
-        }
+        for (int j = 0; j < 8; ++j) x[8 * i + j] = limited(x[8 * i + j]);
     }
 }
 
@@ -181,11 +197,94 @@ __global__ void __launch_bounds__(64 * kMoveWaves) append_kernel(const MoveArgs 
     }
 }
 
+// A few new tokens: a wave takes their positions in its record one by one, with
+// all lanes on one position, E channels each, as a step of decoding has a
+// token or so for each sequence and latency is what counts: 32 sequences of 8
+// heads, one token each, in 17 us with four lanes on a position.
+template <int D, int GROUP>
+__global__ void __launch_bounds__(64 * kMoveWaves) append_few_kernel(const MoveArgs a) {
+    using F = Format<D, GROUP>;
+    constexpr int E = D <= 128 ? 2 : 4;
+    const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+    Unit u;
+    if (!unit_of(a, blockIdx.x * kMoveWaves + wave, u) || !u.rec) return;
+    const int ch = E * lane;
+    if (ch >= D) return;
+    const int p0 = u.tile * kTile;
+    const int from = u.first > p0 ? u.first : p0;
+    const int to = u.first + u.n < p0 + kTile ? u.first + u.n : p0 + kTile;
+    const int grp = ch / GROUP;
+    // this lane's part of a K word, whose first lane stores it
+    const int i = ch / 32, kg = ch % 32 / 8, j = ch % 8;
+    for (int pos = from; pos < to; ++pos) {
+        const int t = pos & (kTile - 1), half = t >> 4, m = t & 15;
+        const int64_t row = u.start + (pos - u.first);
+        const int64_t ka = row * a.k.token_stride + u.head * a.k.head_stride + ch;
+        const int64_t va = row * a.v.token_stride + u.head * a.v.head_stride + ch;
+        float x[2][E];
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+            x[0][e] = limited(elem_to_float(((const uint16_t *)a.k.data)[ka + e], a.k.type));
+            x[1][e] = limited(elem_to_float(((const uint16_t *)a.v.data)[va + e], a.v.type));
+        }
+        // a V code is half a byte of its word; the other half may be another position's
+        const int nibble = nibble_of((t & 3) + 4 * half);
+        uint8_t *byte[E], old[E];
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+            const int chunk = (ch + e) / 16;
+            byte[e] = (uint8_t *)u.rec + F::VC + nibble / 2 +
+                      (((chunk / F::WV) * 64 + 16 * (m >> 2) + (ch + e) % 16) * F::WV + chunk % F::WV) * 4;
+            old[e] = *byte[e];
+        }
+        float lo[2], hi[2];
+        _Float16 scale[2], zero[2];
+        uint8_t code[2][E];
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+            lo[s] = hi[s] = x[s][0];
+#pragma unroll
+            for (int e = 1; e < E; ++e) lo[s] = fminf(lo[s], x[s][e]), hi[s] = fmaxf(hi[s], x[s][e]);
+        }
+#pragma unroll
+        for (int mask = 1; mask < GROUP / E; mask <<= 1)
+#pragma unroll
+            for (int s = 0; s < 2; ++s) {
+                lo[s] = fminf(lo[s], __shfl_xor(lo[s], mask));
+                hi[s] = fmaxf(hi[s], __shfl_xor(hi[s], mask));
+            }
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+            scale_of(lo[s], hi[s], scale[s], zero[s]);
+            codes_of<E>(x[s], (float)zero[s], (float)scale[s], code[s]);
+        }
+        uint32_t word = 0;
+#pragma unroll
+        for (int e = 0; e < E; ++e) word |= (uint32_t)code[0][e] << (4 * nibble_of(j + e));
+#pragma unroll
+        for (int mask = 1; mask < 8 / E; mask <<= 1) word |= __shfl_xor(word, mask);
+        if (j == 0)
+            *reinterpret_cast<uint32_t *>(u.rec + (((half * F::S + i / F::WV) * 64 + 16 * kg + m) * F::WV + i % F::WV) * 4) = word;
+        const int shift = 4 * (nibble & 1);
+#pragma unroll
+        for (int e = 0; e < E; ++e) *byte[e] = (uint8_t)((old[e] & (0xF0 >> shift)) | (code[1][e] << shift));
+        if (ch % GROUP == 0) {
+            *reinterpret_cast<h2 *>(u.rec + F::KP + (grp * kTile + t) * 4) = (h2){scale[0], zero[0]};
+            _Float16 *v = reinterpret_cast<_Float16 *>(u.rec + F::VP) + grp * 64 + 8 * (m >> 2) + 4 * half + (m & 3);
+            v[0] = scale[1], v[32] = zero[1];
+        }
+    }
+}
+
+// Positions out of the cache: V codes through LDS as above; then a lane takes 8
+// channels of a position, neighbouring lanes the next 8, so that a position's
+// row is written in one run.
 template <int D, int GROUP>
 __global__ void __launch_bounds__(64 * kMoveWaves) read_kernel(const MoveArgs a) {
     using F = Format<D, GROUP>;
-    constexpr int PITCH = D + 4;
-    __shared__ uint8_t codes[kMoveWaves][kTile * PITCH];
+    constexpr int PITCH = D + 8;
+    constexpr int LANES = D / 8, AT_ONCE = 64 / LANES;  // of a position, and positions
+    __shared__ __attribute__((aligned(8))) uint8_t codes[kMoveWaves][kTile * PITCH];
     const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, g = lane >> 4, m = lane & 15;
     Unit u;
     if (!unit_of(a, blockIdx.x * kMoveWaves + wave, u)) return;
@@ -207,41 +306,43 @@ __global__ void __launch_bounds__(64 * kMoveWaves) read_kernel(const MoveArgs a)
     __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
     __builtin_amdgcn_wave_barrier();
     __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+    const int which = lane / LANES, ch = 8 * (lane % LANES), grp = ch / GROUP, i = ch / 32, kg = ch % 32 / 8;
+    if (which >= AT_ONCE) return;
+    // all that is read first: no step waits for another's
+    constexpr int STEPS = (kTile + AT_ONCE - 1) / AT_ONCE;
+    uint32_t word[STEPS];
+    h2 kp[STEPS], vp[STEPS];
+    if (u.rec) {
 #pragma unroll
-    for (int half = 0; half < 2; ++half) {
-        const int i = p0 + 16 * half + m - u.first;
-        if (i < 0 || i >= u.n) continue;
-        uint32_t word[F::W];
+        for (int step = 0; step < STEPS; ++step) {
+            const int t = (step * AT_ONCE + which) & (kTile - 1), half = t >> 4, mt = t & 15;
+            word[step] = *reinterpret_cast<const uint32_t *>(
+                u.rec + (((half * F::S + i / F::WV) * 64 + 16 * kg + mt) * F::WV + i % F::WV) * 4);
+            kp[step] = *reinterpret_cast<const h2 *>(u.rec + F::KP + (grp * kTile + t) * 4);
+            const _Float16 *v = reinterpret_cast<const _Float16 *>(u.rec + F::VP) + grp * 64 + 8 * (mt >> 2) + 4 * half + (mt & 3);
+            vp[step] = (h2){v[0], v[32]};
+        }
+    }
+#pragma unroll
+    for (int step = 0; step < STEPS; ++step) {
+        const int t = step * AT_ONCE + which, n = p0 + t - u.first;
+        if (t >= kTile || n < 0 || n >= u.n) continue;
+        float x[8], y[8];
         if (u.rec) {
+            const float ks = (float)kp[step][0], kz = (float)kp[step][1], vs = (float)vp[step][0], vz = (float)vp[step][1];
+            const uint2 c = *reinterpret_cast<const uint2 *>(mine + t * PITCH + ch);
 #pragma unroll
-            for (int s = 0; s < F::S; ++s)
-                load_words<F::WV>(u.rec + (((half * F::S + s) * 64 + lane) * F::WV) * 4, word + s * F::WV);
-        }
-        const int slot = 8 * (m >> 2) + 4 * half + (m & 3);
-#pragma unroll
-        for (int w = 0; w < F::W; ++w) {
-            const int grp = w / F::KG;
-            float x[8], y[8];
-            if (u.rec) {
-                const h2 kp = *reinterpret_cast<const h2 *>(u.rec + F::KP + (grp * kTile + 16 * half + m) * 4);
-                const _Float16 *vp = reinterpret_cast<const _Float16 *>(u.rec + F::VP) + grp * 64 + slot;
-                const float ks = (float)kp[0], kz = (float)kp[1], vs = (float)vp[0], vz = (float)vp[32];
-                const uint32_t *from =
-                    reinterpret_cast<const uint32_t *>(mine + (16 * half + m) * PITCH + 32 * w + 8 * g);
-                const uint32_t c[2] = {from[0], from[1]};
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    x[j] = ks * (float)((word[w] >> (4 * nibble_of(j))) & 15) + kz;
-                    y[j] = vs * (float)((c[j >> 2] >> (8 * (j & 3))) & 255) + vz;
-                }
-            } else {
-#pragma unroll
-                for (int j = 0; j < 8; ++j) x[j] = y[j] = 0.0f;
+            for (int j = 0; j < 8; ++j) {
+                x[j] = fmaf(ks, (float)((word[step] >> (4 * nibble_of(j))) & 15), kz);
+                y[j] = fmaf(vs, (float)(((j < 4 ? c.x : c.y) >> (8 * (j & 3))) & 255), vz);
             }
-            const int64_t row = u.start + i;
-            store8(a.k, row * a.k.token_stride + u.head * a.k.head_stride + 32 * w + 8 * g, x);
-            store8(a.v, row * a.v.token_stride + u.head * a.v.head_stride + 32 * w + 8 * g, y);
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) x[j] = y[j] = 0.0f;
         }
+        const int64_t row = u.start + n;
+        store8(a.k, row * a.k.token_stride + u.head * a.k.head_stride + ch, x);
+        store8(a.v, row * a.v.token_stride + u.head * a.v.head_stride + ch, y);
     }
 }
 
@@ -249,7 +350,9 @@ template <int D, int GROUP>
 static int launch_move(const MoveArgs &a, bool append, void *stream) {
     const int64_t units = (int64_t)a.b.n_seq * a.tiles * a.c.heads;
     const dim3 grid((uint32_t)((units + kMoveWaves - 1) / kMoveWaves)), block(64 * kMoveWaves);
-    if (append)
+    if (append && a.b.max_new <= kFewTokens)
+        append_few_kernel<D, GROUP><<<grid, block, 0, (hipStream_t)stream>>>(a);
+    else if (append)
         append_kernel<D, GROUP><<<grid, block, 0, (hipStream_t)stream>>>(a);
     else
         read_kernel<D, GROUP><<<grid, block, 0, (hipStream_t)stream>>>(a);
