@@ -68,12 +68,9 @@ struct Extent {
     int64_t start;  // first row of its tokens
     int n, len, rows;
     __device__ __forceinline__ Extent(const AttendArgs &a, int seq) {
+        const int l = a.b.lens[seq];
         new_tokens(a.b, seq, start, n);
-        const int64_t width = (int64_t)a.b.table_width << a.c.page_shift;
-        int l = a.b.lens[seq];
-        l = l < 0 ? 0 : l;
-        l = l < a.max_len ? l : a.max_len;
-        len = (int64_t)l < width ? l : (int)width;
+        len = l < 0 ? 0 : l < a.max_len ? l : a.max_len;  // max_len is at most what the table holds
         rows = n * a.group_heads;
     }
     // positions below this are seen by the i-th new token
@@ -86,9 +83,20 @@ struct Chunks {
     int size, n;
     __device__ __forceinline__ Chunks(const AttendArgs &a, int len) {
         constexpr int kStep = kTile * kAttendWaves;
-        const int parts = (len + a.chunk - 1) / a.chunk;
-        size = parts > 1 ? ((len + parts - 1) / parts + kStep - 1) / kStep * kStep : a.chunk;
-        n = len > 0 ? (len + size - 1) / size : 1;
+        const int steps = (len + kStep - 1) / kStep;
+        int each = (1 << a.chunk_shift) / kStep, parts = (len + (1 << a.chunk_shift) - 1) >> a.chunk_shift;
+        if (parts > 1) {
+            each = over(steps, parts);
+            parts = over(steps, each);
+        }
+        size = each * kStep;
+        n = parts > 1 ? parts : 1;
+    }
+    // p / q rounded up, of numbers below 2^24: the quotient in fp32 is one off at most
+    static __device__ __forceinline__ int over(int p, int q) {
+        int r = (int)((float)p * __builtin_amdgcn_rcpf((float)q));
+        r -= (r - 1) * q >= p ? 1 : 0;
+        return r + (r * q < p ? 1 : 0);
     }
 };
 
@@ -170,12 +178,13 @@ __device__ __forceinline__ float over_rows_sum(float v) {  // over 16 neighbouri
 __device__ __forceinline__ void write_row(const AttendArgs &a, const Extent &e, int seq, int head, int row, int channel,
                                           f4 y, float best, float sum) {
     const float inv = sum > 0.0f || sum != sum ? 1.0f / sum : 0.0f;
-    const int i = row / a.group_heads, hq = head * a.group_heads + row % a.group_heads;
+    int rest = row;
+    const int i = divide(rest, a.group_heads, a.by_group_heads), hq = head * a.group_heads + rest;
     store4(a.out, (e.start + i) * a.out.token_stride + hq * a.out.head_stride + channel, y * inv);
     if (channel == 0) {
         const float log_sum = best - kLift + log2f(sum);  // log2(0) = -inf: nothing seen
         a.lse[(e.start + i) * (a.c.heads * a.group_heads) + hq] = log_sum * 0.69314718056f;
-        if (a.frag_q && (sum > 0.0f || sum != sum)) {
+        if (a.row_info && (sum > 0.0f || sum != sum)) {
             const int64_t tile = ((int64_t)seq * a.c.heads + head) * a.row_tiles + row / 16;
             a.row_info[(tile * 16 + row % 16) * 2 + 1] = log_sum;
         }
@@ -189,7 +198,7 @@ struct Row {
     uint4 raw[D / 32];
     __device__ __forceinline__ void load(const AttendArgs &a, const Extent &e, int head, int r, int g, bool live) {
         r = live ? r : 0;  // the first row is read for one that is not there, and dropped
-        const int i = r / a.group_heads, hq = head * a.group_heads + r - i * a.group_heads;
+        const int i = divide(r, a.group_heads, a.by_group_heads), hq = head * a.group_heads + r;
         const int64_t row = (e.start + i) * a.q.token_stride + hq * a.q.head_stride + 8 * g;
 #pragma unroll
         for (int c = 0; c < D / 32; ++c) raw[c] = load8_raw(a.q, row + 32 * c);
@@ -264,15 +273,17 @@ __device__ __forceinline__ float sums_factor(float factor) {
     return fminf(factor * (float)(1 << kSumBits), 0x1.fffffep127f);
 }
 
-// Where the scores kernel finds a tile of 16 rows and what belongs to it.
+// Where the scores kernels find a tile of 16 rows and what belongs to it.
 template <int D, int GROUP>
 __device__ __forceinline__ void keep_rows(const AttendArgs &a, int64_t tile, int lane, const h8 (&q)[D / 32], h8 sums,
                                           float factor) {
     using F = Format<D, GROUP>;
-    h8 *to = (h8 *)a.frag_q + tile * ((F::W + 1) * 64);
+    if (a.frag_q) {
+        h8 *to = (h8 *)a.frag_q + tile * ((F::W + 1) * 64);
 #pragma unroll
-    for (int c = 0; c < F::W; ++c) to[c * 64 + lane] = q[c];
-    to[F::W * 64 + lane] = sums;
+        for (int c = 0; c < F::W; ++c) to[c * 64 + lane] = q[c];
+        to[F::W * 64 + lane] = sums;
+    }
     // a row without positions weighs nothing: its logarithm stays at inf
     if (lane < 16) *reinterpret_cast<float2 *>(a.row_info + (tile * 16 + lane) * 2) = make_float2(factor, __builtin_inff());
 }
@@ -341,6 +352,14 @@ struct Softmax {
     }
 };
 
+// What a workgroup of the attention kernels has to do.
+__device__ __forceinline__ void place(const AttendArgs &a, int &block, int &split, int &head, int &seq) {
+    block = blockIdx.x;
+    split = divide(block, a.row_blocks, a.by_row_blocks);
+    head = divide(split, a.n_split, a.by_split);
+    seq = divide(head, (int)a.c.heads, a.by_heads);
+}
+
 // Few rows: the four waves share them and take every fourth record.  A wave
 // has a ring of two records in LDS, which its loads fill without passing
 // through registers: while it works on one, the other is on its way, and the
@@ -370,12 +389,8 @@ __global__ void __launch_bounds__(64 * kAttendWaves, (FewRows<D, GROUP, NT>::kWa
 
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int lane = threadIdx.x & 63, g = lane >> 4, n = lane & 15;
-    int at = blockIdx.x;
-    const int block = at % a.row_blocks;
-    at /= a.row_blocks;
-    const int split = at % a.n_split;
-    at /= a.n_split;
-    const int head = at % (int)a.c.heads, seq = at / (int)a.c.heads;
+    int block, split, head, seq;
+    place(a, block, split, head, seq);
     const int shift = a.c.page_shift;
     const int32_t *table = a.b.table + seq * a.b.table_stride;
     const Extent e(a, seq);
@@ -387,8 +402,8 @@ __global__ void __launch_bounds__(64 * kAttendWaves, (FewRows<D, GROUP, NT>::kWa
     pages.load(a, table, t0 >> shift, lane);
 
     const int rows_here = e.rows - r0 < R ? e.rows - r0 : R;
-    const int all_see = e.limit(a, r0 / a.group_heads);                  // below this no row is masked
-    int end = e.limit(a, (r0 + rows_here - 1) / a.group_heads);          // at this and above every row is
+    const int all_see = e.limit(a, divided(r0, a.by_group_heads));                  // below this no row is masked
+    int end = e.limit(a, divided(r0 + rows_here - 1, a.by_group_heads));            // at this and above every row is
     end = end < t0 + chunks.size ? end : t0 + chunks.size;
 
     Row<D, GROUP> raw[NT];
@@ -420,7 +435,7 @@ __global__ void __launch_bounds__(64 * kAttendWaves, (FewRows<D, GROUP, NT>::kWa
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
         const int r = r0 + 16 * nt + n;
-        limit[nt] = r < e.rows ? e.limit(a, r / a.group_heads) : 0;
+        limit[nt] = r < e.rows ? e.limit(a, divided(r, a.by_group_heads)) : 0;
         raw[nt].template operand<BF16>(a, q[nt], qsum[nt], factor[nt]);
 #pragma unroll
         for (int grp = 0; grp < F::NG; ++grp) {
@@ -428,7 +443,7 @@ __global__ void __launch_bounds__(64 * kAttendWaves, (FewRows<D, GROUP, NT>::kWa
             first[nt][grp] = (f4){f, f, f, f};
         }
         s[nt].clear();
-        if (a.frag_q && split == 0 && wave == 0 && r0 / 16 + nt < a.row_tiles)
+        if (a.row_info && split == 0 && wave == 0 && r0 / 16 + nt < a.row_tiles)
             keep_rows<D, GROUP>(a, ((int64_t)seq * a.c.heads + head) * a.row_tiles + r0 / 16 + nt, lane, q[nt],
                                 sum_parts<D, GROUP>(qsum[nt], g), sums_factor(factor[nt]));
     }
@@ -452,6 +467,14 @@ __global__ void __launch_bounds__(64 * kAttendWaves, (FewRows<D, GROUP, NT>::kWa
                 for (int nt = 0; nt < NT; ++nt)
                     if (pos >= limit[nt] || gone) x[nt][j] = -__builtin_inff();
             }
+        }
+        if (NT == 1 && a.logits && n < a.rows) {
+            float *to = a.logits + (((int64_t)(seq * (int)a.c.heads + head) * ((a.max_len + kTile - 1) / kTile) + p0 / kTile) *
+                                        a.rows + n) * kTile + 4 * g;
+#pragma unroll
+            for (int half = 0; half < 2; ++half)
+                *reinterpret_cast<f4 *>(to + 16 * half) = (f4){x[0][4 * half], x[0][4 * half + 1], x[0][4 * half + 2],
+                                                              x[0][4 * half + 3]} * factor[0];
         }
         bool grown = false;
         float top[NT];

@@ -99,19 +99,27 @@ __device__ __forceinline__ h8 codes_plus(uint32_t w) {
 // The nibble of code j in its word.
 __device__ __forceinline__ constexpr int nibble_of(int j) { return (j >> 1) + 4 * (j & 1); }
 
-// New tokens of sequence b: their first row and their number.
+__device__ __forceinline__ int divided(int n, Divisor d) {
+    return (int)(((uint64_t)(uint32_t)n * d.mul) >> (31 + d.shift));
+}
+// n / d, and n becomes the rest
+__device__ __forceinline__ int divide(int &n, int d, Divisor by) {
+    const int q = divided(n, by);
+    n -= q * d;
+    return q;
+}
+
+// New tokens of sequence b: their first row and their number.  Without a
+// branch, so that what it reads comes with what others read.
 __device__ __forceinline__ void new_tokens(const Batch &b, int seq, int64_t &start, int &n) {
-    if (b.starts) {
-        const int64_t s = b.starts[seq], e = b.starts[seq + 1];
-        start = s;
-        int64_t m = e - s;
-        // rows outside the token tensors do not exist, whatever starts says
-        if (s < 0 || m < 0 || e > b.n_tokens) m = 0, start = 0;
-        n = (int)(m < b.max_new ? m : b.max_new);
-    } else {
-        start = (int64_t)seq * b.uniform;
-        n = b.uniform < b.max_new ? b.uniform : b.max_new;
-    }
+    const int32_t *from = b.starts ? b.starts + seq : b.lens;
+    const int64_t s = from[0], e = from[b.starts ? 1 : 0];
+    int64_t m = e - s;
+    start = s;
+    // rows outside the token tensors do not exist, whatever starts says
+    if (s < 0 || m < 0 || e > b.n_tokens) m = 0, start = 0;
+    if (!b.starts) m = b.uniform, start = (int64_t)seq * b.uniform;
+    n = (int)(m < b.max_new ? m : b.max_new);
 }
 
 // The page of a position, or -1 where there is none.

@@ -154,6 +154,13 @@ struct Split {
     uint64_t part_o, part_ml, frag_q, row_info, total;  // offsets, and bytes in all
 };
 
+tkv::Divisor divisor(uint32_t d) {
+    tkv::Divisor r{0, 0};
+    while ((1u << r.shift) < d) ++r.shift;
+    r.mul = (uint32_t)(((1ull << (31 + r.shift)) + d - 1) / d);
+    return r;
+}
+
 uint64_t up(uint64_t v, uint64_t to) { return (v + to - 1) / to * to; }
 
 // Rows of a workgroup: 16, or 32 where there are more.  Chunks: as long as
@@ -167,6 +174,11 @@ constexpr int kLeastChunk = 512;
 constexpr int kMostChunk = 1 << 16;
 constexpr int kBlocksPerCu = 8;
 constexpr int kRowBlocksPerCu = 2;
+// Scores of up to so many rows go by logarithms kept in memory, 8 bytes a row
+// and position written and read, against half of a record read again (72 bytes
+// of 128 channels): 16 sequences of up to 16384 positions, 4 rows, 112 us with
+// the second, 71 with the first.
+constexpr int kLogitRows = 8;
 
 Split plan(const Cache &c, int64_t n_seq, int64_t rows, int64_t max_len, bool scores, int cus) {
     Split s{};
@@ -188,7 +200,10 @@ Split plan(const Cache &c, int64_t n_seq, int64_t rows, int64_t max_len, bool sc
     }
     if (scores) {
         s.frag_q = s.total;
-        s.total = up(s.total + heads * s.row_tiles * (32 * c.dim + 1024), 256);
+        if (rows <= kLogitRows)
+            s.total = up(s.total + heads * up((uint64_t)max_len, tkv::kTile) * rows * 4, 256);
+        else
+            s.total = up(s.total + heads * s.row_tiles * (32 * c.dim + 1024), 256);
         s.row_info = s.total;
         s.total = up(s.total + heads * s.row_tiles * 16 * 8, 256);
     }
@@ -308,7 +323,7 @@ tmap_status tkv_attend(const tkv_cache *cache, const tkv_attend_args *args, cons
     const Split s = plan(a.c, a.b.n_seq, a.rows, a.max_len, a.scores_out, cus);
     TKV_REQUIRE((int64_t)a.b.n_seq * a.c.heads * s.n_split * s.row_blocks < kMostBlocks &&
                     (int64_t)a.b.n_seq * a.c.heads * (a.max_len / 128 + 1) < kMostBlocks &&
-                    (int64_t)a.b.n_seq * a.c.heads * a.rows < kMostBlocks,
+                    (int64_t)a.b.n_seq * a.c.heads * a.rows * (a.c.dim / 32) < kMostBlocks,
                 "too many sequences, heads and rows");
     if (s.total) {
         TKV_REQUIRE(args->workspace && aligned(args->workspace, 16), "workspace is NULL or not 16-byte aligned");
@@ -319,13 +334,21 @@ tmap_status tkv_attend(const tkv_cache *cache, const tkv_attend_args *args, cons
     a.row_blocks = s.row_blocks;
     a.row_tiles = s.row_tiles;
     a.n_split = s.n_split;
-    a.chunk = s.chunk;
+    while ((1 << a.chunk_shift) < s.chunk) ++a.chunk_shift;
+    a.by_heads = divisor(a.c.heads);
+    a.by_group_heads = divisor(a.group_heads);
+    a.by_row_blocks = divisor(a.row_blocks);
+    a.by_split = divisor(a.n_split);
+    a.by_rows = divisor(a.rows);
     if (s.n_split > 1) {
         a.part_o = (float *)(ws + s.part_o);
         a.part_ml = (float *)(ws + s.part_ml);
     }
     if (a.scores_out) {
-        a.frag_q = ws + s.frag_q;
+        if (a.rows <= kLogitRows)
+            a.logits = (float *)(ws + s.frag_q);
+        else
+            a.frag_q = ws + s.frag_q;
         a.row_info = (float *)(ws + s.row_info);
     }
     switch (a.c.dim) {

@@ -47,6 +47,13 @@ struct Batch {
     int32_t n_seq, table_width, max_new, uniform;
 };
 
+// Division by a number that the host knows: n / d = n * mul >> (31 + shift),
+// exact for 0 <= n < 2^31.
+struct Divisor {
+    uint32_t mul;
+    int32_t shift;
+};
+
 struct MoveArgs {  // append and read
     Cache c;
     Tokens k, v;
@@ -65,15 +72,17 @@ struct AttendArgs {
     int32_t rows;          // max_new * group_heads
     int32_t row_blocks;
     int32_t max_len;
-    int32_t chunk;         // positions of a workgroup, a power of two
+    int32_t chunk_shift;   // a workgroup has at most 1 << chunk_shift positions
     int32_t n_split;
     float *part_o;         // [n_seq][heads][n_split][rows][dim]
     float *part_ml;        // [n_seq][heads][n_split][rows][2]
-    // with scores: the queries as the matrix unit takes them, and what turns
-    // their products into weights
+    // with scores: what turns products into weights, and either the logarithms
+    // of a few rows' products or the queries as the matrix unit takes them
+    float *logits;         // [n_seq][heads][records of max_len][rows][32], or nullptr
     void *frag_q;          // fp16 [n_seq][heads][row tiles][dim/32 + 1][64 lanes][8]: q, and its sums over groups
     float *row_info;       // [n_seq][heads][row tiles][16][2]: factor, lse2
     int32_t row_tiles;
+    Divisor by_heads, by_group_heads, by_row_blocks, by_split, by_rows;
     const float *scores_in;
     float *scores_out;
     int64_t score_stride;
@@ -102,6 +111,7 @@ int launch_attend_d96(const AttendArgs &a, int row_tile, void *stream);
 int launch_attend_d128(const AttendArgs &a, int row_tile, void *stream);
 int launch_attend_d256(const AttendArgs &a, int row_tile, void *stream);
 int launch_combine(const AttendArgs &a, void *stream);
+int launch_weigh(const AttendArgs &a, void *stream);
 int launch_evict(const EvictArgs &a, void *stream);
 
 }  // namespace tkv

@@ -33,6 +33,7 @@ static int launch_group(const AttendArgs &a, int row_tile, void *stream) {
     int rc = a.q.type == kBf16 ? launch_type<D, GROUP, true>(a, row_tile, stream)
                                : launch_type<D, GROUP, false>(a, row_tile, stream);
     if (rc == 0 && a.n_split > 1) rc = launch_combine(a, stream);
+    if (rc == 0 && a.logits) return launch_weigh(a, stream);
     if (rc == 0 && a.scores_out && a.max_len > 0) {
         constexpr int kPositions = kTile * kAttendWaves * kScoreRecords<D>;
         const int64_t splits = (a.max_len + kPositions - 1) / kPositions;

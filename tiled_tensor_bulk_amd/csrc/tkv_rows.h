@@ -118,12 +118,8 @@ __global__ void __launch_bounds__(64 * kAttendWaves, 2) rows_kernel(const Attend
 
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int lane = threadIdx.x & 63, g = lane >> 4, n = lane & 15;
-    int at = blockIdx.x;
-    const int block = at % a.row_blocks;
-    at /= a.row_blocks;
-    const int split = at % a.n_split;
-    at /= a.n_split;
-    const int head = at % (int)a.c.heads, seq = at / (int)a.c.heads;
+    int block, split, head, seq;
+    place(a, block, split, head, seq);
     const int32_t *table = a.b.table + seq * a.b.table_stride;
     const Extent e(a, seq);
     const Chunks chunks(a, e.len);
@@ -135,11 +131,11 @@ __global__ void __launch_bounds__(64 * kAttendWaves, 2) rows_kernel(const Attend
 
     // positions that some row of the workgroup sees, and of the wave
     const int last = block * R + R < e.rows ? block * R + R - 1 : e.rows - 1;
-    int end = e.limit(a, last / a.group_heads);
+    int end = e.limit(a, divided(last, a.by_group_heads));
     end = end < t0 + chunks.size ? end : t0 + chunks.size;
     const int wave_last = r0 + 16 * NT < e.rows ? r0 + 16 * NT - 1 : e.rows - 1;
-    const int wave_end = r0 < e.rows ? e.limit(a, wave_last / a.group_heads) : 0;
-    const int all_see = r0 < e.rows ? e.limit(a, r0 / a.group_heads) : 0;
+    const int wave_end = r0 < e.rows ? e.limit(a, divided(wave_last, a.by_group_heads)) : 0;
+    const int all_see = r0 < e.rows ? e.limit(a, divided(r0, a.by_group_heads)) : 0;
 
     Row<D, GROUP> raw[NT];
 #pragma unroll
@@ -157,13 +153,13 @@ __global__ void __launch_bounds__(64 * kAttendWaves, 2) rows_kernel(const Attend
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
         const int r = r0 + 16 * nt + n;
-        limit[nt] = r < e.rows ? e.limit(a, r / a.group_heads) : 0;
+        limit[nt] = r < e.rows ? e.limit(a, divided(r, a.by_group_heads)) : 0;
         float qsum[F::NG], f;
         raw[nt].template operand<BF16>(a, q[nt], qsum, f);
         sums[nt] = sum_parts<D, GROUP>(qsum, g);
         factor[nt] = sums_factor(f);
         s[nt].clear();
-        if (a.frag_q && split == 0 && r0 / 16 + nt < a.row_tiles)
+        if (a.row_info && split == 0 && r0 / 16 + nt < a.row_tiles)
             keep_rows<D, GROUP>(a, ((int64_t)seq * a.c.heads + head) * a.row_tiles + r0 / 16 + nt, lane, q[nt],
                                 sums[nt], factor[nt]);
     }

@@ -2,7 +2,7 @@
 //   scores_out = scores_in + sum over rows of exp2(y - lse2)
 // with the logarithms y computed again from the K codes (half of a record)
 // rather than kept in memory by the first kernel, which would be 4 bytes for
-// each position and row.
+// each position and row: less only for up to 8 rows, which weigh_kernel takes.
 //
 // A wave owns RECS records, unpacked in registers with their scales and zeros,
 // and goes over the tiles of 16 rows that see them; a workgroup's waves go over
@@ -92,8 +92,8 @@ __global__ void __launch_bounds__(64 * kAttendWaves) scores_kernel(const AttendA
     const int splits = (a.max_len + kTile * RECS * kAttendWaves - 1) / (kTile * RECS * kAttendWaves);
     int at = blockIdx.x;
     const int split = at % splits;
-    at /= splits;
-    const int head = at % (int)a.c.heads, seq = at / (int)a.c.heads;
+    int head = at / splits;
+    const int seq = divide(head, (int)a.c.heads, a.by_heads);
     const Extent e(a, seq);
     const int p0 = (split * kAttendWaves + wave) * kTile * RECS;
     if (p0 >= e.len) return;
@@ -131,7 +131,7 @@ __global__ void __launch_bounds__(64 * kAttendWaves) scores_kernel(const AttendA
 #pragma unroll
             for (int i = 0; i < RECS; ++i) keys[i].template add<false>(now, 0, 0, lane);
         } else {
-            const int r = t * 16 + n, limit = r < e.rows ? e.limit(a, r / a.group_heads) : 0;
+            const int r = t * 16 + n, limit = r < e.rows ? e.limit(a, divided(r, a.by_group_heads)) : 0;
 #pragma unroll
             for (int i = 0; i < RECS; ++i) keys[i].template add<true>(now, p0 + kTile * i, limit, lane);
         }
