@@ -130,10 +130,13 @@ __device__ __forceinline__ int page_at(const int32_t *row, int width, uint32_t n
 }
 
 // The record of positions 32 * tile .. 32 * tile + 31 of `head`, in `page`.
+// The address passes through a pointer to global memory, as a load through one
+// to anything would wait, and be waited for, with accesses to LDS.
+typedef __attribute__((address_space(1))) char global_char;
 __device__ __forceinline__ char *record_at(const Cache &c, int page, int head, int tile) {
     const uint32_t in_page = (uint32_t)tile & ((1u << (c.page_shift - 5)) - 1);
-    return (char *)c.pool + (uint64_t)(uint32_t)page * c.page_bytes + (uint64_t)(uint32_t)head * c.head_bytes +
-           in_page * c.record;
+    return (char *)(global_char *)(c.pool + (uint64_t)(uint32_t)page * c.page_bytes +
+                                   (uint64_t)(uint32_t)head * c.head_bytes + in_page * c.record);
 }
 
 __device__ __forceinline__ float bf16_to_float(uint16_t u) { return __builtin_bit_cast(float, (uint32_t)u << 16); }

@@ -85,7 +85,7 @@ struct ScoreKeys {  // 32 positions
 };
 
 template <int D, int GROUP>
-__global__ void __launch_bounds__(64 * kAttendWaves) scores_kernel(const AttendArgs a) {
+__global__ void __launch_bounds__(64 * kAttendWaves, 2) scores_kernel(const AttendArgs a) {
     constexpr int RECS = kScoreRecords<D>;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int lane = threadIdx.x & 63, g = lane >> 4, n = lane & 15;
