@@ -45,8 +45,6 @@
 namespace tkv {
 
 constexpr int kAttendWaves = 4;
-template <int D>
-constexpr int kScoreRecords = D <= 128 ? 2 : 1;  // records of a wave of the scores kernel
 constexpr float kFar = -1e30f;  // reference of a row that has seen nothing
 constexpr float kLift = 7.0f;   // weights are held times 2^7
 constexpr float kSlack = 8.0f;

@@ -35,7 +35,7 @@ static int launch_group(const AttendArgs &a, int row_tile, void *stream) {
     if (rc == 0 && a.n_split > 1) rc = launch_combine(a, stream);
     if (rc == 0 && a.logits) return launch_weigh(a, stream);
     if (rc == 0 && a.scores_out && a.max_len > 0) {
-        constexpr int kPositions = kTile * kAttendWaves * kScoreRecords<D>;
+        constexpr int kPositions = kTile * kAttendWaves;
         const int64_t splits = (a.max_len + kPositions - 1) / kPositions;
         scores_kernel<D, GROUP><<<dim3((uint32_t)(splits * a.c.heads * a.b.n_seq)), block, 0, s>>>(a);
         rc = (int)hipGetLastError();
