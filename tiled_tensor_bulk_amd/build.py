@@ -1,10 +1,11 @@
-"""Build libtmap.so and libtkv.so (gfx950) in-tree with hipcc.
+"""Build libtmap.so and libtkv.so (gfx950) in-tree with hipcc, and _tkv.so with g++.
 
     python -m tiled_tensor_bulk_amd.build [--jobs N]
 
 Each translation unit is compiled in parallel into tiled_tensor_bulk_amd/_build
 and linked into tiled_tensor_bulk_amd/libtmap.so (the tile copies) or
-libtkv.so (the 4-bit cache and its operators).  Cross-compiles without a GPU.
+libtkv.so (the 4-bit cache and its operators); _tkv.so is libtkv's calls on torch
+tensors.  Cross-compiles without a GPU.
 """
 from __future__ import annotations
 
@@ -20,6 +21,7 @@ CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libtmap.so")
 TKV_LIB = os.path.join(PKG, "libtkv.so")
+TORCH_LIB = os.path.join(PKG, "_tkv.so")
 ROOT = os.path.dirname(PKG)
 
 SOURCES = (["tmap_host.cpp"] + [f"tmap_{m}_r{r}.hip" for m in ("load", "store", "roundtrip") for r in (2, 5)]
@@ -45,9 +47,26 @@ def common_flags():
             "-I", os.path.join(ROOT, "include")]
 
 
+def torch_command(out: str):
+    """g++'s command for _tkv.so: host code only."""
+    import sysconfig
+
+    import torch
+
+    at = os.path.dirname(torch.__file__)
+    rocm = os.path.dirname(os.path.dirname(os.path.realpath(hipcc())))
+    return (["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden", "-Wall",
+             "-D__HIP_PLATFORM_AMD__", "-DUSE_ROCM", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+             f"-I{at}/include", f"-I{at}/include/torch/csrc/api/include", f"-I{rocm}/include",
+             f"-I{sysconfig.get_paths()['include']}", os.path.join(CSRC, "tkv_torch.cpp"), "-o", out, f"-L{PKG}",
+             "-l:libtkv.so", f"-L{at}/lib"]
+            + [f"-l{n}" for n in ("torch_python", "torch", "torch_cpu", "torch_hip", "c10", "c10_hip")]
+            + ["-Wl,-rpath,$ORIGIN"])
+
+
 def build(jobs: int = 7, verbose: bool = False, incremental: bool = False) -> str:
     """Compile every translation unit (or, with incremental=True, only those
-    older than a source or header) and link both libraries."""
+    older than a source or header) and link the libraries."""
     os.makedirs(BUILD, exist_ok=True)
     cc = hipcc()
     procs = []
@@ -85,8 +104,10 @@ def build(jobs: int = 7, verbose: bool = False, incremental: bool = False) -> st
         objs = [os.path.join(BUILD, src + ".o") for src in sources]
         subprocess.check_call([cc, f"--offload-arch={ARCH}", "-shared", "-fPIC", "-o", tmp, *objs])
         os.replace(tmp, lib)
+    subprocess.check_call(torch_command(TORCH_LIB + ".tmp"))
+    os.replace(TORCH_LIB + ".tmp", TORCH_LIB)
     if verbose:
-        print(f"built {LIB} and {TKV_LIB} in {time.time() - t0:.1f}s", flush=True)
+        print(f"built {LIB}, {TKV_LIB} and {TORCH_LIB} in {time.time() - t0:.1f}s", flush=True)
     return LIB
 
 

@@ -238,7 +238,8 @@ __global__ void __launch_bounds__(64 * kEvictWaves) move_kernel(const EvictArgs 
     const char *src = page < 0 ? nullptr : record_at(a.c, page, head, pos / kTile);
     const uint32_t src_lo = (uint32_t)(uint64_t)src, src_hi = (uint32_t)((uint64_t)src >> 32);
     const auto record_of = [&](int i) {
-        return (const char *)(((uint64_t)(uint32_t)__shfl((int)src_hi, i) << 32) | (uint32_t)__shfl((int)src_lo, i));
+        return (const char *)(global_char *)(((uint64_t)(uint32_t)__shfl((int)src_hi, i) << 32) |
+                                             (uint32_t)__shfl((int)src_lo, i));
     };
 #pragma unroll
     for (int half = 0; half < 2; ++half) {

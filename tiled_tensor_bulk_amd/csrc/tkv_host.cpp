@@ -163,7 +163,12 @@ tkv::Divisor divisor(uint32_t d) {
 
 uint64_t up(uint64_t v, uint64_t to) { return (v + to - 1) / to * to; }
 
-// Rows of a workgroup: 16, or 32 where there are more.  Chunks: as long as
+// Rows of a workgroup: 16 or 32 whose positions its waves share, or 64 or 128
+// that its waves share.  With 256 channels the registers hold 16 in the first
+// manner, and that reads each record for every 16 rows, which pays up to 48 of
+// them: 8 sequences of up to 1500 positions, 34 rows, 21.9 us, with 64 rows of
+// the second manner 30.8 (4 sequences of up to 8192: 32 rows 45 and 50, 48 rows
+// 57 and 51).  Chunks: as long as
 // they leave 8 workgroups for a compute unit, whose lengths may then differ;
 // each costs a partial sum.  A batch of 64 sequences of 4096 to 32768
 // positions, 8 heads: 375 us with 8 workgroups, 425 with 4, 401 with 32;
@@ -182,7 +187,7 @@ constexpr int kLogitRows = 8;
 
 Split plan(const Cache &c, int64_t n_seq, int64_t rows, int64_t max_len, bool scores, int cus) {
     Split s{};
-    s.row_tile = rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 || c.dim > 128 ? 64 : 128;
+    s.row_tile = rows <= 16 || (c.dim > 128 && rows <= 48) ? 16 : rows <= 32 ? 32 : rows <= 64 || c.dim > 128 ? 64 : 128;
     s.row_blocks = (int)((rows + s.row_tile - 1) / s.row_tile);
     s.row_tiles = (int)((rows + 15) / 16);
     const int64_t units = n_seq * c.heads * s.row_blocks;

@@ -14,7 +14,10 @@ static int launch_type(const AttendArgs &a, int row_tile, void *stream) {
     if (row_tile == 16) {
         attend_kernel<D, GROUP, 1, BF16><<<grid, block, 0, s>>>(a);
     } else if (row_tile == 32) {
-        attend_kernel<D, GROUP, 2, BF16><<<grid, block, 0, s>>>(a);
+        if constexpr (D > 128)
+            return (int)hipErrorInvalidValue;
+        else
+            attend_kernel<D, GROUP, 2, BF16><<<grid, block, 0, s>>>(a);
     } else if (row_tile == 64) {
         rows_kernel<D, GROUP, 1, BF16><<<grid, block, 0, s>>>(a);
     } else {
