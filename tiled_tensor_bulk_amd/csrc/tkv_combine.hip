@@ -4,16 +4,16 @@
 // by exp2(-m): with M the largest m, l = sum l_i exp2(m_i - M), and the same
 // for o.  A lane holds 4 channels of a row.  Where a row has many chunks, as a
 // few rows of a long context have, a workgroup takes 32 channels of one row and
-// reads 32 chunks at a time; else a row's lanes go over its chunks alone, four
+// reads 32 chunks at a time; else a row's lanes go over its chunks alone, all
 // of them on their way at once.
 #include "tkv_attend.h"
 
 namespace tkv {
 
 constexpr int kCombineThreads = 256;
-constexpr int kFewParts = 12, kAtOnce = 4;
+constexpr int kFewParts = 16;
 
-template <int D>
+template <int D, int PARTS>
 __global__ void __launch_bounds__(kCombineThreads) combine_few_kernel(const AttendArgs a) {
     constexpr int LANES = D / 4, AT_ONCE = kCombineThreads / LANES;
     const int which = threadIdx.x / LANES, lane = threadIdx.x % LANES;
@@ -28,30 +28,23 @@ __global__ void __launch_bounds__(kCombineThreads) combine_few_kernel(const Atte
     const int64_t first = ((int64_t)unit * a.n_split) * a.rows + row;
     float best = kFar, sum = 0.0f;
     f4 y = (f4){0, 0, 0, 0};
-    for (int s0 = 0; s0 < parts; s0 += kAtOnce) {
-        float2 ml[kAtOnce];
-        f4 o[kAtOnce];
+    float2 ml[PARTS];
+    f4 o[PARTS];
 #pragma unroll
-        for (int s = 0; s < kAtOnce; ++s) {  // past the last one: it again, without weight
-            const int64_t from = first + (int64_t)(s0 + s < parts ? s0 + s : parts - 1) * a.rows;
-            ml[s] = *reinterpret_cast<const float2 *>(a.part_ml + 2 * from);
-            o[s] = *reinterpret_cast<const f4 *>(a.part_o + from * D + 4 * lane);
-        }
-        float top = best;
-#pragma unroll
-        for (int s = 0; s < kAtOnce; ++s) top = fmaxf(top, ml[s].x);
-        const float old = exp2f(best - top);
-        sum *= old;
-        y *= old;
-        best = top;
-#pragma unroll
-        for (int s = 0; s < kAtOnce; ++s)
-            if (s0 + s < parts) {
-                const float f = exp2f(ml[s].x - best);
-                sum += f * ml[s].y;
-                y += f * o[s];
-            }
+    for (int s = 0; s < PARTS; ++s) {  // past the last one: it again, without weight
+        const int64_t from = first + (int64_t)(s < parts ? s : parts - 1) * a.rows;
+        ml[s] = *reinterpret_cast<const float2 *>(a.part_ml + 2 * from);
+        o[s] = *reinterpret_cast<const f4 *>(a.part_o + from * D + 4 * lane);
     }
+#pragma unroll
+    for (int s = 0; s < PARTS; ++s) best = fmaxf(best, ml[s].x);
+#pragma unroll
+    for (int s = 0; s < PARTS; ++s)
+        if (s < parts) {
+            const float f = exp2f(ml[s].x - best);
+            sum += f * ml[s].y;
+            y += f * o[s];
+        }
     write_row(a, e, seq, head, row, 4 * lane, y, best, sum);
 }
 
@@ -103,8 +96,10 @@ template <int D>
 static int launch(const AttendArgs &a, hipStream_t s) {
     const int64_t rows = (int64_t)a.b.n_seq * a.c.heads * a.rows;
     constexpr int AT_ONCE = kCombineThreads / (D / 4);
-    if (a.n_split <= kFewParts)
-        combine_few_kernel<D><<<dim3((uint32_t)((rows + AT_ONCE - 1) / AT_ONCE)), dim3(kCombineThreads), 0, s>>>(a);
+    if (a.n_split <= 4)
+        combine_few_kernel<D, 4><<<dim3((uint32_t)((rows + AT_ONCE - 1) / AT_ONCE)), dim3(kCombineThreads), 0, s>>>(a);
+    else if (a.n_split <= kFewParts)
+        combine_few_kernel<D, kFewParts><<<dim3((uint32_t)((rows + AT_ONCE - 1) / AT_ONCE)), dim3(kCombineThreads), 0, s>>>(a);
     else
         combine_kernel<D><<<dim3((uint32_t)(rows * (D / 32))), dim3(kCombineThreads), 0, s>>>(a);
     return (int)hipGetLastError();
