@@ -369,11 +369,10 @@ struct FewRows {
     static constexpr int kSlot = kLoads * 1024;
     static constexpr int kDepth = 2;
     static constexpr int kRing = kDepth * kSlot;  // a wave's; later CH words of its sums, and its references and sums
-    static constexpr int CH = D == 96 ? 3 : D == 64 && NT == 2 ? 2 : 4;
-    static constexpr int kRounds = 2 * F::W / CH;
-    static_assert(kRounds * CH == 2 * F::W, "rounds cover the channels");
     static constexpr int kJoinM = kRing - 32 * 4 * NT, kJoinL = kRing - 16 * 4 * NT;
-    static_assert(CH * NT * 1024 <= kJoinM, "both fit");
+    static constexpr int kRounds = 2 * F::W * NT * 1024 <= kJoinM ? 1 : 2;
+    static constexpr int CH = 2 * F::W / kRounds;
+    static_assert(CH * kRounds == 2 * F::W && CH * NT * 1024 <= kJoinM, "rounds cover the channels, and fit");
     static constexpr int kRegs = NT * (12 * F::W + 4 * F::NG + 20) + 8 * F::NG + 2 * F::W + 28;
     static constexpr int kWaves = kRegs <= 128 ? 4 : kRegs <= 168 ? 3 : kRegs <= 256 ? 2 : 1;
 };
@@ -529,6 +528,7 @@ __global__ void __launch_bounds__(64 * kAttendWaves, (FewRows<D, GROUP, NT>::kWa
     wait_lds();
     const auto m_of = [&](int w, int r) -> float & { return reinterpret_cast<float *>(ring + w * K::kRing + K::kJoinM)[r]; };
     const auto l_of = [&](int w, int r) -> float & { return reinterpret_cast<float *>(ring + w * K::kRing + K::kJoinL)[r]; };
+    const int row_bits = rows_here > 1 ? 32 - __builtin_clz(rows_here - 1) : 0;  // room for the rows that are there
     const auto o_of = [&](int w, int item) -> f4 & { return reinterpret_cast<f4 *>(ring + w * K::kRing)[item]; };
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
@@ -544,10 +544,10 @@ __global__ void __launch_bounds__(64 * kAttendWaves, (FewRows<D, GROUP, NT>::kWa
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) o_of(wave, (c * NT + nt) * 64 + lane) = s[nt].o[round * K::CH + c];
         __syncthreads();
-        for (int item = threadIdx.x; item < K::CH * NT * 64; item += 64 * kAttendWaves) {
-            const int cn = item >> 6, ln = item & 63;
-            const int rl = 16 * (cn % NT) + (ln & 15), row = r0 + rl;
-            if (row >= e.rows) continue;
+        // four channels of a row that is there for each thread
+        for (int item = threadIdx.x; item < (K::CH * 4) << row_bits; item += 64 * kAttendWaves) {
+            const int rl = item & ((1 << row_bits) - 1), quad = item >> row_bits, row = r0 + rl;
+            if (rl >= rows_here) continue;
             float best = m_of(0, rl);
 #pragma unroll
             for (int w = 1; w < kAttendWaves; ++w) best = fmaxf(best, m_of(w, rl));
@@ -557,9 +557,9 @@ __global__ void __launch_bounds__(64 * kAttendWaves, (FewRows<D, GROUP, NT>::kWa
             for (int w = 0; w < kAttendWaves; ++w) {
                 const float f = __builtin_amdgcn_exp2f(m_of(w, rl) - best);
                 sum += l_of(w, rl) * f;
-                y += o_of(w, item) * f;
+                y += o_of(w, ((quad >> 2) * NT + (rl >> 4)) * 64 + 16 * (quad & 3) + (rl & 15)) * f;
             }
-            const int channel = 16 * (round * K::CH + cn / NT) + 4 * (ln >> 4);
+            const int channel = 16 * K::CH * round + 4 * quad;
             if (a.n_split > 1) {
                 const int64_t to = unit * a.rows + row;
                 *reinterpret_cast<f4 *>(a.part_o + to * D + channel) = y;
