@@ -1,13 +1,12 @@
 // tkv_move.hip -- new tokens into the cache (append) and positions out of it
 // (read).
 //
-// One wave takes one record: 32 positions of one head of one sequence.  A K
+// A wave takes one record: 32 positions of one head of one sequence.  A K
 // word belongs to one position, but a V word holds 8 positions of a channel,
-// so the wave that owns the record also owns its V words: where some of a
-// word's positions are not new, it reads the word, replaces the new nibbles
-// and writes it back, with no atomics.  Rows are read as the K operand lies
-// (lane 16 g + m: position m, channels 32 i + 8 g ..); V codes change places
-// through LDS, as bytes.
+// so one wave owns a record's V words: where some of a word's positions are not
+// new, it reads the word, replaces the new nibbles and writes it back, with no
+// atomics.  Rows are read as the K operand lies (lane 16 g + m: position m,
+// channels 32 i + 8 g ..); V codes change places through LDS, as bytes.
 //
 // What bounds both is memory: two bytes of input (or four of output) for each
 // half byte of cache.
@@ -24,9 +23,9 @@ constexpr int kFewTokens = 4;
 // and a small integer, and differences of fp16 and bf16 numbers, are exact; a
 // lane goes there when one of its N is.
 template <int N>
-__device__ __forceinline__ void codes_of(const float *x, float z, float s, uint8_t *code) {
+__device__ __forceinline__ void codes_of(const float *x, float z, float s, float *c) {
     const float inv = s > 0.0f ? 1.0f / s : 0.0f;
-    float c[N], off = 0.0f;
+    float off = 0.0f;
 #pragma unroll
     for (int i = 0; i < N; ++i) {
         const float t = (x[i] - z) * inv;
@@ -45,8 +44,16 @@ __device__ __forceinline__ void codes_of(const float *x, float z, float s, uint8
         }
     }
 #pragma unroll
-    for (int i = 0; i < N; ++i) code[i] = (uint8_t)fminf(fmaxf(c[i], 0.0f), 15.0f);
+    for (int i = 0; i < N; ++i) c[i] = fminf(fmaxf(c[i], 0.0f), 15.0f);
 }
+// 8 codes as a word: two sums of 16 bits, exact in fp32.
+__device__ __forceinline__ uint32_t word_of(const float *c) {
+    const float lo = fmaf(fmaf(fmaf(c[6], 16.0f, c[4]), 16.0f, c[2]), 16.0f, c[0]);
+    const float hi = fmaf(fmaf(fmaf(c[7], 16.0f, c[5]), 16.0f, c[3]), 16.0f, c[1]);
+    return (uint32_t)lo | ((uint32_t)hi << 16);
+}
+static_assert(nibble_of(0) == 0 && nibble_of(2) == 1 && nibble_of(4) == 2 && nibble_of(6) == 3 && nibble_of(1) == 4 &&
+                  nibble_of(3) == 5 && nibble_of(5) == 6 && nibble_of(7) == 7, "even codes, then odd ones");
 
 __device__ __forceinline__ void scale_of(float lo, float hi, _Float16 &scale, _Float16 &zero) {
     scale = (_Float16)((hi - lo) / 15.0f);
@@ -56,7 +63,7 @@ __device__ __forceinline__ void scale_of(float lo, float hi, _Float16 &scale, _F
 // Quantise one position's channels: lane group g holds channels 32 i + 8 g + j
 // in x[8 i + j]; the four lanes of a position share its scales.
 template <int D, int GROUP>
-__device__ __forceinline__ void quantise(const float *x, _Float16 *scale, _Float16 *zero, uint8_t *code) {
+__device__ __forceinline__ void quantise(const float *x, _Float16 *scale, _Float16 *zero, float *code) {
     using F = Format<D, GROUP>;
 #pragma unroll
     for (int grp = 0; grp < F::NG; ++grp) {
@@ -78,15 +85,12 @@ __device__ __forceinline__ void quantise(const float *x, _Float16 *scale, _Float
 
 __device__ __forceinline__ float limited(float y) { return y != y ? 0.0f : fminf(fmaxf(y, -kLimit), kLimit); }
 
+// A row's channels 32 i + 8 g .. as they lie.
 template <int D>
-__device__ __forceinline__ void load_row(const Tokens &t, int64_t row, int head, int g, float *x) {
+__device__ __forceinline__ void load_row(const Tokens &t, int64_t row, int head, int g, uint4 (&raw)[D / 32]) {
     const int64_t at = row * t.token_stride + head * t.head_stride + 8 * g;
 #pragma unroll
-    for (int i = 0; i < D / 32; ++i) {
-        load8(t, at + 32 * i, x + 8 * i);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) x[8 * i + j] = limited(x[8 * i + j]);
-    }
+    for (int i = 0; i < D / 32; ++i) raw[i] = load8_raw(t, at + 32 * i);
 }
 
 struct Unit {
@@ -112,33 +116,56 @@ __device__ __forceinline__ bool unit_of(const MoveArgs &a, int unit, Unit &u) {
     return true;
 }
 
+// Codes, scales and zeros of one position's channels, from its row.
+template <int D, int GROUP>
+__device__ __forceinline__ void quantise_row(const uint4 (&raw)[D / 32], int type, _Float16 *scale, _Float16 *zero,
+                                             float *code) {
+    float x[D / 4];
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i) {
+        if (type == kBf16)
+            raw_to_float<true>(raw[i], x + 8 * i);
+        else
+            raw_to_float<false>(raw[i], x + 8 * i);
+    }
+#pragma unroll
+    for (int j = 0; j < D / 4; ++j) x[j] = limited(x[j]);
+    quantise<D, GROUP>(x, scale, zero, code);
+}
+
+// Many new tokens: of two waves on a record one takes the keys and one the
+// values.  Each asks for all its rows before it works on the first: with both
+// in one wave and one row at a time a prompt waited for memory four times over.
 template <int D, int GROUP>
 __global__ void __launch_bounds__(64 * kMoveWaves) append_kernel(const MoveArgs a) {
     using F = Format<D, GROUP>;
-    constexpr int PITCH = D + 4;  // bytes of a position's codes in LDS, off a multiple of the banks
-    __shared__ uint8_t codes[kMoveWaves][kTile * PITCH];
+    constexpr int PITCH = D + 4;  // bytes of a row in LDS, off a multiple of the banks
+    __shared__ uint8_t codes[kMoveWaves / 2][16 * PITCH];  // V codes of positions m and m + 16 in a byte
     const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, g = lane >> 4, m = lane & 15;
+    const bool keys = __builtin_amdgcn_readfirstlane(wave & 1) == 0;
     Unit u;
-    if (!unit_of(a, blockIdx.x * kMoveWaves + wave, u) || !u.rec) return;  // waves share nothing
-    uint8_t *mine = codes[wave];
+    if (!unit_of(a, blockIdx.x * (kMoveWaves / 2) + (wave >> 1), u) || !u.rec) return;  // waves share nothing
+    uint8_t *mine = codes[wave >> 1];
     const int p0 = u.tile * kTile;
+    const Tokens &from = keys ? a.k : a.v;
+    uint4 raw[2][F::W];
+    bool live[2];
 #pragma unroll
     for (int half = 0; half < 2; ++half) {
-        const int pos = p0 + 16 * half + m, i = pos - u.first;
-        const bool live = i >= 0 && i < u.n;
-        float x[D / 4];
-        _Float16 scale[F::NG], zero[F::NG];
-        uint8_t code[D / 4];
-        if (live) {
-            load_row<D>(a.k, u.start + i, u.head, g, x);
-            quantise<D, GROUP>(x, scale, zero, code);  // the four lanes of a position are live together
+        const int i = p0 + 16 * half + m - u.first;
+        live[half] = i >= 0 && i < u.n;  // the four lanes of a position are live together
+        load_row<D>(from, u.start + (live[half] ? i : 0), u.head, g, raw[half]);
+    }
+    _Float16 scale[F::NG], zero[F::NG];
+    if (keys) {
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+            float code[D / 4];
+            quantise_row<D, GROUP>(raw[half], from.type, scale, zero, code);
+            if (!live[half]) continue;
             uint32_t word[F::W];
 #pragma unroll
-            for (int w = 0; w < F::W; ++w) {
-                word[w] = 0;
-#pragma unroll
-                for (int j = 0; j < 8; ++j) word[w] |= (uint32_t)code[8 * w + j] << (4 * nibble_of(j));
-            }
+            for (int w = 0; w < F::W; ++w) word[w] = word_of(code + 8 * w);
 #pragma unroll
             for (int s = 0; s < F::S; ++s)
                 store_words<F::WV>(u.rec + (((half * F::S + s) * 64 + lane) * F::WV) * 4, word + s * F::WV);
@@ -148,24 +175,30 @@ __global__ void __launch_bounds__(64 * kMoveWaves) append_kernel(const MoveArgs 
                     *reinterpret_cast<h2 *>(u.rec + F::KP + (grp * kTile + 16 * half + m) * 4) =
                         (h2){scale[grp], zero[grp]};
             }
-            load_row<D>(a.v, u.start + i, u.head, g, x);
-            quantise<D, GROUP>(x, scale, zero, code);
+        }
+        return;
+    }
+    uint32_t low[2 * F::W];  // four channels' codes in a word's bytes, of the first half
 #pragma unroll
-            for (int w = 0; w < F::W; ++w) {
-                uint32_t c[2] = {0, 0};
+    for (int half = 0; half < 2; ++half) {
+        float code[D / 4];
+        quantise_row<D, GROUP>(raw[half], from.type, scale, zero, code);
+        if (live[half] && g == 0) {
+            const int slot = 8 * (m >> 2) + 4 * half + (m & 3);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) c[j >> 2] |= (uint32_t)code[8 * w + j] << (8 * (j & 3));
-                uint32_t *to = reinterpret_cast<uint32_t *>(mine + (16 * half + m) * PITCH + 32 * w + 8 * g);
-                to[0] = c[0], to[1] = c[1];
+            for (int grp = 0; grp < F::NG; ++grp) {
+                _Float16 *to = reinterpret_cast<_Float16 *>(u.rec + F::VP) + grp * 64 + slot;
+                to[0] = scale[grp], to[32] = zero[grp];
             }
-            if (g == 0) {
-                const int slot = 8 * (m >> 2) + 4 * half + (m & 3);
+        }
 #pragma unroll
-                for (int grp = 0; grp < F::NG; ++grp) {
-                    _Float16 *to = reinterpret_cast<_Float16 *>(u.rec + F::VP) + grp * 64 + slot;
-                    to[0] = scale[grp], to[32] = zero[grp];
-                }
-            }
+        for (int w = 0; w < 2 * F::W; ++w) {  // sums of 16 bits, exact in fp32; those of positions not new are masked below
+            const float *c = code + 4 * w;
+            const uint32_t bytes = (uint32_t)fmaf(c[1], 256.0f, c[0]) | (uint32_t)fmaf(c[3], 256.0f, c[2]) << 16;
+            if (half == 0)
+                low[w] = bytes;
+            else
+                *reinterpret_cast<uint32_t *>(mine + m * PITCH + 32 * (w >> 1) + 8 * g + 4 * (w & 1)) = low[w] | bytes << 4;
         }
     }
     __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
@@ -186,11 +219,11 @@ __global__ void __launch_bounds__(64 * kMoveWaves) append_kernel(const MoveArgs 
         if (mask != 0xFFFFFFFFu) load_words<F::WV>(at, word);
 #pragma unroll
         for (int w = 0; w < F::WV; ++w) {
-            const int channel = 16 * (hs * F::WV + w) + m;
-            uint32_t x = 0;
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-                x |= (uint32_t)(mine[(4 * g + (j & 3) + 16 * (j >> 2)) * PITCH + channel] & 15) << (4 * nibble_of(j));
+            // byte j: position 4 g + j below, 16 more above; the places of codes j and j + 4
+            const uint8_t *b = mine + 4 * g * PITCH + 16 * (hs * F::WV + w) + m;
+            const uint32_t even = b[0] | ((uint32_t)b[PITCH] << 16), odd = b[2 * PITCH] | ((uint32_t)b[3 * PITCH] << 16);
+            const uint32_t x = (even & 0x000F000Fu) | (even & 0x00F000F0u) << 4 | (odd & 0x000F000Fu) << 4 |
+                               (odd & 0x00F000F0u) << 8;
             word[w] = mask == 0xFFFFFFFFu ? x : (word[w] & ~mask) | (x & mask);
         }
         store_words<F::WV>(at, word);
@@ -201,7 +234,7 @@ __global__ void __launch_bounds__(64 * kMoveWaves) append_kernel(const MoveArgs 
 // all lanes on one position, E channels each, as a step of decoding has a
 // token or so for each sequence and latency is what counts.  32 sequences of 8
 // heads: 3.6 us for one token each, 6.6 for 4 and 8.6 for 6, where the kernel
-// above takes 12.0, 8.3 and 8.1; so it is used up to kFewTokens.
+// above takes 7.1, 7.2 and 7.4; so it is used up to kFewTokens.
 template <int D, int GROUP>
 __global__ void __launch_bounds__(64 * kMoveWaves) append_few_kernel(const MoveArgs a) {
     using F = Format<D, GROUP>;
@@ -240,7 +273,7 @@ __global__ void __launch_bounds__(64 * kMoveWaves) append_few_kernel(const MoveA
         }
         float lo[2], hi[2];
         _Float16 scale[2], zero[2];
-        uint8_t code[2][E];
+        float code[2][E];
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
             lo[s] = hi[s] = x[s][0];
@@ -268,7 +301,7 @@ __global__ void __launch_bounds__(64 * kMoveWaves) append_few_kernel(const MoveA
             *reinterpret_cast<uint32_t *>(u.rec + (((half * F::S + i / F::WV) * 64 + 16 * kg + m) * F::WV + i % F::WV) * 4) = word;
         const int shift = 4 * (nibble & 1);
 #pragma unroll
-        for (int e = 0; e < E; ++e) *byte[e] = (uint8_t)((old[e] & (0xF0 >> shift)) | (code[1][e] << shift));
+        for (int e = 0; e < E; ++e) *byte[e] = (uint8_t)((old[e] & (0xF0 >> shift)) | ((uint32_t)code[1][e] << shift));
         if (ch % GROUP == 0) {
             *reinterpret_cast<h2 *>(u.rec + F::KP + (grp * kTile + t) * 4) = (h2){scale[0], zero[0]};
             _Float16 *v = reinterpret_cast<_Float16 *>(u.rec + F::VP) + grp * 64 + 8 * (m >> 2) + 4 * half + (m & 3);
@@ -354,7 +387,8 @@ static int launch_move(const MoveArgs &a, bool append, void *stream) {
     if (append && a.b.max_new <= kFewTokens)
         append_few_kernel<D, GROUP><<<grid, block, 0, (hipStream_t)stream>>>(a);
     else if (append)
-        append_kernel<D, GROUP><<<grid, block, 0, (hipStream_t)stream>>>(a);
+        append_kernel<D, GROUP><<<dim3((uint32_t)((units * 2 + kMoveWaves - 1) / kMoveWaves)), block, 0,
+                                  (hipStream_t)stream>>>(a);
     else
         read_kernel<D, GROUP><<<grid, block, 0, (hipStream_t)stream>>>(a);
     return (int)hipGetLastError();
