@@ -25,9 +25,8 @@
  *   K: position 16 * half + m, channel 32 * i + 8 * g + j
  *   V: channel 16 * (half * W + i) + m, position 4 * g + (j & 3) + 16 * (j >> 2)
  * and slot 8 * g + j of the V pairs is that same position.  This is the order
- * in which v_mfma_f32_16x16x32_f16 takes its operands, so attention reads
- * words in whole wave-wide runs and feeds them to the matrix unit without a
- * pass through LDS.
+ * in which v_mfma_f32_16x16x32_f16 takes its operands: attention reads words in
+ * whole wave-wide runs, and a lane's words are its part of the operand.
  *
  * Conventions for every call:
  *   - Pointers are HIP device pointers, unless they are `tkv_cache *`.  The
@@ -128,9 +127,9 @@ tmap_status tkv_read(const tkv_cache *cache, const tkv_tokens *k, const tkv_toke
  * attention weight, for p < lens[b] (other places are left alone).
  * scores_in may be scores_out, or NULL for 0.
  *
- * Products with codes are exact; softmax, sums and scales are fp32; a weight
- * and a V element's scale * code are rounded to fp16 once each on their way
- * into the matrix unit.
+ * Products of q with codes are exact up to their fp32 sum; softmax, sums and
+ * K's scales are fp32; a weight, and a V element's scale * (code - 8), are
+ * rounded to fp16 once each on their way into the matrix unit.
  */
 typedef struct tkv_attend_args {
     tkv_tokens q, out;        /* [n_tokens][q_heads][head_dim], fp16 or bf16, one type  */

@@ -113,6 +113,76 @@ def test_attend_rows(case):
         assert (have[b, :, n:] == -7.0).all()
 
 
+EVEN = [
+    # dim, group, heads, group heads, dtype, lens, new tokens, scores: the table is so wide that positions are dealt evenly
+    (128, 64, 1, 4, "bf16", [2500, 33, 0, 700], [1, 1, 1, 1], True),
+    (128, 64, 2, 3, "f16", [5000], [5], True),                # parts in more than one run of the joining kernel
+    (128, 32, 1, 9, "bf16", [640, 1300], [2, 3], True),       # 27 rows: two tiles, weights computed again
+    (128, 128, 1, 1, "f16", [513, 129, 128], [7, 0, 9], False),
+    (64, 32, 1, 8, "bf16", [1000, 300], [4, 2], False),
+    (64, 64, 2, 2, "f16", [90, 1100], [1, 6], True),
+    (96, 32, 1, 7, "bf16", [777], [2], False),
+    (256, 64, 1, 4, "f16", [300, 600], [10, 3], True),        # 40 rows: three blocks of 16, then one
+    (256, 32, 1, 2, "bf16", [700], [1], False),
+]
+
+
+def even_batch(rng, dim, group, heads, gh, dtype, lens, new, causal, scored, width):
+    page = 32
+    ends = np.cumsum([0] + [-(-n // page) for n in lens])
+    table = np.full((len(lens), width), -1, np.int32)
+    order = rng.permutation(max(1, ends[-1])).astype(np.int32)
+    for b in range(len(lens)):
+        table[b, :ends[b + 1] - ends[b]] = order[ends[b]:ends[b + 1]]
+    ref = a_ref(rng, order.size, heads, dim, page, group, table, lens)
+    cache, pool = a_cache(ref)
+    starts = np.concatenate(([0], np.cumsum(new)))
+    qt, q = typed(1.5 * rng.standard_normal((starts[-1], heads * gh, dim)), dtype)
+    longest = max(lens)
+    scores = rng.random((len(lens), heads, longest)).astype(np.float32) if scored else None
+    out, lse, after, mags = tkv_ref.attend(ref, table, lens, starts, q, dim ** -0.5, causal, scores)
+    extra = {}
+    if scored:
+        wide = torch.zeros((len(lens), heads, width * page), device=DEV)
+        wide[:, :, :longest] = torch.from_numpy(scores).to(DEV)
+        extra = dict(scores=wide, scores_out=wide)
+    got = T.tkv_attend(cache, qt, ints(table), ints(lens), starts=ints(starts), max_new=max(new), causal=causal, **extra)
+    check_attend(got, (out, lse), mags, dtype, dim)
+    if scored:
+        have = to64(wide)
+        worst = 2 * ((dim + 16) * 2.0 ** -24 * mags[2].max() + 2.0 ** -19)
+        for b, n in enumerate(lens):
+            w = after[b, :, :n] - scores[b, :, :n]
+            tol = worst * w + 2.0 ** -23 * after[b, :, :n] + 2.0 ** -24 * max(new) * heads * gh * w
+            assert (np.abs(have[b, :, :n] - after[b, :, :n]) <= tol + 1e-30).all(), b
+            assert np.array_equal(have[b, :, n:longest], scores[b, :, n:]) and not have[b, :, longest:].any()
+    return cache, qt, table, starts, got
+
+
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("case", EVEN, ids=lambda c: f"{c[0]}-{c[1]}-{c[3] * max(c[6])}")
+def test_attend_positions_dealt_evenly(case, causal):
+    dim, group, heads, gh, dtype, lens, new, scored = case
+    say(f"even {case} {causal}")
+    blocks = -(-gh * max(new) // 16)
+    # past 8 workgroups of 512 positions for a compute unit
+    width = 8 * 512 * torch.cuda.get_device_properties(0).multi_processor_count // (heads * blocks * 32 * len(lens)) * 2 + 32
+    even_batch(np.random.default_rng(sum(lens) + dim), dim, group, heads, gh, dtype, lens, new, causal, scored, width)
+
+
+@pytest.mark.parametrize("n,longest", [(256, 40), (200, 500), (37, 1500)])
+def test_attend_even_shares_over_many_sequences(n, longest):
+    """More row blocks than workgroups, empty sequences among them; the same batch with its sequences in another order
+    has the same rows up to the order of sums."""
+    say(f"even sequences {n} {longest}")
+    rng = np.random.default_rng(n)
+    lens = [int(x) for x in rng.integers(0, longest + 1, n)]
+    lens[0], lens[n // 2], lens[-1] = 0, longest, 0
+    new = [int(rng.integers(0, min(3, m) + 1)) for m in lens]
+    new[n // 2] = 2
+    even_batch(rng, 64, 64, 8, 2, "bf16", lens, new, True, False, 600)
+
+
 @pytest.mark.parametrize("gh,new", [(2, 5), (3, 40)])
 def test_rows_that_see_nothing(gh, new):
     """More new tokens than cached positions: the first of them see none."""

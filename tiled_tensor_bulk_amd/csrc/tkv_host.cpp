@@ -151,7 +151,8 @@ tmap_status move_args(const tkv_cache *cache, const tkv_tokens *k, const tkv_tok
 // How attention is split: see plan().
 struct Split {
     int row_tile, row_blocks, n_split, chunk, row_tiles;
-    uint64_t part_o, part_ml, frag_q, row_info, total;  // offsets, and bytes in all
+    bool even;
+    uint64_t part_o, part_ml, dealt, frag_q, row_info, total;  // offsets, and bytes in all
 };
 
 tkv::Divisor divisor(uint32_t d) {
@@ -166,23 +167,36 @@ uint64_t up(uint64_t v, uint64_t to) { return (v + to - 1) / to * to; }
 // Rows of a workgroup: 16 or 32 whose positions its waves share, or 64 or 128
 // that its waves share.  With 256 channels the registers hold 16 in the first
 // manner, and that reads each record for every 16 rows, which pays up to 48 of
-// them: 8 sequences of up to 1500 positions, 34 rows, 21.9 us, with 64 rows of
-// the second manner 30.8 (4 sequences of up to 8192: 32 rows 45 and 50, 48 rows
-// 57 and 51).  Chunks: as long as
-// they leave 8 workgroups for a compute unit, whose lengths may then differ;
-// each costs a partial sum.  A batch of 64 sequences of 4096 to 32768
-// positions, 8 heads: 375 us with 8 workgroups, 425 with 4, 401 with 32;
-// 16 sequences of up to 4099: 25.5 us at least 512 positions each, 29.7 at
-// 1024.  Powers of two, so that another bound on the lengths mostly leaves the
-// order of sums as it is.
+// them: 8 sequences of up to 1500 positions, 34 rows, 22 us, with 64 rows of the
+// second manner 31; 4 of up to 8192, 32 rows 38 us, 48 rows 46 and 42, 64 rows
+// 60 and 44.
+//
+// Chunks: as long as they leave 8 workgroups of few rows for a compute unit, 2
+// of many (512 new tokens over 8192 positions, 2 sequences: 217 us with 2, 307
+// with 1, 243 with 4), and at least 512 positions, as each costs a partial sum:
+// 16 sequences of up to 4099 positions, 22.7 us, at least 256 22.1, 1024 24.8;
+// 12 of up to 8191, 18.2, 20.5 and 17.0.  Powers of two, so that another bound
+// on the lengths mostly leaves the order of sums as it is.
+//
+// The host does not know the lengths, though, and where chunks are long a block
+// is a whole sequence or a good part of one.  Then few rows go by an even split,
+// the lengths in device memory deciding.  128 channels, 8 heads of 4 rows,
+// microseconds, even and in chunks: 64 sequences of 4096 to 32768 positions 269
+// and 290; 120 of 100 to 8000 122 and 133; one of 131072 and 63 of 1000 67 and
+// 227; 64 of 1000 in tables for 32768 29 and 47; but 64 of 8192 128 and 121, for
+// finding its share costs a workgroup some 3 us.  It does not pay where row
+// blocks alone fill the card, 200 sequences of 100 to 4000 109 and 98, or 256 of
+// 1000 62 and 54, unless one may be so long that the others wait for it: one of
+// 131072 and 199 of 1000 102 and 453.
 constexpr int kLeastChunk = 512;
 constexpr int kMostChunk = 1 << 16;
+constexpr int kLongForOne = 1 << 14;
 constexpr int kBlocksPerCu = 8;
 constexpr int kRowBlocksPerCu = 2;
 // Scores of up to so many rows go by logarithms kept in memory, 8 bytes a row
 // and position written and read, against half of a record read again (72 bytes
-// of 128 channels): 16 sequences of up to 16384 positions, 4 rows, 112 us with
-// the second, 71 with the first.
+// of 128 channels): 16 sequences of up to 16384 positions, 4 rows, 95 us with
+// the second, 69 with the first.
 constexpr int kLogitRows = 8;
 
 Split plan(const Cache &c, int64_t n_seq, int64_t rows, int64_t max_len, bool scores, int cus) {
@@ -197,7 +211,19 @@ Split plan(const Cache &c, int64_t n_seq, int64_t rows, int64_t max_len, bool sc
     s.n_split = (int)((max_len + s.chunk - 1) / s.chunk);
     if (s.n_split < 1) s.n_split = 1;
     const uint64_t heads = (uint64_t)n_seq * c.heads;
-    if (s.n_split > 1) {
+    const int64_t groups = (int64_t)cus * tkv::kMostResident;
+    s.even = s.row_tile <= 32 && s.chunk > kLeastChunk && n_seq <= tkv::kEvenSeqs &&
+             (units < groups || max_len > kLongForOne) && units * (max_len / kLeastChunk + 1) < (1 << 28);
+    if (s.even) {
+        s.n_split = (int)(groups / units + 2);
+        const uint64_t parts = (uint64_t)(units + groups) * (rows < s.row_tile ? rows : s.row_tile);
+        s.part_o = s.total;
+        s.total = up(s.total + parts * c.dim * 4, 256);
+        s.part_ml = s.total;
+        s.total = up(s.total + parts * 8, 256);
+        s.dealt = s.total;
+        s.total = up(s.total + (tkv::kEvenSeqs + 1) * 4, 256);
+    } else if (s.n_split > 1) {
         s.part_o = s.total;
         s.total = up(s.total + heads * s.n_split * rows * c.dim * 4, 256);
         s.part_ml = s.total;
@@ -339,6 +365,9 @@ tmap_status tkv_attend(const tkv_cache *cache, const tkv_attend_args *args, cons
     a.row_blocks = s.row_blocks;
     a.row_tiles = s.row_tiles;
     a.n_split = s.n_split;
+    a.even = s.even;
+    a.cus = cus;
+    while ((1 << a.row_shift) < s.row_tile) ++a.row_shift;
     while ((1 << a.chunk_shift) < s.chunk) ++a.chunk_shift;
     a.by_heads = divisor(a.c.heads);
     a.by_group_heads = divisor(a.group_heads);
@@ -348,6 +377,7 @@ tmap_status tkv_attend(const tkv_cache *cache, const tkv_attend_args *args, cons
     if (s.n_split > 1) {
         a.part_o = (float *)(ws + s.part_o);
         a.part_ml = (float *)(ws + s.part_ml);
+        a.dealt = (int32_t *)(ws + s.dealt);
     }
     if (a.scores_out) {
         if (a.rows <= kLogitRows)

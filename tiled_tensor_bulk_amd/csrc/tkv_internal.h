@@ -11,6 +11,8 @@ namespace tkv {
 
 constexpr uint32_t kMagic = 0x544B5634u;  // "TKV4"
 constexpr int kTile = 32;                 // positions of a record
+constexpr int kMostResident = 4;           // workgroups that an even split deals to a compute unit
+constexpr int kEvenSeqs = 256;            // most sequences of an even split
 constexpr float kLimit = 32000.0f;        // largest magnitude quantised: 15 * scale stays inside fp16
 
 // The decoded form of tkv_cache.
@@ -74,8 +76,13 @@ struct AttendArgs {
     int32_t max_len;
     int32_t chunk_shift;   // a workgroup has at most 1 << chunk_shift positions
     int32_t n_split;
-    float *part_o;         // [n_seq][heads][n_split][rows][dim]
-    float *part_ml;        // [n_seq][heads][n_split][rows][2]
+    int32_t even;          // the steps of all sequences are dealt evenly (Even), not in chunks
+    int32_t groups;        // ... to so many workgroups
+    int32_t cus;
+    int32_t *dealt;        // [kEvenSeqs + 1]: the line's steps before each sequence, and a share's
+    int32_t row_shift;     // log2 of a workgroup's rows
+    float *part_o;         // [parts][rows][dim], parts [n_seq][heads][n_split], or as Even numbers them
+    float *part_ml;        // [parts][rows][2]
     // with scores: what turns products into weights, and either the logarithms
     // of a few rows' products or the queries as the matrix unit takes them
     float *logits;         // [n_seq][heads][records of max_len][rows][32], or nullptr

@@ -14,6 +14,13 @@
 // maxima and 4 conversions, some 72 instruction slots of 4 cycles next to 19
 // matrix instructions of 16.  So z * (sum of q) is one more matrix product: the
 // sum of a row's q over a group is held as three fp16 numbers, 33 bits in all.
+//
+// Measured: 2 sequences of up to 8192 positions, the last 512 of them new, 8
+// heads of 4 rows of 128 channels: 150 us, 640 TFLOP/s of products, where a
+// large matrix product reaches 1160.  128 rows a workgroup (NT = 2) share an
+// unpacked record: 177 us with 8 waves of 16, which read LDS twice as much, and
+// 422 with 4 tiles a wave, which are out of registers.  A step of the softmax
+// for each record, with V in registers, took 180.
 #pragma once
 
 #include "tkv_attend.h"

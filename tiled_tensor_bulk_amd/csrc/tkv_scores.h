@@ -10,6 +10,10 @@
 // the same tiles, four at a time from LDS, each of which one wave loads there
 // while the four before are worked on.  One wave adds up a position, in the
 // order of the rows.
+//
+// Bound by the vector units, which take an exponential for each row and
+// position: 2 sequences of up to 8192 positions, 512 tokens of 32 heads on 8, 78
+// us, 610 TFLOP/s of products.
 #pragma once
 
 #include "tkv_attend.h"
