@@ -17,8 +17,9 @@
 //
 // 8 sequences of up to 32768 positions to 8192, 8 heads of 128 channels:
 // choosing 25 us, a pass over LDS for each of three digits by the one workgroup
-// that a row has; moving 77 us for 137 MB written and, as kept positions share
-// 128-byte lines of source words with others, the source read nearly whole.
+// that a row has; moving 70 us for 74 MB written and, as kept positions share
+// 128-byte lines of source words with others, the source read nearly whole (77
+// with each load under its own test of the page, and so a wait for each).
 #include "tkv_format.h"
 
 namespace tkv {
@@ -223,6 +224,7 @@ __global__ void __launch_bounds__(kSelectThreads) select_kernel(const EvictArgs 
 template <int D, int GROUP>
 __global__ void __launch_bounds__(64 * kEvictWaves) move_kernel(const EvictArgs a, const int tiles) {
     using F = Format<D, GROUP>;
+    constexpr int PAIRS = (F::NG + 3) / 4, JS = F::W > 4 ? 4 : 8;
     const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, g = lane >> 4, m = lane & 15;
     const int64_t unit = (int64_t)blockIdx.x * kEvictWaves + wave;
     const int tile = (int)(unit % tiles);
@@ -240,63 +242,78 @@ __global__ void __launch_bounds__(64 * kEvictWaves) move_kernel(const EvictArgs 
     int pos = -1;
     if (lane < kTile && tile * kTile + lane < n) pos = a.kept[row * a.budget + tile * kTile + lane];
     const int page = pos < 0 ? -1 : page_at(table, a.b.table_width, a.c.n_pages, pos >> a.c.page_shift);
-    const char *src = page < 0 ? nullptr : record_at(a.c, page, head, pos / kTile);
+    if (page < 0) pos = -1;
+    // what has no source reads the destination's record, and drops it
+    const char *src = page < 0 ? dst : record_at(a.c, page, head, pos / kTile);
     const uint32_t src_lo = (uint32_t)(uint64_t)src, src_hi = (uint32_t)((uint64_t)src >> 32);
     const auto record_of = [&](int i) {
         return (const char *)(global_char *)(((uint64_t)(uint32_t)__shfl((int)src_hi, i) << 32) |
                                              (uint32_t)__shfl((int)src_lo, i));
     };
+    // All loads of K and the pairs, then of V's words for JS codes at a time: no
+    // load waits for another's.
+    uint32_t key[2][F::W], kp[2][PAIRS];
+    uint16_t vs[2][PAIRS], vz[2][PAIRS];
 #pragma unroll
     for (int half = 0; half < 2; ++half) {
         const char *rec = record_of(16 * half + m);
         const int place = __shfl(pos, 16 * half + m) & 31;
         const int from_half = place >> 4, from_lane = 16 * g + (place & 15);
 #pragma unroll
-        for (int s = 0; s < F::S; ++s) {
-            uint32_t word[F::WV];
-#pragma unroll
-            for (int w = 0; w < F::WV; ++w) word[w] = 0;
-            if (rec) load_words<F::WV>(rec + (((from_half * F::S + s) * 64 + from_lane) * F::WV) * 4, word);
-            store_words<F::WV>(dst + (((half * F::S + s) * 64 + lane) * F::WV) * 4, word);
-        }
+        for (int s = 0; s < F::S; ++s)
+            load_words<F::WV>(rec + (((from_half * F::S + s) * 64 + from_lane) * F::WV) * 4, key[half] + s * F::WV);
         // lane g takes every fourth group's pairs of position m
         const int from_slot = 8 * ((place & 15) >> 2) + 4 * from_half + (place & 3);
-        const int to_slot = 8 * (m >> 2) + 4 * half + (m & 3);
 #pragma unroll
-        for (int base = 0; base < F::NG; base += 4) {
-            const int grp = base + g;
-            if (grp < F::NG) {
-                uint32_t kp = 0;
-                uint16_t vs = 0, vz = 0;
-                if (rec) {
-                    kp = *reinterpret_cast<const uint32_t *>(rec + F::KP + (grp * kTile + place) * 4);
-                    const uint16_t *vp = reinterpret_cast<const uint16_t *>(rec + F::VP) + grp * 64 + from_slot;
-                    vs = vp[0], vz = vp[32];
-                }
-                *reinterpret_cast<uint32_t *>(dst + F::KP + (grp * kTile + 16 * half + m) * 4) = kp;
-                uint16_t *vp = reinterpret_cast<uint16_t *>(dst + F::VP) + grp * 64 + to_slot;
-                vp[0] = vs, vp[32] = vz;
-            }
+        for (int i = 0; i < PAIRS; ++i) {
+            const int grp = 4 * i + g < F::NG ? 4 * i + g : 0;
+            const uint16_t *vp = reinterpret_cast<const uint16_t *>(rec + F::VP) + grp * 64 + from_slot;
+            kp[half][i] = *reinterpret_cast<const uint32_t *>(rec + F::KP + (grp * kTile + place) * 4);
+            vs[half][i] = vp[0], vz[half][i] = vp[32];
         }
     }
     uint32_t word[2 * F::W];
 #pragma unroll
     for (int w = 0; w < 2 * F::W; ++w) word[w] = 0;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        const int i = 4 * g + (j & 3) + 16 * (j >> 2);
-        const char *rec = record_of(i);
-        const int place = __shfl(pos, i) & 31;
-        const int from_lane = 16 * ((place & 15) >> 2) + m, from_j = (place & 3) + 4 * (place >> 4);
-        const int from_shift = 4 * nibble_of(from_j);
-        if (rec) {
+    for (int js = 0; js < 8; js += JS) {
+        uint32_t x[JS][2 * F::W];
+        int at[JS];
 #pragma unroll
-            for (int hs = 0; hs < 2 * F::S; ++hs) {
-                uint32_t x[F::WV];
-                load_words<F::WV>(rec + F::VC + ((hs * 64 + from_lane) * F::WV) * 4, x);
+        for (int j = 0; j < JS; ++j) {
+            const int i = 4 * g + ((js + j) & 3) + 16 * ((js + j) >> 2);
+            const char *rec = record_of(i);
+            at[j] = __shfl(pos, i);
+            const int from_lane = 16 * ((at[j] & 15) >> 2) + m;
 #pragma unroll
-                for (int w = 0; w < F::WV; ++w)
-                    word[hs * F::WV + w] |= ((x[w] >> from_shift) & 15u) << (4 * nibble_of(j));
+            for (int hs = 0; hs < 2 * F::S; ++hs)
+                load_words<F::WV>(rec + F::VC + ((hs * 64 + from_lane) * F::WV) * 4, x[j] + hs * F::WV);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int j = 0; j < JS; ++j) {
+            const int from_shift = 4 * nibble_of((at[j] & 3) + ((at[j] & 16) >> 2));
+            const uint32_t mask = at[j] < 0 ? 0u : 15u;
+#pragma unroll
+            for (int w = 0; w < 2 * F::W; ++w) word[w] |= ((x[j][w] >> from_shift) & mask) << (4 * nibble_of(js + j));
+        }
+    }
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+        const bool there = __shfl(pos, 16 * half + m) >= 0;
+#pragma unroll
+        for (int w = 0; w < F::W; ++w) key[half][w] = there ? key[half][w] : 0;
+#pragma unroll
+        for (int s = 0; s < F::S; ++s)
+            store_words<F::WV>(dst + (((half * F::S + s) * 64 + lane) * F::WV) * 4, key[half] + s * F::WV);
+        const int to_slot = 8 * (m >> 2) + 4 * half + (m & 3);
+#pragma unroll
+        for (int i = 0; i < PAIRS; ++i) {
+            const int grp = 4 * i + g;
+            if (grp < F::NG) {
+                uint16_t *vp = reinterpret_cast<uint16_t *>(dst + F::VP) + grp * 64 + to_slot;
+                *reinterpret_cast<uint32_t *>(dst + F::KP + (grp * kTile + 16 * half + m) * 4) = there ? kp[half][i] : 0;
+                vp[0] = there ? vs[half][i] : 0, vp[32] = there ? vz[half][i] : 0;
             }
         }
     }
