@@ -210,7 +210,8 @@ def tkv_attend(cache: tkv_cache, q, table, lens, starts=None, max_new: Optional[
 
 def tkv_attend_workspace(cache: tkv_cache, n_seq: int, q_heads: int, max_new: int, max_len: int,
                          scores: bool = False) -> int:
-    """Bytes of workspace for tkv_attend with at most max_new tokens a sequence and positions below max_len."""
+    """Bytes of workspace for a tkv_attend call to which these max_new and max_len are given (smaller ones may need
+    more, as the work is then split in another way)."""
     width = -(-max_len // cache.page_tokens)
     t = tkv_tokens(None, 0, 0, _DTYPES[torch.bfloat16])
     a = tkv_attend_args(t, t, None, None, 4 if scores else None, max_len, q_heads, max_len, 1.0, 0, None, 0)
