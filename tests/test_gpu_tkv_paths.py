@@ -183,6 +183,52 @@ def test_attend_even_shares_over_many_sequences(n, longest):
     even_batch(rng, 64, 64, 8, 2, "bf16", lens, new, True, False, 600)
 
 
+def test_even_shares_in_a_graph():
+    """The shares go by the lengths in device memory: a captured call follows them from replay to replay, and gives the
+    same bits as an eager one."""
+    say("even graph")
+    rng = np.random.default_rng(3)
+    n, heads, gh, dim, page, width = 3, 2, 4, 128, 32, 24000
+    held = 1300 // page + 1
+    table = np.full((n, width), -1, np.int32)
+    table[:, :held] = rng.permutation(n * held).reshape(n, held)
+    ref = a_ref(rng, n * held, heads, dim, page, 64, table, [1300] * n)
+    cache, pool = a_cache(ref)
+    tab, lens = ints(table), ints([700, 1, 64])
+    qt, q = typed(rng.standard_normal((n, heads * gh, dim)), "bf16")
+    out, lse = torch.empty_like(qt), torch.empty((n, heads * gh), device=DEV)
+    ws = torch.empty(T.tkv_attend_workspace(cache, n, heads * gh, 1, width * page), dtype=torch.uint8, device=DEV)
+    T.tkv_attend(cache, qt, tab, lens, out=out, lse=lse, workspace=ws)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        T.tkv_attend(cache, qt, tab, lens, out=out, lse=lse, workspace=ws)
+    for now in ([700, 1, 64], [1300, 1299, 1], [0, 1300, 0], [0, 0, 0], [129, 128, 127]):
+        lens.copy_(ints(now))
+        out.fill_(7)
+        graph.replay()
+        torch.cuda.synchronize()
+        eager = T.tkv_attend(cache, qt, tab, lens)
+        assert torch.equal(out, eager[0]) and torch.equal(lse, eager[1])
+        o, ls, _, mags = tkv_ref.attend(ref, table, now, np.arange(n + 1), q, dim ** -0.5, True)
+        check_attend((out, lse), (o, ls), mags, "bf16", dim)
+
+
+@pytest.mark.parametrize("n,length", [(1, 512), (1, 513), (2, 900), (9, 2100)])
+def test_attend_chunks_by_how_many_there_are(n, length):
+    """One chunk, chunks of 256 and of 512."""
+    say(f"chunks {n} {length}")
+    rng = np.random.default_rng(length)
+    heads, gh, dim, page = 8, 2, 64, 64
+    lens = [length - 5 * i for i in range(n)]
+    table, _ = tables(rng, n, -(-length // page))
+    ref = a_ref(rng, table.size, heads, dim, page, 64, table, lens)
+    cache, _ = a_cache(ref)
+    qt, q = typed(rng.standard_normal((n, heads * gh, dim)), "f16")
+    out, lse, _, mags = tkv_ref.attend(ref, table, lens, np.arange(n + 1), q, dim ** -0.5, True)
+    check_attend(T.tkv_attend(cache, qt, ints(table), ints(lens), max_len=length), (out, lse), mags, "f16", dim)
+
+
 @pytest.mark.parametrize("gh,new", [(2, 5), (3, 40)])
 def test_rows_that_see_nothing(gh, new):
     """More new tokens than cached positions: the first of them see none."""

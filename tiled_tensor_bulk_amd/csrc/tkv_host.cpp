@@ -175,7 +175,10 @@ uint64_t up(uint64_t v, uint64_t to) { return (v + to - 1) / to * to; }
 // of many (512 new tokens over 8192 positions, 2 sequences: 217 us with 2, 307
 // with 1, 243 with 4), and at least 512 positions, as each costs a partial sum:
 // 16 sequences of up to 4099 positions, 22.7 us, at least 256 22.1, 1024 24.8;
-// 12 of up to 8191, 18.2, 20.5 and 17.0.  Powers of two, so that another bound
+// 12 of up to 8191, 18.2, 20.5 and 17.0.  Few rows have chunks of 256 as long
+// as that is no more than 2 workgroups for a compute unit: 8 heads, 1 sequence of
+// 2000 positions 10.7 us, 512 at least 12.3; 16 of 1000 12.1 and 12.8; but 16 of
+// 2000 17.0 and 15.8.  Powers of two, so that another bound
 // on the lengths mostly leaves the order of sums as it is.
 //
 // The host does not know the lengths, though, and where chunks are long a block
@@ -207,6 +210,7 @@ Split plan(const Cache &c, int64_t n_seq, int64_t rows, int64_t max_len, bool sc
     const int64_t units = n_seq * c.heads * s.row_blocks;
     s.chunk = kLeastChunk;
     const int64_t most = (int64_t)cus * (s.row_tile <= 32 ? kBlocksPerCu : kRowBlocksPerCu);
+    if (s.row_tile <= 32 && max_len > kLeastChunk && units * ((max_len + 255) / 256) <= (int64_t)cus * 2) s.chunk = 256;
     while (s.chunk < kMostChunk && units * ((max_len + s.chunk - 1) / s.chunk) > most) s.chunk *= 2;
     s.n_split = (int)((max_len + s.chunk - 1) / s.chunk);
     if (s.n_split < 1) s.n_split = 1;
