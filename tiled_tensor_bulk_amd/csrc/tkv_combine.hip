@@ -16,41 +16,52 @@ namespace tkv {
 
 constexpr int kCombineThreads = 256;
 constexpr int kFewParts = 16;
+constexpr int kWeighPositions = 4 * kCombineThreads;
+
+// Where a row's partial sums are: part s at first + s * stride.
+struct Parts {
+    int n, stride;  // n 0: the row has been written where it was computed
+    int64_t first;
+    __device__ __forceinline__ Parts(const AttendArgs &a, const Extent &e, int unit, int seq, int head, int row) {
+        if (a.even) {
+            const int rows = 1 << a.row_shift, steps = Even::steps(e), block = row >> a.row_shift;
+            const uint32_t share = (uint32_t)a.dealt[kEvenSeqs];
+            const uint32_t from = (uint32_t)(a.dealt[seq] + Even::kLead +
+                                             (head * Even::blocks(a, e) + block) * (steps + Even::kLead));
+            const uint32_t part = from / share;
+            n = (int)((from + steps - 1) / share - part) + 1;
+            n = n == 1 ? 0 : n;
+            stride = a.rows < rows ? a.rows : rows;
+            first = ((int64_t)unit * a.row_blocks + block + part) * stride + (row & (rows - 1));
+        } else {
+            n = Chunks(a, e.len).n;
+            stride = a.rows;
+            first = (int64_t)unit * a.n_split * a.rows + row;
+        }
+    }
+};
 
 template <int D, int PARTS>
-__global__ void __launch_bounds__(kCombineThreads) combine_few_kernel(const AttendArgs a) {
+__device__ __forceinline__ void combine_few(const AttendArgs &a, int workgroup) {
     constexpr int LANES = D / 4, AT_ONCE = kCombineThreads / LANES;
     const int which = threadIdx.x / LANES, lane = threadIdx.x % LANES;
-    int row = blockIdx.x * AT_ONCE + which;
+    int row = workgroup * AT_ONCE + which;
     const int unit = divide(row, a.rows, a.by_rows);
     int head = unit;
     const int seq = divide(head, (int)a.c.heads, a.by_heads);
     if (which >= AT_ONCE || seq >= a.b.n_seq) return;
     const Extent e(a, seq);
     if (row >= e.rows) return;
-    int parts, part_rows = a.rows;
-    int64_t first;
-    if (a.even) {
-        const int rows = 1 << a.row_shift, steps = Even::steps(e), block = row >> a.row_shift;
-        const uint32_t share = (uint32_t)a.dealt[kEvenSeqs];
-        const uint32_t from = (uint32_t)(a.dealt[seq] + (head * Even::blocks(a, e) + block) * (steps + Even::kLead) + Even::kLead);
-        const uint32_t part = from / share;
-        parts = (int)((from + steps - 1) / share - part) + 1;
-        if (parts == 1) return;  // written where it was computed
-        part_rows = part_rows < rows ? part_rows : rows;
-        first = ((int64_t)unit * a.row_blocks + block + part) * part_rows + (row & (rows - 1));
-    } else {
-        parts = Chunks(a, e.len).n;
-        first = ((int64_t)unit * a.n_split) * a.rows + row;
-    }
+    const Parts parts(a, e, unit, seq, head, row);
+    if (parts.n == 0) return;
     float best = kFar, sum = 0.0f;
     f4 y = (f4){0, 0, 0, 0};
-    for (int base = 0; base < parts; base += PARTS) {  // once, but for an even split's longest
+    for (int base = 0; base < parts.n; base += PARTS) {
         float2 ml[PARTS];
         f4 o[PARTS];
 #pragma unroll
         for (int s = 0; s < PARTS; ++s) {  // past the last one: it again, without weight
-            const int64_t from = first + (int64_t)(base + s < parts ? base + s : parts - 1) * part_rows;
+            const int64_t from = parts.first + (int64_t)(base + s < parts.n ? base + s : parts.n - 1) * parts.stride;
             ml[s] = *reinterpret_cast<const float2 *>(a.part_ml + 2 * from);
             o[s] = *reinterpret_cast<const f4 *>(a.part_o + from * D + 4 * lane);
         }
@@ -61,13 +72,18 @@ __global__ void __launch_bounds__(kCombineThreads) combine_few_kernel(const Atte
         best = m, sum *= f, y *= f;
 #pragma unroll
         for (int s = 0; s < PARTS; ++s)
-            if (base + s < parts) {
+            if (base + s < parts.n) {
                 const float f = exp2f(ml[s].x - best);
                 sum += f * ml[s].y;
                 y += f * o[s];
             }
     }
     write_row(a, e, seq, head, row, 4 * lane, y, best, sum);
+}
+
+template <int D, int PARTS>
+__global__ void __launch_bounds__(kCombineThreads) combine_few_kernel(const AttendArgs a) {
+    combine_few<D, PARTS>(a, blockIdx.x);
 }
 
 template <int D>
@@ -114,52 +130,103 @@ __global__ void __launch_bounds__(kCombineThreads) combine_kernel(const AttendAr
     write_row(a, e, seq, head, row, channel, y, best, sum);
 }
 
-template <int D>
-static int launch(const AttendArgs &a, hipStream_t s) {
-    const int64_t rows = (int64_t)a.b.n_seq * a.c.heads * a.rows;
-    constexpr int AT_ONCE = kCombineThreads / (D / 4);
-    if (a.n_split <= 4)  // an even split: its usual number
-        combine_few_kernel<D, 4><<<dim3((uint32_t)((rows + AT_ONCE - 1) / AT_ONCE)), dim3(kCombineThreads), 0, s>>>(a);
-    else if (a.even || a.n_split <= kFewParts)
-        combine_few_kernel<D, kFewParts><<<dim3((uint32_t)((rows + AT_ONCE - 1) / AT_ONCE)), dim3(kCombineThreads), 0, s>>>(a);
-    else
-        combine_kernel<D><<<dim3((uint32_t)(rows * (D / 32))), dim3(kCombineThreads), 0, s>>>(a);
-    return (int)hipGetLastError();
-}
-
 // scores_out = scores_in + the weights of a few rows, exp2(y - lse2), summed,
 // from the logarithms that the first kernel has kept: masked ones are -inf.
-// A lane takes 4 positions.  Memory bounds it: 16 sequences of up to 16384
-// positions, 8 heads of 4 rows, 9 us for 32 MB, some of it still in the caches.
-__global__ void __launch_bounds__(256) weigh_kernel(const AttendArgs a, const int blocks) {
-    const int64_t unit = blockIdx.x / (uint32_t)blocks;
-    const int block = blockIdx.x % (uint32_t)blocks;
-    int head = (int)unit;
+// A lane takes 4 positions.  JOIN: lse2 comes of the partial sums, so that this
+// need not wait for them to be joined.
+template <bool JOIN>
+__device__ __forceinline__ void weigh(const AttendArgs &a, int workgroup, int blocks) {
+    __shared__ float joined[kLogitRows];
+    const int unit = workgroup / blocks, block = workgroup % blocks;
+    int head = unit;
     const int seq = divide(head, (int)a.c.heads, a.by_heads);
     const Extent e(a, seq);
-    const int pos = (block * 256 + (int)threadIdx.x) * 4;
-    if (pos >= e.len) return;
+    if (block * kWeighPositions >= e.len) return;
+    const int pos = block * kWeighPositions + (int)threadIdx.x * 4;
     const int64_t records = (a.max_len + kTile - 1) / kTile;
     const float *y = a.logits + (unit * records + pos / kTile) * a.rows * kTile + (pos & (kTile - 1));
-    const float *info = a.row_info + unit * 16 * 2;
-    f4 sum = {0, 0, 0, 0};
-    for (int r = 0; r < e.rows; ++r) {
-        const f4 x = *reinterpret_cast<const f4 *>(y + r * kTile);
-        const float lse2 = info[2 * r + 1];
+    const float *info = a.row_info + (int64_t)unit * 16 * 2;
+    f4 x[kLogitRows];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) sum[i] += __builtin_amdgcn_exp2f(x[i] - lse2);
+    for (int r = 0; r < kLogitRows; ++r)
+        if (r < e.rows && pos < e.len) x[r] = *reinterpret_cast<const f4 *>(y + r * kTile);
+    if (JOIN) {
+        const int r = threadIdx.x / 32, lane = threadIdx.x % 32;
+        static_assert(kLogitRows * 32 == kCombineThreads, "32 lanes for each row");
+        if (r < e.rows) {
+            const Parts parts(a, e, unit, seq, head, r);
+            float best = kFar, sum = 0.0f;
+            for (int s = lane; s < parts.n; s += 32) {
+                const float2 ml = *reinterpret_cast<const float2 *>(a.part_ml + 2 * (parts.first + (int64_t)s * parts.stride));
+                const float m = fmaxf(best, ml.x);
+                sum = sum * exp2f(best - m) + ml.y * exp2f(ml.x - m);
+                best = m;
+            }
+#pragma unroll
+            for (int mask = 16; mask; mask >>= 1) {
+                const float other = __shfl_xor(best, mask), m = fmaxf(best, other);
+                sum = sum * exp2f(best - m) + __shfl_xor(sum, mask) * exp2f(other - m);
+                best = m;
+            }
+            const float lse2 = sum > 0.0f || sum != sum ? best - kLift + log2f(sum) : __builtin_inff();
+            if (lane == 0) joined[r] = parts.n ? lse2 : info[2 * r + 1];
+        }
+        __syncthreads();
     }
+    if (pos >= e.len) return;
+    f4 sum = {0, 0, 0, 0};
+#pragma unroll
+    for (int r = 0; r < kLogitRows; ++r)
+        if (r < e.rows) {
+            const float lse2 = JOIN ? joined[r] : info[2 * r + 1];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) sum[i] += __builtin_amdgcn_exp2f(x[r][i] - lse2);
+        }
     const int64_t at = unit * a.score_stride + pos;
 #pragma unroll
     for (int i = 0; i < 4; ++i)
         if (pos + i < e.len) a.scores_out[at + i] = (a.scores_in ? a.scores_in[at + i] : 0.0f) + sum[i];
 }
 
-int launch_weigh(const AttendArgs &a, void *stream) {
-    const int blocks = (a.max_len + 1023) / 1024;
-    const int64_t grid = (int64_t)a.b.n_seq * a.c.heads * blocks;
-    if (grid == 0) return 0;
-    weigh_kernel<<<dim3((uint32_t)grid), dim3(256), 0, (hipStream_t)stream>>>(a, blocks);
+__global__ void __launch_bounds__(kCombineThreads) weigh_kernel(const AttendArgs a, const int blocks) {
+    weigh<false>(a, blockIdx.x, blocks);
+}
+
+// Joining and weighing in one launch, where a row has few parts: 16 sequences of
+// up to 16384 positions, 8 heads of 4 rows, 11.5 us, where two take 5.1 and 9.0.
+// The logarithms, 20 MB mostly in the caches yet, are less of it than the way to
+// the partial sums by lengths and shares.
+template <int D>
+__global__ void __launch_bounds__(kCombineThreads) combine_weigh_kernel(const AttendArgs a, const int combining,
+                                                                        const int blocks) {
+    if ((int)blockIdx.x < combining)
+        combine_few<D, 4>(a, blockIdx.x);
+    else
+        weigh<true>(a, blockIdx.x - combining, blocks);
+}
+
+template <int D>
+static int launch(const AttendArgs &a, hipStream_t s) {
+    const int64_t rows = (int64_t)a.b.n_seq * a.c.heads * a.rows;
+    constexpr int AT_ONCE = kCombineThreads / (D / 4);
+    const int combining = (int)((rows + AT_ONCE - 1) / AT_ONCE);
+    const int blocks = (a.max_len + kWeighPositions - 1) / kWeighPositions;
+    const int64_t weighing = a.logits ? (int64_t)a.b.n_seq * a.c.heads * blocks : 0;
+    const dim3 block(kCombineThreads);
+    const bool few = a.even || a.n_split <= kFewParts;
+    if (a.n_split > 1) {
+        if (few && weighing) {
+            combine_weigh_kernel<D><<<dim3((uint32_t)(combining + weighing)), block, 0, s>>>(a, combining, blocks);
+            return (int)hipGetLastError();
+        }
+        if (a.n_split <= 4)  // an even split: its usual number
+            combine_few_kernel<D, 4><<<dim3((uint32_t)combining), block, 0, s>>>(a);
+        else if (few)
+            combine_few_kernel<D, kFewParts><<<dim3((uint32_t)combining), block, 0, s>>>(a);
+        else
+            combine_kernel<D><<<dim3((uint32_t)(rows * (D / 32))), block, 0, s>>>(a);
+    }
+    if (weighing) weigh_kernel<<<dim3((uint32_t)weighing), block, 0, s>>>(a, blocks);
     return (int)hipGetLastError();
 }
 

@@ -196,11 +196,6 @@ constexpr int kMostChunk = 1 << 16;
 constexpr int kLongForOne = 1 << 14;
 constexpr int kBlocksPerCu = 8;
 constexpr int kRowBlocksPerCu = 2;
-// Scores of up to so many rows go by logarithms kept in memory, 8 bytes a row
-// and position written and read, against half of a record read again (72 bytes
-// of 128 channels): 16 sequences of up to 16384 positions, 4 rows, 95 us with
-// the second, 69 with the first.
-constexpr int kLogitRows = 8;
 
 Split plan(const Cache &c, int64_t n_seq, int64_t rows, int64_t max_len, bool scores, int cus) {
     Split s{};
@@ -235,7 +230,7 @@ Split plan(const Cache &c, int64_t n_seq, int64_t rows, int64_t max_len, bool sc
     }
     if (scores) {
         s.frag_q = s.total;
-        if (rows <= kLogitRows)
+        if (rows <= tkv::kLogitRows)
             s.total = up(s.total + heads * up((uint64_t)max_len, tkv::kTile) * rows * 4, 256);
         else
             s.total = up(s.total + heads * s.row_tiles * (32 * c.dim + 1024), 256);
@@ -384,7 +379,7 @@ tmap_status tkv_attend(const tkv_cache *cache, const tkv_attend_args *args, cons
         a.dealt = (int32_t *)(ws + s.dealt);
     }
     if (a.scores_out) {
-        if (a.rows <= kLogitRows)
+        if (a.rows <= tkv::kLogitRows)
             a.logits = (float *)(ws + s.frag_q);
         else
             a.frag_q = ws + s.frag_q;

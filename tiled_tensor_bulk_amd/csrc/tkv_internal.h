@@ -13,6 +13,11 @@ constexpr uint32_t kMagic = 0x544B5634u;  // "TKV4"
 constexpr int kTile = 32;                 // positions of a record
 constexpr int kMostResident = 4;           // workgroups that an even split deals to a compute unit
 constexpr int kEvenSeqs = 256;            // most sequences of an even split
+// Scores of up to so many rows go by logarithms kept in memory, 8 bytes a row
+// and position written and read, against half of a record read again (72 bytes
+// of 128 channels): 16 sequences of up to 16384 positions, 4 rows, 95 us with
+// the second, 69 with the first.
+constexpr int kLogitRows = 8;
 constexpr float kLimit = 32000.0f;        // largest magnitude quantised: 15 * scale stays inside fp16
 
 // The decoded form of tkv_cache.
@@ -118,7 +123,6 @@ int launch_attend_d96(const AttendArgs &a, int row_tile, void *stream);
 int launch_attend_d128(const AttendArgs &a, int row_tile, void *stream);
 int launch_attend_d256(const AttendArgs &a, int row_tile, void *stream);
 int launch_combine(const AttendArgs &a, void *stream);
-int launch_weigh(const AttendArgs &a, void *stream);
 int launch_evict(const EvictArgs &a, void *stream);
 
 }  // namespace tkv

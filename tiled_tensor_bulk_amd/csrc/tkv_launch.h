@@ -44,9 +44,8 @@ static int launch_group(AttendArgs a, int row_tile, void *stream) {
     hipStream_t s = (hipStream_t)stream;
     int rc = a.q.type == kBf16 ? launch_type<D, GROUP, true>(a, row_tile, stream)
                                : launch_type<D, GROUP, false>(a, row_tile, stream);
-    if (rc == 0 && a.n_split > 1) rc = launch_combine(a, stream);
-    if (rc == 0 && a.logits) return launch_weigh(a, stream);
-    if (rc == 0 && a.scores_out && a.max_len > 0) {
+    if (rc == 0 && (a.n_split > 1 || a.logits)) rc = launch_combine(a, stream);
+    if (rc == 0 && a.scores_out && !a.logits && a.max_len > 0) {
         constexpr int kPositions = kTile * kAttendWaves;
         const int64_t splits = (a.max_len + kPositions - 1) / kPositions;
         scores_kernel<D, GROUP><<<dim3((uint32_t)(splits * a.c.heads * a.b.n_seq)), block, 0, s>>>(a);
