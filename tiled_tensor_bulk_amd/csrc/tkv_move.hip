@@ -13,7 +13,6 @@
 // 17 instructions to quantise an element.  8 prompts of up to 4001 tokens, 25
 // thousand in all, 8 heads of 128 channels: append 47 us for 131 MB, 2.8 TB/s, of
 // which the instructions alone are 29; read into fp32 50 us for 234 MB, 4.7 TB/s,
-// what a copy reaches.
 #include "tkv_format.h"
 
 namespace tkv {
@@ -314,7 +313,8 @@ __global__ void __launch_bounds__(64 * kMoveWaves) append_few_kernel(const MoveA
     }
 }
 
-// Positions out of the cache: V codes through LDS as above; then a lane takes 8
+// Positions out of the cache, keys and values by a wave each: V codes go through
+// LDS as above; then a lane takes 8
 // channels of a position, neighbouring lanes the next 8, so that a position's
 // row is written in one run.
 template <int D, int GROUP>
@@ -322,65 +322,69 @@ __global__ void __launch_bounds__(64 * kMoveWaves) read_kernel(const MoveArgs a)
     using F = Format<D, GROUP>;
     constexpr int PITCH = D + 8;
     constexpr int LANES = D / 8, AT_ONCE = 64 / LANES;  // of a position, and positions
-    __shared__ __attribute__((aligned(8))) uint8_t codes[kMoveWaves][kTile * PITCH];
+    __shared__ __attribute__((aligned(8))) uint8_t codes[kMoveWaves / 2][kTile * PITCH];
     const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, g = lane >> 4, m = lane & 15;
+    const bool values = wave & 1;
     Unit u;
-    if (!unit_of(a, blockIdx.x * kMoveWaves + wave, u)) return;
-    uint8_t *mine = codes[wave];
+    if (!unit_of(a, blockIdx.x * (kMoveWaves / 2) + (wave >> 1), u)) return;
+    uint8_t *mine = codes[wave >> 1];  // of the wave with the values alone
     const int p0 = u.tile * kTile;
-    if (u.rec) {
-#pragma unroll
-        for (int hs = 0; hs < 2 * F::S; ++hs) {
-            uint32_t word[F::WV];
-            load_words<F::WV>(u.rec + F::VC + ((hs * 64 + lane) * F::WV) * 4, word);
-#pragma unroll
-            for (int w = 0; w < F::WV; ++w)
-#pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    mine[(4 * g + (j & 3) + 16 * (j >> 2)) * PITCH + 16 * (hs * F::WV + w) + m] =
-                        (uint8_t)((word[w] >> (4 * nibble_of(j))) & 15);
-        }
-    }
-    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-    __builtin_amdgcn_wave_barrier();
-    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
     const int which = lane / LANES, ch = 8 * (lane % LANES), grp = ch / GROUP, i = ch / 32, kg = ch % 32 / 8;
-    if (which >= AT_ONCE) return;
     // all that is read first: no step waits for another's
     constexpr int STEPS = (kTile + AT_ONCE - 1) / AT_ONCE;
     uint32_t word[STEPS];
-    h2 kp[STEPS], vp[STEPS];
-    if (u.rec) {
+    h2 pair[STEPS];
+    if (u.rec && values) {
+        uint32_t own[2 * F::W];
+#pragma unroll
+        for (int hs = 0; hs < 2 * F::S; ++hs)
+            load_words<F::WV>(u.rec + F::VC + ((hs * 64 + lane) * F::WV) * 4, own + hs * F::WV);
+#pragma unroll
+        for (int step = 0; step < STEPS; ++step) {
+            const int t = (step * AT_ONCE + which) & (kTile - 1), half = t >> 4, mt = t & 15;
+            const _Float16 *v = reinterpret_cast<const _Float16 *>(u.rec + F::VP) + grp * 64 + 8 * (mt >> 2) + 4 * half;
+            pair[step] = (h2){v[mt & 3], v[32 + (mt & 3)]};
+        }
+#pragma unroll
+        for (int w = 0; w < 2 * F::W; ++w)
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                mine[(4 * g + (j & 3) + 16 * (j >> 2)) * PITCH + 16 * w + m] =
+                    (uint8_t)((own[w] >> (4 * nibble_of(j))) & 15);
+        __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+        __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+    } else if (u.rec) {
 #pragma unroll
         for (int step = 0; step < STEPS; ++step) {
             const int t = (step * AT_ONCE + which) & (kTile - 1), half = t >> 4, mt = t & 15;
             word[step] = *reinterpret_cast<const uint32_t *>(
                 u.rec + (((half * F::S + i / F::WV) * 64 + 16 * kg + mt) * F::WV + i % F::WV) * 4);
-            kp[step] = *reinterpret_cast<const h2 *>(u.rec + F::KP + (grp * kTile + t) * 4);
-            const _Float16 *v = reinterpret_cast<const _Float16 *>(u.rec + F::VP) + grp * 64 + 8 * (mt >> 2) + 4 * half + (mt & 3);
-            vp[step] = (h2){v[0], v[32]};
+            pair[step] = *reinterpret_cast<const h2 *>(u.rec + F::KP + (grp * kTile + t) * 4);
         }
     }
+    if (which >= AT_ONCE) return;
+    const Tokens &to = values ? a.v : a.k;
 #pragma unroll
     for (int step = 0; step < STEPS; ++step) {
         const int t = step * AT_ONCE + which, n = p0 + t - u.first;
         if (t >= kTile || n < 0 || n >= u.n) continue;
-        float x[8], y[8];
+        float x[8];
         if (u.rec) {
-            const float ks = (float)kp[step][0], kz = (float)kp[step][1], vs = (float)vp[step][0], vz = (float)vp[step][1];
-            const uint2 c = *reinterpret_cast<const uint2 *>(mine + t * PITCH + ch);
+            const float scale = (float)pair[step][0], zero = (float)pair[step][1];
+            if (values) {
+                const uint2 c = *reinterpret_cast<const uint2 *>(mine + t * PITCH + ch);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                x[j] = fmaf(ks, (float)((word[step] >> (4 * nibble_of(j))) & 15), kz);
-                y[j] = fmaf(vs, (float)(((j < 4 ? c.x : c.y) >> (8 * (j & 3))) & 255), vz);
+                for (int j = 0; j < 8; ++j) x[j] = fmaf(scale, (float)(((j < 4 ? c.x : c.y) >> (8 * (j & 3))) & 255), zero);
+            } else {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) x[j] = fmaf(scale, (float)((word[step] >> (4 * nibble_of(j))) & 15), zero);
             }
         } else {
 #pragma unroll
-            for (int j = 0; j < 8; ++j) x[j] = y[j] = 0.0f;
+            for (int j = 0; j < 8; ++j) x[j] = 0.0f;
         }
-        const int64_t row = u.start + n;
-        store8(a.k, row * a.k.token_stride + u.head * a.k.head_stride + ch, x);
-        store8(a.v, row * a.v.token_stride + u.head * a.v.head_stride + ch, y);
+        store8(to, (u.start + n) * to.token_stride + u.head * to.head_stride + ch, x);
     }
 }
 
@@ -388,13 +392,13 @@ template <int D, int GROUP>
 static int launch_move(const MoveArgs &a, bool append, void *stream) {
     const int64_t units = (int64_t)a.b.n_seq * a.tiles * a.c.heads;
     const dim3 grid((uint32_t)((units + kMoveWaves - 1) / kMoveWaves)), block(64 * kMoveWaves);
+    const dim3 two_waves((uint32_t)((units * 2 + kMoveWaves - 1) / kMoveWaves));  // for a record
     if (append && a.b.max_new <= kFewTokens)
         append_few_kernel<D, GROUP><<<grid, block, 0, (hipStream_t)stream>>>(a);
     else if (append)
-        append_kernel<D, GROUP><<<dim3((uint32_t)((units * 2 + kMoveWaves - 1) / kMoveWaves)), block, 0,
-                                  (hipStream_t)stream>>>(a);
+        append_kernel<D, GROUP><<<two_waves, block, 0, (hipStream_t)stream>>>(a);
     else
-        read_kernel<D, GROUP><<<grid, block, 0, (hipStream_t)stream>>>(a);
+        read_kernel<D, GROUP><<<two_waves, block, 0, (hipStream_t)stream>>>(a);
     return (int)hipGetLastError();
 }
 
