@@ -119,7 +119,8 @@ tmap_status tkv_read(const tkv_cache *cache, const tkv_tokens *k, const tkv_toke
  * on key/value head a / (q_heads / n_heads), lse the logarithm of the
  * softmax's denominator.  lens[b] counts every cached position, the new
  * tokens' own included.  With causal, the i-th of n new tokens sees positions
- * below lens[b] - n + 1 + i, else all lens[b].  A row that sees no position
+ * below lens[b] - n + 1 + i, else all lens[b]; lens[b] itself counts there,
+ * also where it is more than the table holds.  A row that sees no position
  * gives 0 and lse -inf.
  *
  * With scores_out, also scores_out[b][h][p] = scores_in[b][h][p] + the sum

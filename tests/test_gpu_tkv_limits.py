@@ -1,0 +1,94 @@
+"""The operators on the 4-bit cache at the edges of their batches: lengths past what a table holds.  The plain
+implementation is tests/tkv_ref.py, asked for one new token at a time; tolerances are those of tests/test_gpu_tkv.py, and
+what is not a number fails."""
+import numpy as np
+import pytest
+
+from tests import tkv_ref
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+if not torch.cuda.is_available():
+    pytest.skip("no GPU", allow_module_level=True)
+
+from tests.test_gpu_tkv import DEV, T, a_cache, a_ref, bounds, ints, say, tables, to64, typed  # noqa: E402
+
+
+def attend_by_token(ref, table, lens, starts, q, scale, causal=True):
+    """out, lse, the weights [sequences, heads, positions] and the magnitudes of tkv_ref.attend, where the i-th of n new
+    tokens sees positions below lens[b] - n + 1 + i (all of lens[b] if not causal) as far as the table goes."""
+    n, hq, dim = q.shape
+    held = table.shape[1] * ref.page
+    out, lse = np.zeros((n, hq, dim)), np.full((n, hq), -np.inf)
+    mags = [np.zeros((n, hq, dim)), np.zeros((n, hq, dim)), np.zeros((n, hq))]
+    weights = np.zeros((len(lens), ref.heads, held))
+    none = np.zeros((1, ref.heads, held))
+    for b, length in enumerate(lens):
+        new = starts[b + 1] - starts[b]
+        for i in range(new):
+            row = starts[b] + i
+            sees = max(0, min(length - new + 1 + i if causal else length, held))
+            o, ls, w, m = tkv_ref.attend(ref, table[b:b + 1], [sees], [0, 1], q[row:row + 1], scale, False, none)
+            out[row], lse[row] = o[0], ls[0]
+            weights[b] += w[0]
+            for all_, one in zip(mags, m):
+                all_[row] = one[0]
+    return out, lse, weights, mags
+
+
+def check_numbers(got, want, mags, dtype, dim):
+    """As check_attend of tests/test_gpu_tkv.py, with comparisons that a NaN fails."""
+    out, lse = to64(got[0]), to64(got[1])
+    tol, tol_lse = bounds(want, mags, dtype, dim)
+    assert np.isfinite(tol).all()
+    empty = ~np.isfinite(want[1])
+    assert np.array_equal(lse[empty], want[1][empty]) and (out[empty] == 0).all()
+    assert np.isfinite(out).all()
+    good = np.abs(out - want[0]) <= tol
+    assert good.all(), (np.argwhere(~good)[:5], out[~good][:5], want[0][~good][:5], tol[~good][:5])
+    assert (np.abs(lse - want[1])[~empty] <= tol_lse[~empty]).all()
+
+
+def check_weights(have, weights, mags, rows, dim):
+    """scores_out that began at 0"""
+    worst = 2 * ((dim + 16) * 2.0 ** -24 * mags[2].max() + 2.0 ** -19)
+    tol = (worst + 2.0 ** -23 + 2.0 ** -24 * rows) * weights + 1e-30
+    assert (np.abs(have - weights) <= tol).all()
+
+
+# ------------------------------------------------------------------ lengths past the table
+
+PAST = [
+    # dim, group, heads, group heads, dtype, lens, new tokens: 64 positions are held
+    (128, 64, 2, 1, "bf16", [70, 64, 65], [8, 8, 3]),     # 8 rows: the logarithms are kept for the scores
+    (128, 64, 1, 3, "f16", [70, 500, 66], [8, 8, 1]),     # 24 rows
+    (64, 32, 1, 2, "bf16", [80, 40], [40, 40]),           # waves with rows of their own
+    (96, 32, 1, 1, "f16", [100, 63], [60, 63]),
+    (256, 64, 1, 4, "bf16", [67, 2000], [9, 12]),
+    (128, 128, 1, 2, "f16", [150], [75]),                 # two blocks of rows
+]
+
+
+@pytest.mark.parametrize("bounded", [False, True])
+@pytest.mark.parametrize("case", PAST, ids=lambda c: f"{c[0]}-{c[1]}-{c[3] * max(c[6])}")
+def test_causal_lengths_past_the_table(case, bounded):
+    """A sequence that has outgrown its table: its last positions do not exist, and which ones a new token sees goes by
+    the length all the same.  Bounded: the table holds them, max_len does not reach them."""
+    dim, group, heads, gh, dtype, lens, new = case
+    say(f"past {case} {bounded}")
+    rng = np.random.default_rng(sum(lens) + dim)
+    page, held = 32, 64
+    table, _ = tables(rng, len(lens), held // page + (2 if bounded else 0), 1)
+    ref = a_ref(rng, table.size + 1, heads, dim, page, group, table, [min(n, held) for n in lens])
+    cache, _ = a_cache(ref)
+    starts = np.concatenate(([0], np.cumsum(new)))
+    qt, q = typed(1.5 * rng.standard_normal((starts[-1], heads * gh, dim)), dtype)
+    out, lse, weights, mags = attend_by_token(ref, table[:, :held // page], lens, starts, q, dim ** -0.5)
+    so = torch.zeros((len(lens), heads, table.shape[1] * page), device=DEV)
+    got = T.tkv_attend(cache, qt, ints(table), ints(lens), starts=ints(starts), max_new=max(new),
+                       max_len=held if bounded else None, scores_out=so)
+    check_numbers(got, (out, lse), mags, dtype, dim)
+    have = to64(so)
+    assert (have[..., held:] == 0).all()
+    check_weights(have[..., :held], weights, mags, max(new) * gh, dim)

@@ -82,14 +82,18 @@ __device__ __forceinline__ h8 one_row(int lane) {
 struct Extent {
     int64_t start;  // first row of its tokens
     int n, len, rows;
+    int sees;  // causal: the first new token sees positions below this, by the length before it is cut to what exists
     __device__ __forceinline__ Extent(const AttendArgs &a, int seq) {
-        const int l = a.b.lens[seq];
+        const int given = a.b.lens[seq], l = given < 0 ? 0 : given;
         new_tokens(a.b, seq, start, n);
-        len = l < 0 ? 0 : l < a.max_len ? l : a.max_len;  // max_len is at most what the table holds
+        len = l < a.max_len ? l : a.max_len;  // max_len is at most what the table holds
+        sees = l - n + 1;
         rows = n * a.group_heads;
     }
     // positions below this are seen by the i-th new token
-    __device__ __forceinline__ int limit(const AttendArgs &a, int i) const { return a.causal ? len - n + 1 + i : len; }
+    __device__ __forceinline__ int limit(const AttendArgs &a, int i) const {
+        return a.causal && sees + i < len ? sees + i : len;
+    }
 };
 
 // A sequence's chunks: as few as the launch's chunk allows, of equal length up

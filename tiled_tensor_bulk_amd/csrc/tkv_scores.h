@@ -111,7 +111,7 @@ __global__ void __launch_bounds__(64 * kAttendWaves, (D > 128 ? 2 : D / GROUP > 
     keys.load(record_at(a.c, page < 0 ? 0 : page, head, p0 / kTile), lane);
     int t0 = 0;  // the first tile with a row that sees the workgroup's first position
     if (a.causal) {
-        const int i = first_pos - (e.len - e.n);
+        const int i = first_pos + 1 - e.sees;
         if (i > 0) t0 = (int)((int64_t)i * a.group_heads / 16);
     }
     // tiles whose every row sees all of the wave's positions, and, before and after, others
@@ -119,7 +119,7 @@ __global__ void __launch_bounds__(64 * kAttendWaves, (D > 128 ? 2 : D / GROUP > 
     if (!a.causal) {
         if (p0 + kTile <= e.len) full = 0;
     } else {
-        const int i = p0 + kTile - 1 - (e.len - e.n);  // the first new token that does
+        const int i = p0 + kTile - e.sees;  // the first new token that does
         const int64_t r = i > 0 ? (int64_t)i * a.group_heads : 0;
         if (p0 + kTile <= e.len && r <= e.rows) full = (int)((r + 15) / 16);
     }
