@@ -165,7 +165,8 @@ tmap_status tkv_attend_workspace(const tkv_cache *cache, const tkv_attend_args *
  *   scores      [n_seq][n_heads][score_stride]
  *   scores_out  [n_seq][n_heads][budget]: the kept positions', then 0
  *   kept        int32 [n_seq][n_heads][budget]: kept positions, then -1
- *   lens_out    int32 [n_seq]: min(lens[b], budget)
+ *   lens_out    int32 [n_seq]: min(lens[b], budget); may be lens, and else
+ *               may not overlap it
  * scores_out and scores may not overlap.  batch: table, lens and n_seq are
  * used.
  */

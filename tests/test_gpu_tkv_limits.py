@@ -92,3 +92,37 @@ def test_causal_lengths_past_the_table(case, bounded):
     have = to64(so)
     assert (have[..., held:] == 0).all()
     check_weights(have[..., :held], weights, mags, max(new) * gh, dim)
+
+
+# ------------------------------------------------------------------ eviction: lengths in place
+
+@pytest.mark.parametrize("heads,page,lens,budget,recent", [
+    (64, 32, [300, 20, 301, 0, 299, 128, 129, 300], 128, 30),  # many heads: one's workgroups long after another's
+    (3, 1024, [40000, 9000, 8999], 9000, 100),                 # scores read anew in each pass
+    (2, 64, [70, 5], 0, 3),                                    # nothing stays
+])
+def test_evict_shrinks_lens_in_place(heads, page, lens, budget, recent):
+    say(f"in place {heads} {lens} {budget}")
+    rng = np.random.default_rng(budget)
+    dim, group, n = 64, 64, len(lens)
+    width, dst_width = -(-max(lens) // page), max(1, -(-budget // page))
+    table, rest = tables(rng, n, width, n * dst_width)
+    pool = torch.from_numpy(rng.integers(0, 256, (table.size + rest.size) * T.tkv_page_bytes_of(heads, dim, page, group),
+                                         dtype=np.uint8)).to(DEV)
+    scores = torch.from_numpy(rng.random((n, heads, width * page)).astype(np.float32)).to(DEV)
+    results = []
+    for in_place in (False, True):
+        held = pool.clone()
+        cache = T.tkv_encode(held, heads, dim, page, group)
+        now = ints(lens)
+        kept, out, sc = T.tkv_evict(cache, ints(table), now, scores, budget, recent, ints(rest.reshape(n, dst_width)),
+                                    lens_out=now if in_place else None)
+        assert out.tolist() == [min(x, budget) for x in lens] and (out is now) == in_place
+        assert in_place or now.tolist() == lens
+        results.append((kept, sc, held))
+    for a, b in zip(*results):
+        assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
+    for b, length in enumerate(lens):
+        for h in range(heads):
+            want = tkv_ref.evict(length, scores[b, h].cpu().numpy(), budget, recent)
+            assert results[1][0][b, h, :len(want)].tolist() == want.tolist()

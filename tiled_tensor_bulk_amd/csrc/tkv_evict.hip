@@ -13,7 +13,9 @@
 //
 // Moving.  One wave takes one record of the destination.  K words and pairs
 // move as they are, 16 bytes a lane; a V word is put together from 8 nibbles
-// of 8 source words.
+// of 8 source words.  What stays is known from `kept`, and a sequence's new
+// length is written here, by the only wave that still reads the old one: lens
+// may be shrunk in place.
 //
 // 8 sequences of up to 32768 positions to 8192, 8 heads of 128 channels:
 // choosing 25 us, a pass over LDS for each of three digits by the one workgroup
@@ -97,8 +99,9 @@ struct Scores {
     }
 };
 
+// only: no moves follow, and then nothing that is left to do goes by the length.
 template <int HELD>
-__global__ void __launch_bounds__(kSelectThreads) select_kernel(const EvictArgs a) {
+__global__ void __launch_bounds__(kSelectThreads) select_kernel(const EvictArgs a, const bool only) {
     __shared__ uint32_t bins[kBins];
     __shared__ uint32_t found[2];  // digit, and how many are still wanted below it
     __shared__ int count_above[kSelectWaves], count_equal[kSelectWaves];
@@ -110,7 +113,7 @@ __global__ void __launch_bounds__(kSelectThreads) select_kernel(const EvictArgs 
     const float *scores = a.scores + unit * a.score_stride;
     float *scores_out = a.scores_out + unit * a.budget;
     int32_t *kept = a.kept + unit * a.budget;
-    if (head == 0 && tid == 0) a.lens_out[seq] = n;
+    if (only && head == 0 && tid == 0) a.lens_out[seq] = n;
     for (int i = n + tid; i < a.budget; i += kSelectThreads) kept[i] = -1, scores_out[i] = 0.0f;
     if (len <= a.budget) {
         for (int i = tid; i < n; i += kSelectThreads) kept[i] = i, scores_out[i] = scores[i];
@@ -232,15 +235,18 @@ __global__ void __launch_bounds__(64 * kEvictWaves) move_kernel(const EvictArgs 
     const int head = (int)(row % a.c.heads);
     if (row / a.c.heads >= a.b.n_seq) return;
     const int seq = (int)(row / a.c.heads);
-    const int len = evict_len(a, seq), n = len < a.budget ? len : a.budget;
-    if (tile * kTile >= n) return;
+    // lane i < 32: where the record of the i-th kept position is, and its place there
+    int pos = -1;
+    if (lane < kTile && tile * kTile + lane < a.budget) pos = a.kept[row * a.budget + tile * kTile + lane];
+    if (tile == 0 && head == 0 && lane == 0) {
+        const int len = evict_len(a, seq);
+        a.lens_out[seq] = len < a.budget ? len : a.budget;
+    }
+    if (!__any(pos >= 0)) return;
     const int dst_page = page_at(a.dst_table + seq * a.dst_stride, a.dst_width, a.c.n_pages, tile >> (a.c.page_shift - 5));
     if (dst_page < 0) return;
     char *dst = record_at(a.c, dst_page, head, tile);
     const int32_t *table = a.b.table + seq * a.b.table_stride;
-    // lane i < 32: where the record of the i-th kept position is, and its place there
-    int pos = -1;
-    if (lane < kTile && tile * kTile + lane < n) pos = a.kept[row * a.budget + tile * kTile + lane];
     const int page = pos < 0 ? -1 : page_at(table, a.b.table_width, a.c.n_pages, pos >> a.c.page_shift);
     if (page < 0) pos = -1;
     // what has no source reads the destination's record, and drops it
@@ -323,10 +329,7 @@ __global__ void __launch_bounds__(64 * kEvictWaves) move_kernel(const EvictArgs 
 }
 
 template <int D, int GROUP>
-static int launch_moves(const EvictArgs &a, void *stream) {
-    const int most = a.budget < a.max_len ? a.budget : a.max_len;
-    const int tiles = (most + kTile - 1) / kTile;
-    if (tiles == 0) return 0;
+static int launch_moves(const EvictArgs &a, int tiles, void *stream) {
     const int64_t units = (int64_t)a.b.n_seq * a.c.heads * tiles;
     move_kernel<D, GROUP><<<dim3((uint32_t)((units + kEvictWaves - 1) / kEvictWaves)), dim3(64 * kEvictWaves), 0,
                             (hipStream_t)stream>>>(a, tiles);
@@ -337,24 +340,26 @@ int launch_evict(const EvictArgs &a, void *stream) {
     const dim3 grid((uint32_t)(a.b.n_seq * (int64_t)a.c.heads)), block(kSelectThreads);
     hipStream_t s = (hipStream_t)stream;
     constexpr int kRow = 256 * kSelectWaves;  // positions of a row of every wave
+    const int most = a.budget < a.max_len ? a.budget : a.max_len;
+    const int tiles = (most + kTile - 1) / kTile;
     if (a.max_len <= kRow)
-        select_kernel<1><<<grid, block, 0, s>>>(a);
+        select_kernel<1><<<grid, block, 0, s>>>(a, tiles == 0);
     else if (a.max_len <= kHeld * kRow)
-        select_kernel<kHeld><<<grid, block, 0, s>>>(a);
+        select_kernel<kHeld><<<grid, block, 0, s>>>(a, tiles == 0);
     else
-        select_kernel<0><<<grid, block, 0, s>>>(a);
+        select_kernel<0><<<grid, block, 0, s>>>(a, tiles == 0);
     const int rc = (int)hipGetLastError();
-    if (rc) return rc;
+    if (rc || tiles == 0) return rc;
     switch (a.c.dim * 1000 + a.c.group) {
-        case 64032: return launch_moves<64, 32>(a, stream);
-        case 64064: return launch_moves<64, 64>(a, stream);
-        case 96032: return launch_moves<96, 32>(a, stream);
-        case 128032: return launch_moves<128, 32>(a, stream);
-        case 128064: return launch_moves<128, 64>(a, stream);
-        case 128128: return launch_moves<128, 128>(a, stream);
-        case 256032: return launch_moves<256, 32>(a, stream);
-        case 256064: return launch_moves<256, 64>(a, stream);
-        case 256128: return launch_moves<256, 128>(a, stream);
+        case 64032: return launch_moves<64, 32>(a, tiles, stream);
+        case 64064: return launch_moves<64, 64>(a, tiles, stream);
+        case 96032: return launch_moves<96, 32>(a, tiles, stream);
+        case 128032: return launch_moves<128, 32>(a, tiles, stream);
+        case 128064: return launch_moves<128, 64>(a, tiles, stream);
+        case 128128: return launch_moves<128, 128>(a, tiles, stream);
+        case 256032: return launch_moves<256, 32>(a, tiles, stream);
+        case 256064: return launch_moves<256, 64>(a, tiles, stream);
+        case 256128: return launch_moves<256, 128>(a, tiles, stream);
     }
     return (int)hipErrorInvalidValue;
 }

@@ -404,6 +404,10 @@ tmap_status tkv_evict(const tkv_cache *cache, const tkv_evict_args *args, const 
                 "dst_width must be >= 0 and at most dst_stride");
     const bool any = a.b.n_seq > 0;
     TKV_REQUIRE(!any || (args->lens_out && aligned(args->lens_out, 4)), "lens_out is NULL or not 4-byte aligned");
+    // one sequence's new length may not take another's place before that is read
+    const uintptr_t lens_in = (uintptr_t)a.b.lens, lens_out = (uintptr_t)args->lens_out, size = 4 * (uintptr_t)a.b.n_seq;
+    TKV_REQUIRE(lens_out == lens_in || lens_out >= lens_in + size || lens_in >= lens_out + size,
+                "lens_out overlaps lens and is not lens itself");
     if (any && args->budget > 0) {
         TKV_REQUIRE(args->kept && args->scores_out && aligned(args->kept, 4) && aligned(args->scores_out, 4),
                     "kept or scores_out is NULL or not 4-byte aligned");

@@ -226,8 +226,8 @@ def tkv_evict(cache: tkv_cache, table, lens, scores, budget: int, recent: int, d
               kept=None, lens_out=None, scores_out=None, stream=None):
     """Shrink each sequence to `budget` positions a head: the last `recent` and, of the others, those of the largest
     scores (fp32 [sequences, heads, positions]), in their order, moved to the pages of dst_table, which the source
-    table must not name.  Returns kept (int32 [sequences, heads, budget], -1 past the end), the new lens and the
-    kept positions' scores (0 past the end)."""
+    table must not name.  Returns kept (int32 [sequences, heads, budget], -1 past the end), the new lens (lens_out,
+    which may be lens) and the kept positions' scores (0 past the end)."""
     st, ke, le, sc = _torch.evict(cache.calls, table, lens, scores, budget, recent, dst_table, max_len, kept, lens_out,
                                   scores_out, _stream(stream))
     if stream is not None:
