@@ -1,6 +1,6 @@
-"""The operators on the 4-bit cache at the edges of their batches: lengths past what a table holds.  The plain
-implementation is tests/tkv_ref.py, asked for one new token at a time; tolerances are those of tests/test_gpu_tkv.py, and
-what is not a number fails."""
+"""The operators on the 4-bit cache at the edges of their batches: lengths past what a table holds, lengths shrunk in place,
+streams other than the current one.  The plain implementation is tests/tkv_ref.py, asked for one new token at a time;
+tolerances are those of tests/test_gpu_tkv.py, and what is not a number fails."""
 import numpy as np
 import pytest
 
@@ -126,3 +126,79 @@ def test_evict_shrinks_lens_in_place(heads, page, lens, budget, recent):
         for h in range(heads):
             want = tkv_ref.evict(length, scores[b, h].cpu().numpy(), budget, recent)
             assert results[1][0][b, h, :len(want)].tolist() == want.tolist()
+
+
+# ------------------------------------------------------------------ streams
+
+def stream_calls():
+    """A cache and calls on it that make their outputs: {name: f(stream) -> outputs}, and shapes as large as those and
+    the workspace."""
+    rng = np.random.default_rng(31)
+    heads, gh, dim, page, n = 2, 4, 64, 64, 700
+    width = -(-n // page)
+    table, rest = tables(rng, 2, width, 2 * 4)
+    ref = a_ref(rng, table.size + rest.size, heads, dim, page, 64, table, [n, n])
+    cache, pool = a_cache(ref)
+    tab, lens, dst, zero = ints(table), ints([n, n - 1]), ints(rest.reshape(2, 4)), ints([0, 0])
+    q, _ = typed(rng.standard_normal((2, heads * gh, dim)), "bf16")
+    scores = torch.from_numpy(rng.random((2, heads, width * page)).astype(np.float32)).to(DEV)
+    so = torch.zeros_like(scores)
+    calls = {
+        "attend": lambda s: T.tkv_attend(cache, q, tab, lens, max_len=n, scores=scores, scores_out=so, stream=s) + (so,),
+        "read": lambda s: T.tkv_read(cache, tab, zero, n_tokens=2 * n, stream=s),
+        "evict": lambda s: T.tkv_evict(cache, tab, lens, scores, 200, 20, dst, max_len=n, stream=s),
+    }
+    room = T.tkv_attend_workspace(cache, 2, heads * gh, 1, n, scores=True)
+    sizes = {
+        "attend": [2 * heads * gh * dim * 2, 2 * heads * gh * 4, room],
+        "read": [2 * n * heads * dim * 2] * 2,
+        "evict": [2 * heads * 200 * 4, 8, 2 * heads * 200 * 4],
+    }
+    return calls, sizes, pool
+
+
+@pytest.mark.parametrize("name", ["attend", "read", "evict"])
+@pytest.mark.parametrize("how", ["stream", "handle"])
+def test_outputs_made_on_another_stream(name, how):
+    """Memory that was given back on the current stream, with work on it still queued there, is not what a call on
+    another stream writes to: neither disturbs the other."""
+    say(f"stream {name} {how}")
+    calls, sizes, pool = stream_calls()
+    f = calls[name]
+    want = [x.clone() for x in f(None)]
+    side = torch.cuda.Stream()
+    big = torch.randn((8192, 8192), device=DEV).bfloat16()
+    other = torch.empty_like(big)
+    f(side)  # whatever a first call sets up
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    blocks = [torch.zeros(n, dtype=torch.uint8, device=DEV) for n in sizes[name] for _ in range(3)]
+    at = {b.data_ptr() for b in blocks}
+    torch.cuda.synchronize()
+    for _ in range(30):  # some 25 ms
+        torch.mm(big, big, out=other)
+    for b in blocks:
+        b.fill_(0x55)
+    del blocks, b
+    got = f(side.cuda_stream if how == "handle" else side)
+    side.synchronize()
+    made = got[:2] if name == "attend" else got
+    assert not at & {x.data_ptr() for x in made}
+    with torch.cuda.stream(side):
+        early = [x.cpu() for x in got]
+    torch.cuda.synchronize()
+    for w, e, g in zip(want, early, got):
+        assert torch.equal(w.cpu(), e) and torch.equal(w, g)
+
+
+def test_the_default_stream_by_its_handle():
+    calls, _, _ = stream_calls()
+    want = [x.clone() for x in calls["attend"](None)]
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        got = calls["attend"](0)
+    torch.cuda.synchronize()
+    for w, g in zip(want, got):
+        assert torch.equal(w, g)
+    assert torch.cuda.current_stream() == torch.cuda.default_stream()

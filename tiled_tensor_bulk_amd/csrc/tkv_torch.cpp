@@ -8,6 +8,7 @@
 #include <torch/csrc/utils/pybind.h>
 
 #include <ATen/ops/empty.h>
+#include <c10/hip/HIPGuard.h>
 #include <c10/hip/HIPStream.h>
 
 #include <cmath>
@@ -87,6 +88,12 @@ Table table_of(const Tensor &t, const char *what, int64_t n_seq, const Cache &c)
     return {t.data_ptr<int32_t>(), n_seq < 2 ? t.size(1) : t.stride(0), (int32_t)t.size(1)};
 }
 
+void on_current_device(const Cache &c) {
+    const auto current = c10::hip::current_device();
+    TKV_CHECK(current == c.pool.get_device(), "the cache is on ", c.pool.device(), ", the current device is ",
+              (int)current);
+}
+
 struct Batch {
     tkv_batch b;
     int64_t held;  // positions that a row of the table holds
@@ -94,9 +101,7 @@ struct Batch {
 
 Batch batch(const Cache &c, const Tensor &table, const Tensor &lens, const Maybe &starts, int64_t n_tokens,
             std::optional<int64_t> max_new) {
-    const auto current = c10::hip::current_device();
-    TKV_CHECK(current == c.pool.get_device(), "the cache is on ", c.pool.device(), ", the current device is ",
-              (int)current);
+    on_current_device(c);
     typed(lens, "lens", at::kInt, c);
     TKV_CHECK(lens.dim() == 1 && (lens.size(0) < 2 || lens.stride(0) == 1), "lens must be a contiguous vector");
     const int64_t n_seq = lens.size(0);
@@ -119,10 +124,21 @@ Batch batch(const Cache &c, const Tensor &table, const Tensor &lens, const Maybe
             t.width * c.page_tokens};
 }
 
-// The stream's handle: the given one, or torch's current.
-void *stream_of(std::optional<int64_t> stream) {
-    return stream ? reinterpret_cast<void *>(*stream) : (void *)c10::hip::getCurrentHIPStream().stream();
-}
+// The stream of a call's work: the given one, or torch's current.  A given one is
+// torch's current one for as long as this lives, so that what the call makes is
+// memory of that stream: another stream's may still be in use there by work
+// that was queued before the memory was given back.
+struct Stream {
+    std::optional<c10::hip::HIPStreamGuard> guard;
+    void *handle;
+    Stream(const Cache &c, std::optional<int64_t> given) {
+        if (given) {
+            on_current_device(c);
+            guard.emplace(c10::hip::getStreamFromExternal((hipStream_t)*given, c.pool.device().index()));
+        }
+        handle = (void *)c10::hip::getCurrentHIPStream().stream();
+    }
+};
 
 Tensor made(at::IntArrayRef size, at::ScalarType type, const Cache &c) {
     return at::empty(size, at::TensorOptions().dtype(type).device(c.pool.device()));
@@ -134,13 +150,15 @@ int do_append(const Cache &c, const Tensor &k, const Tensor &v, const Tensor &ta
     const int64_t n = k.size(0);
     const tkv_tokens vt = tokens(v, "v", c.heads, n, false, c);
     const Batch b = batch(c, table, lens, starts, n, max_new);
-    return tkv_append(&c.described, &kt, &vt, &b.b, stream_of(stream));
+    const Stream on(c, stream);
+    return tkv_append(&c.described, &kt, &vt, &b.b, on.handle);
 }
 
 py::tuple do_read(const Cache &c, const Tensor &table, const Tensor &lens, const Maybe &starts,
                std::optional<int64_t> max_new, std::optional<int64_t> n_tokens, at::ScalarType dtype, const Maybe &k_,
                const Maybe &v_, std::optional<int64_t> stream) {
     TKV_CHECK(k_.has_value() == v_.has_value(), "give both k and v, or neither");
+    const Stream on(c, stream);
     Tensor k, v;
     if (k_) {
         k = *k_, v = *v_;
@@ -153,7 +171,7 @@ py::tuple do_read(const Cache &c, const Tensor &table, const Tensor &lens, const
     const tkv_tokens kt = tokens(k, "k", c.heads, n_tokens.value_or(-1), true, c);
     const tkv_tokens vt = tokens(v, "v", c.heads, k.size(0), true, c);
     const Batch b = batch(c, table, lens, starts, k.size(0), max_new);
-    const int st = tkv_read(&c.described, &kt, &vt, &b.b, stream_of(stream));
+    const int st = tkv_read(&c.described, &kt, &vt, &b.b, on.handle);
     return py::make_tuple(st, k, v);
 }
 
@@ -174,6 +192,7 @@ py::tuple do_attend(const Cache &c, const Tensor &q, const Tensor &table, const 
                  std::optional<int64_t> max_new, std::optional<int64_t> max_len, std::optional<double> scale, bool causal,
                  const Maybe &scores, const Maybe &scores_out, const Maybe &out_, const Maybe &lse_,
                  const Maybe &workspace, std::optional<int64_t> stream) {
+    const Stream on(c, stream);
     tkv_attend_args a{};
     a.q = tokens(q, "q", -1, -1, false, c);
     const int64_t n = q.size(0), heads = q.size(1);
@@ -215,14 +234,15 @@ py::tuple do_attend(const Cache &c, const Tensor &q, const Tensor &table, const 
         a.workspace = room.data_ptr();
         a.workspace_bytes = (uint64_t)room.numel();
     }
-    if (st == TMAP_SUCCESS) st = tkv_attend(&c.described, &a, &b.b, stream_of(stream));
-    return py::make_tuple(st, out, lse, room.defined() ? py::cast(room) : py::none());
+    if (st == TMAP_SUCCESS) st = tkv_attend(&c.described, &a, &b.b, on.handle);
+    return py::make_tuple(st, out, lse);
 }
 
 py::tuple do_evict(const Cache &c, const Tensor &table, const Tensor &lens, const Tensor &scores, int64_t budget,
                 int64_t recent, const Tensor &dst_table, std::optional<int64_t> max_len, const Maybe &kept_,
                 const Maybe &lens_out_, const Maybe &scores_out_, std::optional<int64_t> stream) {
     const Batch b = batch(c, table, lens, std::nullopt, 0, 0);
+    const Stream on(c, stream);
     tkv_evict_args a{};
     a.max_len = (int32_t)bound(max_len, b.held);
     a.scores = scores_of(scores, "scores", c, b.b.n_seq, a.max_len);
@@ -248,7 +268,7 @@ py::tuple do_evict(const Cache &c, const Tensor &table, const Tensor &lens, cons
     a.dst_width = t.width;
     a.budget = (int32_t)budget;
     a.recent = (int32_t)recent;
-    const int st = tkv_evict(&c.described, &a, &b.b, stream_of(stream));
+    const int st = tkv_evict(&c.described, &a, &b.b, on.handle);
     return py::make_tuple(st, kept, lens_out, scores_out);
 }
 

@@ -6,7 +6,10 @@ others through ctypes, whose structures are those of the header.
 
 Names match the C ABI.  Tensors lie on the current GPU; work goes to `stream`
 (an int, a torch stream, or None: torch's current one).  Outputs and the
-workspace are allocated with torch where they are not given.
+workspace are allocated with torch where they are not given, from the memory
+of that stream; outputs are kept for torch's current stream too.  A caller who
+names a stream orders it after the work that makes the inputs, and keeps these
+until it is done with them, as everywhere in torch.
 
     pool  = torch.empty(n_pages * tkv_page_bytes_of(heads, dim, page, group), dtype=torch.uint8, device="cuda")
     cache = tkv_encode(pool, heads, dim, page, group)
@@ -127,14 +130,12 @@ def _stream(s):
 
 
 def _keep(s, device, *made):
-    """Tensors made here are kept for the stream that they are used on."""
-    on = s
-    if isinstance(s, int):
-        on = torch.cuda.ExternalStream(s, device=device) if s else torch.cuda.default_stream(device)
-    if on != torch.cuda.current_stream(device):
+    """Tensors made from the memory of stream s are kept for torch's current one, where the caller goes on with them."""
+    here = torch.cuda.current_stream(device)
+    if here.cuda_stream != _stream(s):
         for t in made:
             if t is not None:
-                t.record_stream(on)
+                t.record_stream(here)
 
 
 def tkv_page_bytes_of(n_heads: int, head_dim: int, page_tokens: int, group: int) -> int:
@@ -199,11 +200,10 @@ def tkv_attend(cache: tkv_cache, q, table, lens, starts=None, max_new: Optional[
     it are not seen.  scale: default 1 / sqrt(head_dim).  scores_out (fp32 [sequences, heads, positions]): written
     with scores (None: 0) plus each position's attention weight summed over the new tokens and the head's query
     heads; may be scores itself.  workspace: a uint8 tensor of at least tkv_attend_workspace bytes."""
-    st, o, ls, room = _torch.attend(cache.calls, q, table, lens, starts, max_new, max_len, scale, causal, scores,
-                                    scores_out, out, lse, workspace, _stream(stream))
+    st, o, ls = _torch.attend(cache.calls, q, table, lens, starts, max_new, max_len, scale, causal, scores, scores_out,
+                              out, lse, workspace, _stream(stream))
     if stream is not None:
-        _keep(stream, cache.pool.device, o if out is None else None, ls if lse is None else None,
-              room if workspace is None else None)
+        _keep(stream, cache.pool.device, o if out is None else None, ls if lse is None else None)
     _check(st, "tkv_attend")
     return o, ls
 
