@@ -202,3 +202,36 @@ def test_the_default_stream_by_its_handle():
     for w, g in zip(want, got):
         assert torch.equal(w, g)
     assert torch.cuda.current_stream() == torch.cuda.default_stream()
+
+
+# ------------------------------------------------------------------ scores of sequences without new tokens
+
+@pytest.mark.parametrize("from_scores", [False, True])
+@pytest.mark.parametrize("gh,new", [(1, [0, 0, 0]), (2, [0, 3, 0]), (5, [0, 3, 0]), (9, [0, 9, 0])])
+def test_scores_where_nothing_is_new(gh, new, from_scores):
+    """scores_out is scores, or 0, for a sequence with no new token: in a batch that has none at all, and beside one
+    that has some, of few rows and of many."""
+    say(f"scores {gh} {new} {from_scores}")
+    rng = np.random.default_rng(gh)
+    heads, dim, page, lens = 2, 64, 32, [60, 1030, 0]
+    table, _ = tables(rng, 3, 33)
+    ref = a_ref(rng, table.size, heads, dim, page, 32, table, lens)
+    cache, _ = a_cache(ref)
+    starts = np.concatenate(([0], np.cumsum(new)))
+    qt, q = typed(rng.standard_normal((starts[-1], heads * gh, dim)), "f16")
+    base = torch.from_numpy(rng.random((3, heads, 33 * page)).astype(np.float32)).to(DEV)
+    so = torch.full_like(base, 5.0)
+    T.tkv_attend(cache, qt, ints(table), ints(lens), starts=ints(starts), max_new=max(new),
+                 scores=base if from_scores else None, scores_out=so)
+    for b, n in enumerate(lens):
+        if new[b] == 0:
+            assert torch.equal(so[b, :, :n], base[b, :, :n] if from_scores else torch.zeros_like(so[b, :, :n]))
+        assert (so[b, :, n:] == 5.0).all()
+    if starts[-1]:
+        _, _, weights, mags = attend_by_token(ref, table, lens, starts, q, dim ** -0.5)
+        have = to64(so[1, :, :lens[1]]) - (to64(base[1, :, :lens[1]]) if from_scores else 0.0)
+        assert np.abs(have - weights[1, :, :lens[1]]).max() < 1e-5  # the sum's rounding is 2^-24 of at most 1 + 9 * 9
+    else:
+        st = base.clone()
+        T.tkv_attend(cache, qt, ints(table), ints(lens), starts=ints(starts), max_new=0, scores=st, scores_out=st)
+        assert torch.equal(st, base)

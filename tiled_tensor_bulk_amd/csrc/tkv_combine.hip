@@ -205,12 +205,21 @@ __global__ void __launch_bounds__(kCombineThreads) combine_weigh_kernel(const At
         weigh<true>(a, blockIdx.x - combining, blocks);
 }
 
+static int weighing_blocks(const AttendArgs &a) { return (a.max_len + kWeighPositions - 1) / kWeighPositions; }
+
+int launch_weigh(const AttendArgs &a, void *stream) {
+    const int blocks = weighing_blocks(a);
+    weigh_kernel<<<dim3((uint32_t)((int64_t)a.b.n_seq * a.c.heads * blocks)), dim3(kCombineThreads), 0,
+                   (hipStream_t)stream>>>(a, blocks);
+    return (int)hipGetLastError();
+}
+
 template <int D>
 static int launch(const AttendArgs &a, hipStream_t s) {
     const int64_t rows = (int64_t)a.b.n_seq * a.c.heads * a.rows;
     constexpr int AT_ONCE = kCombineThreads / (D / 4);
     const int combining = (int)((rows + AT_ONCE - 1) / AT_ONCE);
-    const int blocks = (a.max_len + kWeighPositions - 1) / kWeighPositions;
+    const int blocks = weighing_blocks(a);
     const int64_t weighing = a.logits ? (int64_t)a.b.n_seq * a.c.heads * blocks : 0;
     const dim3 block(kCombineThreads);
     const bool few = a.even || a.n_split <= kFewParts;

@@ -349,7 +349,13 @@ tmap_status tkv_attend(const tkv_cache *cache, const tkv_attend_args *args, cons
     TKV_TRY(attend_args(cache, args, batch, true, a));
     int cus = 0;
     TKV_TRY(device(cus));
-    if (a.b.n_seq == 0 || a.rows == 0) return ok();
+    if (a.b.n_seq == 0) return ok();
+    if (a.rows == 0) {  // no row to answer; scores_out is still to be scores_in, or 0
+        if (!a.scores_out || a.scores_out == a.scores_in || a.max_len == 0) return ok();
+        TKV_REQUIRE((int64_t)a.b.n_seq * a.c.heads * (a.max_len / 128 + 1) < kMostBlocks, "too many sequences and heads");
+        a.by_heads = divisor(a.c.heads);
+        return launched(tkv::launch_weigh(a, hip_stream));
+    }
     const Split s = plan(a.c, a.b.n_seq, a.rows, a.max_len, a.scores_out, cus);
     TKV_REQUIRE((int64_t)a.b.n_seq * a.c.heads * s.n_split * s.row_blocks < kMostBlocks &&
                     (int64_t)a.b.n_seq * a.c.heads * (a.max_len / 128 + 1) < kMostBlocks &&

@@ -123,6 +123,7 @@ int launch_attend_d96(const AttendArgs &a, int row_tile, void *stream);
 int launch_attend_d128(const AttendArgs &a, int row_tile, void *stream);
 int launch_attend_d256(const AttendArgs &a, int row_tile, void *stream);
 int launch_combine(const AttendArgs &a, void *stream);
+int launch_weigh(const AttendArgs &a, void *stream);  // of sequences without rows: the scores as they are
 int launch_evict(const EvictArgs &a, void *stream);
 
 }  // namespace tkv
