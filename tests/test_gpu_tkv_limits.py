@@ -235,3 +235,31 @@ def test_scores_where_nothing_is_new(gh, new, from_scores):
         st = base.clone()
         T.tkv_attend(cache, qt, ints(table), ints(lens), starts=ints(starts), max_new=0, scores=st, scores_out=st)
         assert torch.equal(st, base)
+
+
+# ------------------------------------------------------------------ errors of others
+
+def test_an_earlier_error_of_the_runtime_is_not_the_calls():
+    """A HIP call of somebody else that was refused on this thread, here one that names no device, is not reported as a
+    launch that failed, and stops none of a call's launches."""
+    import ctypes
+
+    hip = ctypes.CDLL("libamdhip64.so")
+    calls, _, _ = stream_calls()
+    want = {name: [x.clone() for x in f(None)] for name, f in calls.items()}
+    torch.cuda.synchronize()
+    for name, f in calls.items():
+        got = None
+        assert hip.hipSetDevice(4711) != 0  # stays this thread's last error
+        got = f(None)
+        torch.cuda.synchronize()
+        for w, g in zip(want[name], got):
+            assert torch.equal(w, g), name
+    q = torch.ones((2, 2, 64), dtype=torch.float16, device=DEV)
+    pool = torch.zeros(2 * T.tkv_page_bytes_of(2, 64, 32, 32), dtype=torch.uint8, device=DEV)
+    cache, table, lens = T.tkv_encode(pool, 2, 64, 32, 32), ints([[0], [1]]), ints([0, 0])
+    torch.cuda.synchronize()
+    assert hip.hipSetDevice(4711) != 0
+    T.tkv_append(cache, q, q, table, lens)
+    torch.cuda.synchronize()
+    assert pool.any()

@@ -69,6 +69,7 @@ tmap_status device(int &cus) {
         seen[dev].store(v, std::memory_order_relaxed);
     }
     if (v < 0) return fail(TMAP_ERROR_UNSUPPORTED_DEVICE, "device %d is not gfx950", dev);
+    (void)hipGetLastError();  // one that an earlier call on this thread left is not this call's
     cus = v;
     return TMAP_SUCCESS;
 }
