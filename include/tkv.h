@@ -41,6 +41,9 @@
  *     of the token tensors (`starts` int32 [n_seq + 1], 0 first and n_tokens
  *     last), at most max_new of them; with starts == NULL every sequence has
  *     n_tokens / n_seq.  Rows past max_new are left alone.
+ *   - A row of the table holds fewer than 2^31 - 2^17 positions, and a call
+ *     has fewer than 2^31 records, and rows times head_dim / 32, of all
+ *     sequences and heads.
  *   - Positions whose page is outside the pool (< 0 or >= n_pages), or past
  *     the table's width, do not exist: they are never read or written.
  *   - No two sequences may name the same page where a call writes to it.
@@ -62,7 +65,7 @@ typedef struct __attribute__((aligned(64))) tkv_cache {
 /*
  * tkv_encode -- describe a pool.  Host-only: needs no GPU.
  *   pool         device, n_pages * tkv_page_bytes bytes, 16-byte aligned
- *   n_pages      1 .. 2^31 - 1
+ *   n_pages      1 .. 2^31 - 2
  *   n_heads      key/value heads, 1 .. 65535
  *   head_dim     64, 96, 128 or 256
  *   page_tokens  a power of two, 32 .. 1024

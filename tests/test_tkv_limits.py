@@ -1,4 +1,4 @@
-"""What libtkv refuses beyond tests/test_tkv_boundary.py: overlaps.  Without a GPU, with pointers that nothing reads;
+"""What libtkv refuses beyond tests/test_tkv_boundary.py: overlaps, and sizes that no launch has.  Without a GPU, with pointers that nothing reads;
 what is not refused stops at the device."""
 import ctypes
 
@@ -6,9 +6,9 @@ import pytest
 
 torch = pytest.importorskip("torch")
 
-from tests.test_tkv_boundary import AT, batch, encode, evict_args, refused  # noqa: E402
+from tests.test_tkv_boundary import AT, attend_args, batch, encode, evict_args, refused, tokens  # noqa: E402
 from tiled_tensor_bulk_amd import tkv as T  # noqa: E402
-from tiled_tensor_bulk_amd.tmap import UNSUPPORTED_DEVICE  # noqa: E402
+from tiled_tensor_bulk_amd.tmap import INVALID_VALUE, UNSUPPORTED_DEVICE  # noqa: E402
 
 no_gpu = pytest.mark.skipif(torch.cuda.is_available(), reason="with a GPU what is accepted would run")
 
@@ -28,3 +28,53 @@ def test_evict_refuses_lengths_that_overlap(off):
 @pytest.mark.parametrize("off", [-12, 0, 12])
 def test_evict_takes_lengths_in_place_and_apart(off):
     assert evict(lens_out=AT + off, n_seq=3) == UNSUPPORTED_DEVICE
+
+
+# ------------------------------------------------------------------ sizes
+
+def moves(**kw):
+    _, c = encode(heads=kw.pop("heads", 4), page=kw.pop("page", 64))
+    k, b = tokens(), batch(**kw)
+    return [f(ctypes.byref(c), ctypes.byref(k), ctypes.byref(k), ctypes.byref(b), None)
+            for f in (T.lib().tkv_append, T.lib().tkv_read)]
+
+
+def attend(heads=4, page=64, scored=False, **kw):
+    _, c = encode(heads=heads, page=page)
+    b = {k: kw.pop(k) for k in list(kw) if k in dict(T.tkv_batch._fields_)}
+    if scored:
+        kw.update(scores_out=AT, score_stride=kw["max_len"])
+    return T.lib().tkv_attend(ctypes.byref(c), ctypes.byref(attend_args(**kw)), ctypes.byref(batch(**b)), None)
+
+
+MANY = (1 << 31) - 1
+
+
+@pytest.mark.parametrize("kw", [
+    dict(n_tokens=MANY, max_new=MANY, n_seq=1, starts=AT, heads=32),            # the number of records passes 31 bits
+    dict(n_tokens=MANY, max_new=MANY, n_seq=MANY, starts=AT, heads=65535),      # and their product 64
+    dict(n_tokens=1 << 30, max_new=1 << 30, n_seq=1 << 25, starts=AT, heads=1 << 13),  # which comes out as 0 there
+])
+def test_moves_refuse_sizes_past_what_integers_hold(kw):
+    for st in moves(**kw):
+        refused(st, "too many")
+
+
+def test_attend_and_evict_refuse_sizes_past_what_integers_hold():
+    wide = dict(table_width=1 << 20, table_stride=1 << 20, page=1024)
+    refused(attend(n_seq=1 << 26, n_tokens=0, heads=1 << 15, q_heads=1 << 15,
+                   max_len=1 << 30, **wide), "too many")  # 2^64 steps
+    refused(attend(n_seq=1 << 24, n_tokens=MANY, starts=AT, max_new=1 << 16, heads=1 << 13, q_heads=1 << 24, max_len=5),
+            "too many")
+    refused(evict(n_seq=1 << 27, budget=(1 << 31) - 32, score_stride=512), "too many")  # 2^55 records
+    _, c = encode(heads=1 << 14)
+    assert T.lib().tkv_evict(ctypes.byref(c), ctypes.byref(evict_args(budget=(1 << 31) - 32)),
+                             ctypes.byref(batch(n_seq=1 << 30)), None) == INVALID_VALUE  # 2^70
+
+
+def test_tables_that_hold_2_to_the_31_positions_are_refused():
+    wide = dict(table_width=1 << 21, table_stride=1 << 21)
+    for st in moves(page=1024, **wide) + [attend(page=1024, **wide)]:
+        refused(st, "2^31")
+    _, c = encode(page=1024)
+    refused(T.lib().tkv_evict(ctypes.byref(c), ctypes.byref(evict_args()), ctypes.byref(batch(**wide)), None), "2^31")

@@ -81,11 +81,23 @@ tmap_status launched(int rc) {
 
 constexpr int64_t kMostBlocks = 0x7FFFFFFF;
 
-tmap_status check_batch(const tkv_batch *in, tkv::Batch &b, bool tokens) {
+// Whether a product of sizes is less than kMostBlocks; of numbers that the
+// arguments' types allow it may take more than 64 bits.
+template <class... Sizes>
+bool launchable(Sizes... sizes) {
+    return ((__int128)1 * ... * (int64_t)sizes) < kMostBlocks;
+}
+
+// Positions of a sequence: what kernels add to one before they compare it, a
+// chunk at most, stays within 31 bits.
+constexpr int64_t kMostPositions = 0x7FFFFFFF - 2 * (1 << 16);
+
+tmap_status check_batch(const Cache &c, const tkv_batch *in, tkv::Batch &b, bool tokens) {
     TKV_REQUIRE(in, "batch is NULL");
     TKV_REQUIRE(in->n_seq >= 0, "n_seq is negative");
     TKV_REQUIRE(in->table_width >= 0 && in->table_stride >= in->table_width,
                 "table_width must be >= 0 and at most table_stride");
+    TKV_REQUIRE(((int64_t)in->table_width << c.page_shift) <= kMostPositions, "a row of the table holds 2^31 positions");
     TKV_REQUIRE(in->n_seq == 0 || (in->lens && aligned(in->lens, 4)), "lens is NULL or not 4-byte aligned");
     TKV_REQUIRE(in->n_seq == 0 || in->table_width == 0 || (in->table && aligned(in->table, 4)),
                 "table is NULL or not 4-byte aligned");
@@ -139,13 +151,13 @@ tmap_status move_args(const tkv_cache *cache, const tkv_tokens *k, const tkv_tok
                       bool fp32_too, tkv::MoveArgs &a) {
     TKV_REQUIRE(decode(cache, a.c), "cache was never encoded");
     TKV_REQUIRE(k && v, "k or v is NULL");
-    TKV_TRY(check_batch(batch, a.b, true));
+    TKV_TRY(check_batch(a.c, batch, a.b, true));
     TKV_TRY(check_tokens(*k, "k", fp32_too, a.b.n_tokens == 0, a.k));
     TKV_TRY(check_tokens(*v, "v", fp32_too, a.b.n_tokens == 0, a.v));
     TKV_REQUIRE(k->dtype == v->dtype, "k and v must have one type");
     // a run of n positions that starts anywhere touches at most this many records
-    a.tiles = a.b.max_new == 0 ? 0 : (a.b.max_new + 2 * (tkv::kTile - 1)) / tkv::kTile;
-    TKV_REQUIRE((int64_t)a.tiles * a.b.n_seq * a.c.heads < kMostBlocks, "too many sequences, heads and new tokens");
+    a.tiles = a.b.max_new == 0 ? 0 : (int32_t)(((int64_t)a.b.max_new + 2 * (tkv::kTile - 1)) / tkv::kTile);
+    TKV_REQUIRE(launchable(a.tiles, a.b.n_seq, a.c.heads), "too many sequences, heads and new tokens");
     return TMAP_SUCCESS;
 }
 
@@ -193,7 +205,7 @@ uint64_t up(uint64_t v, uint64_t to) { return (v + to - 1) / to * to; }
 // 1000 62 and 54, unless one may be so long that the others wait for it: one of
 // 131072 and 199 of 1000 102 and 453.
 constexpr int kLeastChunk = 512;
-constexpr int kMostChunk = 1 << 16;
+constexpr int kMostChunk = 1 << 16;  // kMostPositions leaves room for two
 constexpr int kLongForOne = 1 << 14;
 constexpr int kBlocksPerCu = 8;
 constexpr int kRowBlocksPerCu = 2;
@@ -245,7 +257,7 @@ tmap_status attend_args(const tkv_cache *cache, const tkv_attend_args *in, const
                         tkv::AttendArgs &a) {
     TKV_REQUIRE(decode(cache, a.c), "cache was never encoded");
     TKV_REQUIRE(in, "args is NULL");
-    TKV_TRY(check_batch(batch, a.b, true));
+    TKV_TRY(check_batch(a.c, batch, a.b, true));
     const bool empty = !pointers || a.b.n_tokens == 0;
     TKV_TRY(check_tokens(in->q, "q", false, empty, a.q));
     TKV_TRY(check_tokens(in->out, "out", false, empty, a.out));
@@ -272,6 +284,8 @@ tmap_status attend_args(const tkv_cache *cache, const tkv_attend_args *in, const
     // no position lies past the table
     const int64_t width = (int64_t)a.b.table_width << a.c.page_shift;
     if (a.max_len > width) a.max_len = (int32_t)width;
+    TKV_REQUIRE(launchable(a.b.n_seq, a.c.heads, a.max_len / 128 + 1) &&
+                    launchable(a.b.n_seq, a.c.heads, a.rows, a.c.dim / 32), "too many sequences, heads and rows");
     a.scores_in = in->scores_in;
     a.scores_out = in->scores_out;
     a.score_stride = in->score_stride;
@@ -353,15 +367,11 @@ tmap_status tkv_attend(const tkv_cache *cache, const tkv_attend_args *args, cons
     if (a.b.n_seq == 0) return ok();
     if (a.rows == 0) {  // no row to answer; scores_out is still to be scores_in, or 0
         if (!a.scores_out || a.scores_out == a.scores_in || a.max_len == 0) return ok();
-        TKV_REQUIRE((int64_t)a.b.n_seq * a.c.heads * (a.max_len / 128 + 1) < kMostBlocks, "too many sequences and heads");
         a.by_heads = divisor(a.c.heads);
         return launched(tkv::launch_weigh(a, hip_stream));
     }
     const Split s = plan(a.c, a.b.n_seq, a.rows, a.max_len, a.scores_out, cus);
-    TKV_REQUIRE((int64_t)a.b.n_seq * a.c.heads * s.n_split * s.row_blocks < kMostBlocks &&
-                    (int64_t)a.b.n_seq * a.c.heads * (a.max_len / 128 + 1) < kMostBlocks &&
-                    (int64_t)a.b.n_seq * a.c.heads * a.rows * (a.c.dim / 32) < kMostBlocks,
-                "too many sequences, heads and rows");
+    TKV_REQUIRE(launchable(a.b.n_seq, a.c.heads, s.n_split, s.row_blocks), "too many sequences, heads and rows");
     if (s.total) {
         TKV_REQUIRE(args->workspace && aligned(args->workspace, 16), "workspace is NULL or not 16-byte aligned");
         TKV_REQUIRE(args->workspace_bytes >= s.total, "workspace holds %llu bytes, %llu are needed",
@@ -404,7 +414,7 @@ tmap_status tkv_evict(const tkv_cache *cache, const tkv_evict_args *args, const 
     tkv::EvictArgs a{};
     TKV_REQUIRE(decode(cache, a.c), "cache was never encoded");
     TKV_REQUIRE(args, "args is NULL");
-    TKV_TRY(check_batch(batch, a.b, false));
+    TKV_TRY(check_batch(a.c, batch, a.b, false));
     TKV_REQUIRE(args->budget >= 0 && args->recent >= 0, "budget or recent is negative");
     TKV_REQUIRE(args->max_len >= 0 && args->score_stride >= args->max_len, "score_stride is less than max_len");
     TKV_REQUIRE(args->dst_width >= 0 && args->dst_stride >= args->dst_width,
@@ -423,7 +433,7 @@ tmap_status tkv_evict(const tkv_cache *cache, const tkv_evict_args *args, const 
         TKV_REQUIRE(args->dst_width == 0 || (args->dst_table && aligned(args->dst_table, 4)),
                     "dst_table is NULL or not 4-byte aligned");
     }
-    TKV_REQUIRE((int64_t)a.b.n_seq * a.c.heads * ((int64_t)args->budget / tkv::kTile + 1) < kMostBlocks,
+    TKV_REQUIRE(launchable(a.b.n_seq, a.c.heads, args->budget / tkv::kTile + 1),
                 "too many sequences, heads and positions");
     a.scores = args->scores;
     a.scores_out = args->scores_out;
