@@ -41,9 +41,10 @@
  *     of the token tensors (`starts` int32 [n_seq + 1], 0 first and n_tokens
  *     last), at most max_new of them; with starts == NULL every sequence has
  *     n_tokens / n_seq.  Rows past max_new are left alone.
- *   - A row of the table holds fewer than 2^31 - 2^17 positions, and a call
- *     has fewer than 2^31 records, and rows times head_dim / 32, of all
- *     sequences and heads.
+ *   - A row of the table holds fewer than 2^31 - 2^17 positions.  A call is
+ *     refused whose sequences and heads have together more records, rows or
+ *     positions than launches of 2^32 threads hold (2^25 records of a read or
+ *     2^24 heads of up to 128 positions, for example).
  *   - Positions whose page is outside the pool (< 0 or >= n_pages), or past
  *     the table's width, do not exist: they are never read or written.
  *   - No two sequences may name the same page where a call writes to it.

@@ -34,26 +34,45 @@ static void expect(bool ok, const char *what) {
     if (!ok && bad++ < 20) std::fprintf(stderr, "unexpected: %s (%s)\n", what, tkv_last_error_detail());
 }
 
-namespace tkv {
-static int moved(const MoveArgs &a) {
+// A kernel of so many threads for each of so many units of work, some of which a workgroup takes.
+static void launch(const char *what, double units, int of_a_workgroup, int threads = 256) {
     ++launches;
-    expect(a.tiles > 0 && a.tiles >= a.b.max_new / kTile, "records of a move");
+    const double blocks = std::ceil(units / of_a_workgroup);
+    expect(blocks >= 1 && blocks * threads < 4294967296.0, what);
+}
+
+namespace tkv {
+static int moved(const MoveArgs &a, bool append) {
+    launch("records of a move", (double)a.tiles * a.b.n_seq * a.c.heads, append && a.b.max_new <= 4 ? 4 : 2);
+    expect(a.tiles > 0 && a.tiles >= a.b.max_new / kTile, "positions of a move");
     return 0;
 }
-int launch_append(const MoveArgs &a, void *) { return moved(a); }
-int launch_read(const MoveArgs &a, void *) { return moved(a); }
+int launch_append(const MoveArgs &a, void *) { return moved(a, true); }
+int launch_read(const MoveArgs &a, void *) { return moved(a, false); }
 static int attended(const AttendArgs &a, int row_tile) {
-    ++launches;
+    const double heads = (double)a.b.n_seq * a.c.heads;
     expect((int64_t)a.row_blocks * row_tile >= a.rows && (1 << a.row_shift) == row_tile, "rows of attention");
     expect(a.even || ((int64_t)a.n_split << a.chunk_shift) >= a.max_len, "positions of attention");
+    if (!a.even) launch("attention", heads * a.n_split * a.row_blocks, 1);
+    if (a.n_split > 1 && (a.even || a.n_split <= 16)) launch("joining few parts", heads * a.rows, 1024 / a.c.dim);
+    if (a.n_split > 16 && !a.even) launch("joining", heads * a.rows * (a.c.dim / 32), 1);
+    if (a.scores_out && a.max_len) launch("scores", heads * std::ceil(a.max_len / (a.rows <= 8 ? 1024.0 : 128.0)), 1);
     return 0;
 }
 int launch_attend_d64(const AttendArgs &a, int row_tile, void *) { return attended(a, row_tile); }
 int launch_attend_d96(const AttendArgs &a, int row_tile, void *) { return attended(a, row_tile); }
 int launch_attend_d128(const AttendArgs &a, int row_tile, void *) { return attended(a, row_tile); }
 int launch_attend_d256(const AttendArgs &a, int row_tile, void *) { return attended(a, row_tile); }
-int launch_weigh(const AttendArgs &, void *) { return ++launches, 0; }
-int launch_evict(const EvictArgs &, void *) { return ++launches, 0; }
+int launch_weigh(const AttendArgs &a, void *) {
+    launch("scores alone", (double)a.b.n_seq * a.c.heads * std::ceil(a.max_len / 1024.0), 1);
+    return 0;
+}
+int launch_evict(const EvictArgs &a, void *) {
+    const double heads = (double)a.b.n_seq * a.c.heads, most = a.budget < a.max_len ? a.budget : a.max_len;
+    launch("choosing", heads, 1, 1024);
+    if (most) launch("moving", heads * std::ceil(most / 32), 4);
+    return 0;
+}
 }  // namespace tkv
 
 static uint64_t g_state = 0x9E3779B97F4A7C15ull;

@@ -78,3 +78,26 @@ def test_tables_that_hold_2_to_the_31_positions_are_refused():
         refused(st, "2^31")
     _, c = encode(page=1024)
     refused(T.lib().tkv_evict(ctypes.byref(c), ctypes.byref(evict_args()), ctypes.byref(batch(**wide)), None), "2^31")
+
+
+@pytest.mark.parametrize("kw", [
+    dict(n_tokens=1 << 29, max_new=1 << 29, n_seq=1, starts=AT),                 # two waves for each of 2^26 records
+    dict(n_tokens=1 << 25, max_new=1, n_seq=1 << 24, starts=AT),                 # one for each of 2^26
+])
+def test_moves_refuse_more_threads_than_a_launch_has(kw):
+    refused(moves(**kw)[1], "too many")
+    if kw["max_new"] > 4:
+        refused(moves(**kw)[0], "too many")
+
+
+def test_evict_refuses_more_threads_than_a_launch_has():
+    refused(evict(n_seq=1 << 20, budget=0), "too many")                  # 2^22 workgroups of 1024
+    wide = dict(table_width=16, table_stride=16, max_len=1024, score_stride=1024)
+    refused(evict(n_seq=1 << 19, budget=2000, **wide), "too many")       # four waves each for 2^26 records
+
+
+@no_gpu
+def test_what_a_launch_has_is_taken():
+    st = moves(n_tokens=1 << 25, max_new=1, n_seq=(1 << 23) - 1, starts=AT)  # 2^25 records less 4
+    assert st == [UNSUPPORTED_DEVICE] * 2
+    assert evict(n_seq=(1 << 20) - 1, budget=0) == UNSUPPORTED_DEVICE

@@ -61,7 +61,7 @@
 
 namespace tkv {
 
-constexpr int kAttendWaves = 4;
+constexpr int kAttendWaves = kBlockThreads / 64;
 constexpr float kFar = -1e30f;  // reference of a row that has seen nothing
 constexpr float kLift = 7.0f;   // weights are held times 2^7
 constexpr float kSlack = 8.0f;

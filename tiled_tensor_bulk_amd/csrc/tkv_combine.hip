@@ -14,9 +14,7 @@
 
 namespace tkv {
 
-constexpr int kCombineThreads = 256;
-constexpr int kFewParts = 16;
-constexpr int kWeighPositions = 4 * kCombineThreads;
+constexpr int kCombineThreads = kBlockThreads;
 
 // Where a row's partial sums are: part s at first + s * stride.
 struct Parts {

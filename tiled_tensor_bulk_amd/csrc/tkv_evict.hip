@@ -26,11 +26,10 @@
 
 namespace tkv {
 
-constexpr int kSelectThreads = 1024;
 constexpr int kSelectWaves = kSelectThreads / 64;
 constexpr int kBins = 2048;
 constexpr int kHeld = 8;  // rows of 4 scores that a lane holds
-constexpr int kEvictWaves = 4;
+constexpr int kEvictWaves = kBlockThreads / 64;
 
 __device__ __forceinline__ uint32_t key_of(float f) {
     uint32_t u = __builtin_bit_cast(uint32_t, f);

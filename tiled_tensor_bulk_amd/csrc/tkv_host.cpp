@@ -88,6 +88,10 @@ bool launchable(Sizes... sizes) {
     return ((__int128)1 * ... * (int64_t)sizes) < kMostBlocks;
 }
 
+// A launch has fewer than 2^32 threads.
+bool fits(int64_t blocks, int threads = tkv::kBlockThreads) { return blocks <= 0xFFFFFFFF / threads; }
+int64_t over(int64_t n, int64_t d) { return (n + d - 1) / d; }
+
 // Positions of a sequence: what kernels add to one before they compare it, a
 // chunk at most, stays within 31 bits.
 constexpr int64_t kMostPositions = 0x7FFFFFFF - 2 * (1 << 16);
@@ -148,16 +152,21 @@ tmap_status check_tokens(const tkv_tokens &in, const char *name, bool fp32_too, 
 }
 
 tmap_status move_args(const tkv_cache *cache, const tkv_tokens *k, const tkv_tokens *v, const tkv_batch *batch,
-                      bool fp32_too, tkv::MoveArgs &a) {
+                      bool append, tkv::MoveArgs &a) {
     TKV_REQUIRE(decode(cache, a.c), "cache was never encoded");
     TKV_REQUIRE(k && v, "k or v is NULL");
     TKV_TRY(check_batch(a.c, batch, a.b, true));
-    TKV_TRY(check_tokens(*k, "k", fp32_too, a.b.n_tokens == 0, a.k));
-    TKV_TRY(check_tokens(*v, "v", fp32_too, a.b.n_tokens == 0, a.v));
+    TKV_TRY(check_tokens(*k, "k", !append, a.b.n_tokens == 0, a.k));
+    TKV_TRY(check_tokens(*v, "v", !append, a.b.n_tokens == 0, a.v));
     TKV_REQUIRE(k->dtype == v->dtype, "k and v must have one type");
     // a run of n positions that starts anywhere touches at most this many records
     a.tiles = a.b.max_new == 0 ? 0 : (int32_t)(((int64_t)a.b.max_new + 2 * (tkv::kTile - 1)) / tkv::kTile);
-    TKV_REQUIRE(launchable(a.tiles, a.b.n_seq, a.c.heads), "too many sequences, heads and new tokens");
+    // a wave for each record, or two
+    constexpr int kWaves = tkv::kBlockThreads / 64;
+    TKV_REQUIRE(launchable(a.tiles, a.b.n_seq, a.c.heads) &&
+                    fits(over((int64_t)a.tiles * a.b.n_seq * a.c.heads,
+                              append && a.b.max_new <= tkv::kFewTokens ? kWaves : kWaves / 2)),
+                "too many sequences, heads and new tokens");
     return TMAP_SUCCESS;
 }
 
@@ -331,7 +340,7 @@ uint64_t tkv_page_bytes(const tkv_cache *cache) {
 tmap_status tkv_append(const tkv_cache *cache, const tkv_tokens *k, const tkv_tokens *v, const tkv_batch *batch,
                        void *hip_stream) {
     tkv::MoveArgs a{};
-    TKV_TRY(move_args(cache, k, v, batch, false, a));
+    TKV_TRY(move_args(cache, k, v, batch, true, a));
     int cus = 0;
     TKV_TRY(device(cus));
     if (a.tiles == 0 || a.b.n_seq == 0) return ok();
@@ -341,7 +350,7 @@ tmap_status tkv_append(const tkv_cache *cache, const tkv_tokens *k, const tkv_to
 tmap_status tkv_read(const tkv_cache *cache, const tkv_tokens *k, const tkv_tokens *v, const tkv_batch *batch,
                      void *hip_stream) {
     tkv::MoveArgs a{};
-    TKV_TRY(move_args(cache, k, v, batch, true, a));
+    TKV_TRY(move_args(cache, k, v, batch, false, a));
     int cus = 0;
     TKV_TRY(device(cus));
     if (a.tiles == 0 || a.b.n_seq == 0) return ok();
@@ -367,11 +376,21 @@ tmap_status tkv_attend(const tkv_cache *cache, const tkv_attend_args *args, cons
     if (a.b.n_seq == 0) return ok();
     if (a.rows == 0) {  // no row to answer; scores_out is still to be scores_in, or 0
         if (!a.scores_out || a.scores_out == a.scores_in || a.max_len == 0) return ok();
+        TKV_REQUIRE(fits((int64_t)a.b.n_seq * a.c.heads * over(a.max_len, tkv::kWeighPositions)),
+                    "too many sequences, heads and positions");
         a.by_heads = divisor(a.c.heads);
         return launched(tkv::launch_weigh(a, hip_stream));
     }
     const Split s = plan(a.c, a.b.n_seq, a.rows, a.max_len, a.scores_out, cus);
-    TKV_REQUIRE(launchable(a.b.n_seq, a.c.heads, s.n_split, s.row_blocks), "too many sequences, heads and rows");
+    // every launch of the call, so that none is refused after another has begun
+    const int64_t heads = (int64_t)a.b.n_seq * a.c.heads;
+    int64_t joining = 0, weighing = 0;
+    if (s.n_split > 1)
+        joining = s.even || s.n_split <= tkv::kFewParts ? over(heads * a.rows, tkv::kBlockThreads / (a.c.dim / 4))
+                                                        : heads * a.rows * (a.c.dim / 32);
+    if (a.scores_out) weighing = heads * over(a.max_len, a.rows <= tkv::kLogitRows ? tkv::kWeighPositions : 128);
+    TKV_REQUIRE((s.even || (launchable(heads, s.n_split, s.row_blocks) && fits(heads * s.n_split * s.row_blocks))) &&
+                    fits(joining + weighing), "too many sequences, heads, rows and positions");
     if (s.total) {
         TKV_REQUIRE(args->workspace && aligned(args->workspace, 16), "workspace is NULL or not 16-byte aligned");
         TKV_REQUIRE(args->workspace_bytes >= s.total, "workspace holds %llu bytes, %llu are needed",
@@ -448,6 +467,10 @@ tmap_status tkv_evict(const tkv_cache *cache, const tkv_evict_args *args, const 
     a.max_len = args->max_len;
     const int64_t width = (int64_t)a.b.table_width << a.c.page_shift;
     if (a.max_len > width) a.max_len = (int32_t)width;
+    const int64_t heads = (int64_t)a.b.n_seq * a.c.heads;
+    TKV_REQUIRE(fits(heads, tkv::kSelectThreads) &&
+                    fits(over(heads * over(a.budget < a.max_len ? a.budget : a.max_len, tkv::kTile), tkv::kBlockThreads / 64)),
+                "too many sequences, heads and positions");
     int cus = 0;
     TKV_TRY(device(cus));
     if (!any) return ok();

@@ -11,6 +11,11 @@ namespace tkv {
 
 constexpr uint32_t kMagic = 0x544B5634u;  // "TKV4"
 constexpr int kTile = 32;                 // positions of a record
+constexpr int kBlockThreads = 256;        // of a workgroup of every kernel but the next
+constexpr int kSelectThreads = 1024;      // ... of the one that chooses what eviction keeps
+constexpr int kFewTokens = 4;             // up to so many new ones append takes one by one
+constexpr int kFewParts = 16;             // up to so many partial sums of a row are joined by its own lanes
+constexpr int kWeighPositions = 4 * kBlockThreads;  // of a workgroup that turns logarithms into weights
 constexpr int kMostResident = 4;           // workgroups that an even split deals to a compute unit
 constexpr int kEvenSeqs = 256;            // most sequences of an even split
 // Scores of up to so many rows go by logarithms kept in memory, 8 bytes a row

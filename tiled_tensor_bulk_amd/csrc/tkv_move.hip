@@ -17,8 +17,7 @@
 
 namespace tkv {
 
-constexpr int kMoveWaves = 4;
-constexpr int kFewTokens = 4;
+constexpr int kMoveWaves = kBlockThreads / 64;
 
 // Nearest whole numbers to (x - z) / s within 0..15, ties to even.  The
 // quotient in fp32 is within 1e-5 of the true one, so only one that close to a
