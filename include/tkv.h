@@ -43,8 +43,7 @@
  *     n_tokens / n_seq.  Rows past max_new are left alone.
  *   - A row of the table holds fewer than 2^31 - 2^17 positions.  A call is
  *     refused whose sequences and heads have together more records, rows or
- *     positions than launches of 2^32 threads hold (2^25 records of a read or
- *     2^24 heads of up to 128 positions, for example).
+ *     positions than launches of 2^32 threads hold.
  *   - Positions whose page is outside the pool (< 0 or >= n_pages), or past
  *     the table's width, do not exist: they are never read or written.
  *   - No two sequences may name the same page where a call writes to it.
@@ -154,9 +153,16 @@ tmap_status tkv_attend(const tkv_cache *cache, const tkv_attend_args *args, cons
 
 /* Workspace that tkv_attend needs for these arguments (pointers are not
  * read; a gfx950 device must be current, as the split of the work goes by
- * its number of compute units). */
+ * its number of compute units).  Smaller sizes may need more, since fewer
+ * workgroups are given shorter pieces. */
 tmap_status tkv_attend_workspace(const tkv_cache *cache, const tkv_attend_args *args, const tkv_batch *batch,
                                  uint64_t *bytes);
+
+/* Enough for these arguments and for every call with no more sequences, new
+ * tokens (n_tokens and max_new) and positions (max_len and what the table
+ * holds), with scores if these have them: to allocate once. */
+tmap_status tkv_attend_workspace_bound(const tkv_cache *cache, const tkv_attend_args *args, const tkv_batch *batch,
+                                       uint64_t *bytes);
 
 /*
  * tkv_evict -- shrink sequences to `budget` positions for each head: the

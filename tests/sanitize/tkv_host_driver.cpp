@@ -161,6 +161,24 @@ int main() {
                 expect(tkv_attend(&c, &a, &b, nullptr) == TMAP_ERROR_INVALID_VALUE, "attend with less workspace");
             }
         }
+        uint64_t bound = 0;
+        if (st == TMAP_SUCCESS) {
+            expect(documented(tkv_attend_workspace_bound(&c, &a, &b, &bound)) && bound >= need, "the bound of a workspace");
+            for (int i = 0; i < 4; ++i) {  // smaller calls
+                tkv_attend_args less = a;
+                tkv_batch fewer = b;
+                if (rnd() % 2) less.max_len = (int32_t)any(a.max_len);
+                if (rnd() % 2) fewer.table_width = (int32_t)any(b.table_width);
+                if (rnd() % 2) fewer.max_new = (int32_t)any(b.max_new);
+                if (rnd() % 2) fewer.n_seq = (int32_t)any(b.n_seq);
+                if (rnd() % 2) fewer.n_tokens = any(b.n_tokens);
+                if (rnd() % 2) less.scores_out = nullptr;
+                fewer.starts = (const int32_t *)kAt;
+                uint64_t some = 0;
+                expect(tkv_attend_workspace(&c, &less, &fewer, &some) == TMAP_SUCCESS && some <= bound,
+                       "the workspace of a smaller call");
+            }
+        }
         tkv_evict_args e;
         std::memset(&e, 0, sizeof e);
         e.scores = (const float *)kAt;

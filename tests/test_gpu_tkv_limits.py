@@ -263,3 +263,36 @@ def test_an_earlier_error_of_the_runtime_is_not_the_calls():
     T.tkv_append(cache, q, q, table, lens)
     torch.cuda.synchronize()
     assert pool.any()
+
+
+# ------------------------------------------------------------------ a workspace made once
+
+def test_a_workspace_serves_smaller_calls():
+    """Room for the largest call of a loop is room for every other one: fewer new tokens, sequences and positions are
+    split in other ways, which may take more of it than the largest call does."""
+    say("workspace")
+    gen = torch.Generator(device=DEV).manual_seed(5)
+    heads, gh, dim, page, n, longest, most = 2, 6, 64, 1024, 3, 60000, 8
+    width = -(-longest // page)
+    pool = torch.empty(n * width * T.tkv_page_bytes_of(heads, dim, page, 64), dtype=torch.uint8, device=DEV)
+    cache = T.tkv_encode(pool, heads, dim, page, 64)
+    table = torch.randperm(n * width, device=DEV, generator=gen).to(torch.int32).view(n, width)
+    k, v = (torch.randn((n * longest, heads, dim), device=DEV, generator=gen).half() for _ in range(2))
+    T.tkv_append(cache, k, v, table, ints([0] * n))
+    q = torch.randn((n * most, heads * gh, dim), device=DEV, generator=gen).half()
+    for scored in (False, True):
+        room = torch.empty(T.tkv_attend_workspace(cache, n, heads * gh, most, longest, scores=scored), dtype=torch.uint8,
+                           device=DEV)
+        for new, max_new, max_len in (([8, 8, 8], 8, 60000), ([8], 8, 60000), ([5], 8, 60000), ([5], 5, 60000), ([1], 1, 60000),
+                                      ([1, 1, 0], 8, 60000), ([1, 1, 1], 1, 30000), ([3], 3, 2000), ([8, 1], 8, 511),
+                                      ([2, 2, 1], 2, 16385)):
+            b, t = len(new), sum(new)
+            lens, starts = ints([max_len - i for i in range(b)]), ints(np.concatenate(([0], np.cumsum(new))))
+            results = []
+            for ws in (None, room):
+                so = torch.zeros((b, heads, width * page), device=DEV) if scored else None
+                got = T.tkv_attend(cache, q[:t], table[:b], lens, starts=starts, max_new=max_new, max_len=max_len,
+                                   scores_out=so, workspace=ws)
+                results.append(got + ((so,) if scored else ()))
+            for x, y in zip(*results):
+                assert torch.equal(x, y), (new, max_new, max_len)

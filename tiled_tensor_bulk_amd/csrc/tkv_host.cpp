@@ -262,6 +262,31 @@ Split plan(const Cache &c, int64_t n_seq, int64_t rows, int64_t max_len, bool sc
     return s;
 }
 
+// What plan() takes at most of a workspace for no more sequences, rows and
+// positions than these.  Fewer of them may need more: chunks get shorter when
+// there are fewer workgroups to fill the card with.
+uint64_t most_workspace(const Cache &c, int64_t n_seq, int64_t rows, int64_t max_len, bool scores, int cus) {
+    const auto least = [](uint64_t a, uint64_t b) { return a < b ? a : b; };
+    const auto most = [](uint64_t a, uint64_t b) { return a > b ? a : b; };
+    const uint64_t heads = (uint64_t)n_seq * c.heads, few = least(rows, 48);
+    const auto chunks = [&](int64_t chunk) { return (uint64_t)((max_len + chunk - 1) / chunk); };
+    // rows of partial sums.  In chunks shorter than kMostChunk: the workgroups, kBlocksPerCu for a
+    // compute unit of 32 rows or kRowBlocksPerCu of 128, and no more than chunks of 256 make
+    uint64_t parts = least((uint64_t)cus * most(kBlocksPerCu * 32, kRowBlocksPerCu * 128), heads * rows * chunks(256));
+    if (chunks(kMostChunk) > 1) parts = most(parts, heads * rows * chunks(kMostChunk));
+    if (max_len > kLeastChunk)  // an even split: tiles of 16 rows up to 48 of them, or of 32
+        parts = most(parts, least(n_seq, tkv::kEvenSeqs) * c.heads * (few + 15) +
+                                (uint64_t)cus * tkv::kMostResident * least(rows, 32));
+    uint64_t total = 0;
+    if (max_len > 256) total = up(parts * c.dim * 4, 256) + up(parts * 8, 256) + up((tkv::kEvenSeqs + 1) * 4, 256);
+    if (scores) {
+        const uint64_t tiles = (uint64_t)(rows + 15) / 16;
+        const uint64_t logits = heads * up((uint64_t)max_len, tkv::kTile) * least(rows, tkv::kLogitRows) * 4;
+        total += up(most(logits, heads * tiles * (32 * c.dim + 1024)), 256) + up(heads * tiles * 16 * 8, 256);
+    }
+    return total;
+}
+
 tmap_status attend_args(const tkv_cache *cache, const tkv_attend_args *in, const tkv_batch *batch, bool pointers,
                         tkv::AttendArgs &a) {
     TKV_REQUIRE(decode(cache, a.c), "cache was never encoded");
@@ -365,6 +390,17 @@ tmap_status tkv_attend_workspace(const tkv_cache *cache, const tkv_attend_args *
     int cus = 0;
     TKV_TRY(device(cus));
     *bytes = a.rows > 0 && a.b.n_seq > 0 ? plan(a.c, a.b.n_seq, a.rows, a.max_len, a.scores_out, cus).total : 0;
+    return ok();
+}
+
+tmap_status tkv_attend_workspace_bound(const tkv_cache *cache, const tkv_attend_args *args, const tkv_batch *batch,
+                                       uint64_t *bytes) {
+    tkv::AttendArgs a{};
+    TKV_REQUIRE(bytes, "bytes is NULL");
+    TKV_TRY(attend_args(cache, args, batch, false, a));
+    int cus = 0;
+    TKV_TRY(device(cus));
+    *bytes = a.rows > 0 && a.b.n_seq > 0 ? most_workspace(a.c, a.b.n_seq, a.rows, a.max_len, a.scores_out, cus) : 0;
     return ok();
 }
 

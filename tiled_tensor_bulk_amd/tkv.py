@@ -87,8 +87,10 @@ def lib():
             f.restype = ctypes.c_int
         L.tkv_attend.argtypes = [P(tkv_cache), P(tkv_attend_args), P(tkv_batch), vp]
         L.tkv_attend.restype = ctypes.c_int
-        L.tkv_attend_workspace.argtypes = [P(tkv_cache), P(tkv_attend_args), P(tkv_batch), P(ctypes.c_uint64)]
-        L.tkv_attend_workspace.restype = ctypes.c_int
+        for name in ("tkv_attend_workspace", "tkv_attend_workspace_bound"):
+            f = getattr(L, name)
+            f.argtypes = [P(tkv_cache), P(tkv_attend_args), P(tkv_batch), P(ctypes.c_uint64)]
+            f.restype = ctypes.c_int
         L.tkv_evict.argtypes = [P(tkv_cache), P(tkv_evict_args), P(tkv_batch), vp]
         L.tkv_evict.restype = ctypes.c_int
         L.tkv_last_error_detail.argtypes = []
@@ -210,15 +212,16 @@ def tkv_attend(cache: tkv_cache, q, table, lens, starts=None, max_new: Optional[
 
 def tkv_attend_workspace(cache: tkv_cache, n_seq: int, q_heads: int, max_new: int, max_len: int,
                          scores: bool = False) -> int:
-    """Bytes of workspace for a tkv_attend call to which these max_new and max_len are given (smaller ones may need
-    more, as the work is then split in another way)."""
+    """Bytes of workspace that are enough for every tkv_attend call with at most n_seq sequences, max_new new tokens
+    of each and max_len positions (as given, or as what the table holds), with scores if asked for.  With scores of few
+    rows, 4 bytes for each sequence, head, row and position of max_len are the most of it."""
     width = -(-max_len // cache.page_tokens)
     t = tkv_tokens(None, 0, 0, _DTYPES[torch.bfloat16])
     a = tkv_attend_args(t, t, None, None, 4 if scores else None, max_len, q_heads, max_len, 1.0, 0, None, 0)
     b = tkv_batch(4, width, 4, None, n_seq * max_new, n_seq, width, max_new)  # pointers are not read
     need = ctypes.c_uint64()
-    _check(lib().tkv_attend_workspace(ctypes.byref(cache), ctypes.byref(a), ctypes.byref(b), ctypes.byref(need)),
-           "tkv_attend_workspace")
+    _check(lib().tkv_attend_workspace_bound(ctypes.byref(cache), ctypes.byref(a), ctypes.byref(b), ctypes.byref(need)),
+           "tkv_attend_workspace_bound")
     return need.value
 
 
