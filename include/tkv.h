@@ -79,7 +79,8 @@ tmap_status tkv_encode(tkv_cache *cache, void *pool, int64_t n_pages, uint32_t n
 uint64_t tkv_page_bytes(const tkv_cache *cache);
 
 /* A strided tensor of 16- or 32-bit elements [tokens][heads][head_dim], the
- * last dimension contiguous; strides in elements. */
+ * last dimension contiguous; strides in elements.  Rows that a call writes lie
+ * apart, and apart from what it reads, but that out may be q itself. */
 typedef struct tkv_tokens {
     void *data;
     int64_t token_stride, head_stride;

@@ -296,3 +296,51 @@ def test_a_workspace_serves_smaller_calls():
                 results.append(got + ((so,) if scored else ()))
             for x, y in zip(*results):
                 assert torch.equal(x, y), (new, max_new, max_len)
+
+
+# ------------------------------------------------------------------ outputs over one another, and over the queries
+
+def test_outputs_whose_rows_overlap_are_refused():
+    rng = np.random.default_rng(1)
+    table, _ = tables(rng, 1, 2)
+    ref = a_ref(rng, 2, 2, 64, 32, 32, table, [40])
+    cache, _ = a_cache(ref)
+    q = torch.ones((3, 4, 64), dtype=torch.float16, device=DEV)
+    flat = torch.zeros(4096, dtype=torch.float16, device=DEV)
+    for out in (q[:1].expand(3, 4, 64), q[:, :1].expand(3, 4, 64), flat.as_strided((3, 4, 64), (128, 64, 1)),
+                flat.as_strided((3, 4, 64), (64, 128, 1))):
+        with pytest.raises(ValueError, match="out's rows overlap"):
+            T.tkv_attend(cache, q, ints(table), ints([40]), out=out)
+    k = flat[:2 * 64].view(1, 2, 64).expand(3, 2, 64)
+    with pytest.raises(ValueError, match="k's rows overlap"):
+        T.tkv_read(cache, ints(table), ints([0]), k=k, v=k)
+    # rows by heads first, and queries that are one row
+    out = torch.zeros((4, 3, 64), dtype=torch.float16, device=DEV).transpose(0, 1)
+    one = q[:1, :1].expand(3, 4, 64)
+    T.tkv_attend(cache, one, ints(table), ints([40]), out=out)
+    want, _ = T.tkv_attend(cache, q, ints(table), ints([40]))
+    assert torch.equal(out, want)
+
+
+@pytest.mark.parametrize("gh,new,wide,length", [(4, 1, 1, 30), (4, 1, 1, 3000), (8, 1, 600, 900), (7, 3, 1, 700), (5, 13, 1, 600),
+                                                (3, 50, 1, 3000)])
+def test_the_output_in_place_of_the_queries(gh, new, wide, length):
+    """Every way of splitting the work reads a row of q before it, or a later kernel, writes that row."""
+    say(f"in place {gh} {new} {length}")
+    rng = np.random.default_rng(gh + new)
+    heads, dim, page, n = 2, 128, 32, 3
+    held = -(-length // page)
+    table = np.full((n, held * wide), -1, np.int32)
+    table[:, :held] = rng.permutation(n * held).reshape(n, held)
+    ref = a_ref(rng, n * held, heads, dim, page, 64, table, [length] * n)
+    cache, _ = a_cache(ref)
+    q, _ = typed(rng.standard_normal((n * new, heads * gh, dim)), "bf16")
+    for scored in (False, True):
+        got = []
+        for out in (None, q.clone()):
+            so = torch.zeros((n, heads, held * wide * page), device=DEV) if scored else None
+            o, lse = T.tkv_attend(cache, q if out is None else out, ints(table), ints([length, length - 5, 1]), scores_out=so,
+                                  out=out)
+            got.append((o, lse) + ((so,) if scored else ()))
+        for x, y in zip(*got):
+            assert torch.equal(x, y)

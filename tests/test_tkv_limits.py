@@ -101,3 +101,24 @@ def test_what_a_launch_has_is_taken():
     st = moves(n_tokens=1 << 25, max_new=1, n_seq=(1 << 23) - 1, starts=AT)  # 2^25 records less 4
     assert st == [UNSUPPORTED_DEVICE] * 2
     assert evict(n_seq=(1 << 20) - 1, budget=0) == UNSUPPORTED_DEVICE
+
+
+# ------------------------------------------------------------------ rows that are written over one another
+
+@pytest.mark.parametrize("kw", [dict(ts=0), dict(hs=0), dict(ts=127), dict(hs=64)])
+def test_written_rows_that_overlap_are_refused(kw):
+    _, c = encode()
+    r = ctypes.byref
+    refused(T.lib().tkv_read(r(c), r(tokens(**kw)), r(tokens()), r(batch()), None), "k's rows overlap")
+    refused(T.lib().tkv_read(r(c), r(tokens()), r(tokens(**kw)), r(batch()), None), "v's rows overlap")
+    refused(attend(out=tokens(**kw)), "out's rows overlap")
+
+
+@no_gpu
+def test_rows_that_are_read_may_be_one():
+    _, c = encode()
+    one, r = tokens(ts=0, hs=0), ctypes.byref
+    assert T.lib().tkv_append(r(c), r(one), r(one), r(batch()), None) == UNSUPPORTED_DEVICE
+    assert attend(q=one) == UNSUPPORTED_DEVICE
+    alone = batch(n_seq=1, n_tokens=1, max_new=1)  # the stride of a single row is not looked at
+    assert T.lib().tkv_read(r(c), r(tokens(ts=0)), r(tokens(ts=0)), r(alone), None) == UNSUPPORTED_DEVICE

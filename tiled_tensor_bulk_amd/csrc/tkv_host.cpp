@@ -151,6 +151,13 @@ tmap_status check_tokens(const tkv_tokens &in, const char *name, bool fp32_too, 
     return TMAP_SUCCESS;
 }
 
+// Rows that a call writes may not lie in one another.
+tmap_status check_written(const tkv_tokens &out, const char *name, int64_t n_tokens, int64_t heads, uint32_t dim) {
+    TKV_REQUIRE((n_tokens < 2 || out.token_stride >= dim) && (heads < 2 || out.head_stride >= dim),
+                "%s's rows overlap: a stride is less than head_dim", name);
+    return TMAP_SUCCESS;
+}
+
 tmap_status move_args(const tkv_cache *cache, const tkv_tokens *k, const tkv_tokens *v, const tkv_batch *batch,
                       bool append, tkv::MoveArgs &a) {
     TKV_REQUIRE(decode(cache, a.c), "cache was never encoded");
@@ -159,6 +166,10 @@ tmap_status move_args(const tkv_cache *cache, const tkv_tokens *k, const tkv_tok
     TKV_TRY(check_tokens(*k, "k", !append, a.b.n_tokens == 0, a.k));
     TKV_TRY(check_tokens(*v, "v", !append, a.b.n_tokens == 0, a.v));
     TKV_REQUIRE(k->dtype == v->dtype, "k and v must have one type");
+    if (!append) {
+        TKV_TRY(check_written(*k, "k", a.b.n_tokens, a.c.heads, a.c.dim));
+        TKV_TRY(check_written(*v, "v", a.b.n_tokens, a.c.heads, a.c.dim));
+    }
     // a run of n positions that starts anywhere touches at most this many records
     a.tiles = a.b.max_new == 0 ? 0 : (int32_t)(((int64_t)a.b.max_new + 2 * (tkv::kTile - 1)) / tkv::kTile);
     // a wave for each record, or two
@@ -298,6 +309,7 @@ tmap_status attend_args(const tkv_cache *cache, const tkv_attend_args *in, const
     TKV_REQUIRE(in->q.dtype == in->out.dtype, "q and out must have one type");
     TKV_REQUIRE(empty || (in->lse && aligned(in->lse, 4)), "lse is NULL or not 4-byte aligned");
     TKV_REQUIRE(in->q_heads > 0 && in->q_heads % (int64_t)a.c.heads == 0, "q_heads must be a multiple of n_heads");
+    if (pointers) TKV_TRY(check_written(in->out, "out", a.b.n_tokens, in->q_heads, a.c.dim));
     TKV_REQUIRE(in->max_len >= 0, "max_len is negative");
     TKV_REQUIRE(std::isfinite(in->scale), "scale is not finite");
     TKV_REQUIRE(in->causal == 0 || in->causal == 1, "causal must be 0 or 1");

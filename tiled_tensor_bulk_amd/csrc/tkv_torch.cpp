@@ -73,6 +73,14 @@ tkv_tokens tokens(const Tensor &t, const char *what, int64_t heads, int64_t n_to
     return {t.data_ptr(), t.stride(0), t.stride(1), type};
 }
 
+// A tensor that a call writes: its rows are apart.
+void apart(const tkv_tokens &t, const char *what, const Tensor &x) {
+    const int64_t n = x.size(0), heads = x.size(1), dim = x.size(2), ts = t.token_stride, hs = t.head_stride;
+    TKV_CHECK((n < 2 || ts >= (heads - 1) * hs + dim || heads < 2 || hs >= (n - 1) * ts + dim) &&
+                  (n < 2 || ts >= dim) && (heads < 2 || hs >= dim), what, "'s rows overlap: strides ", x.strides(), " of ",
+              x.sizes());
+}
+
 struct Table {
     const int32_t *data;
     int64_t stride;
@@ -170,6 +178,8 @@ py::tuple do_read(const Cache &c, const Tensor &table, const Tensor &lens, const
     }
     const tkv_tokens kt = tokens(k, "k", c.heads, n_tokens.value_or(-1), true, c);
     const tkv_tokens vt = tokens(v, "v", c.heads, k.size(0), true, c);
+    apart(kt, "k", k);
+    apart(vt, "v", v);
     const Batch b = batch(c, table, lens, starts, k.size(0), max_new);
     const int st = tkv_read(&c.described, &kt, &vt, &b.b, on.handle);
     return py::make_tuple(st, k, v);
@@ -200,6 +210,7 @@ py::tuple do_attend(const Cache &c, const Tensor &q, const Tensor &table, const 
     const Tensor out = out_ ? *out_ : made({n, heads, c.dim}, q.scalar_type(), c);
     const Tensor lse = lse_ ? *lse_ : made({n, heads}, at::kFloat, c);
     a.out = tokens(out, "out", heads, n, false, c);
+    apart(a.out, "out", out);
     TKV_CHECK(out.scalar_type() == q.scalar_type(), "out must be ", name_of(q.scalar_type()));
     typed(lse, "lse", at::kFloat, c);
     TKV_CHECK(lse.dim() == 2 && lse.size(0) == n && lse.size(1) == heads && lse.is_contiguous(),
