@@ -344,3 +344,22 @@ def test_the_output_in_place_of_the_queries(gh, new, wide, length):
             got.append((o, lse) + ((so,) if scored else ()))
         for x, y in zip(*got):
             assert torch.equal(x, y)
+
+
+# ------------------------------------------------------------------ gradients
+
+def test_gradients_are_refused_and_not_needed_under_no_grad():
+    pool = torch.zeros(T.tkv_page_bytes_of(2, 64, 32, 32), dtype=torch.uint8, device=DEV)
+    cache, table, lens = T.tkv_encode(pool, 2, 64, 32, 32), ints([[0]]), ints([0])
+    x = torch.ones((1, 2, 64), dtype=torch.float16, device=DEV, requires_grad=True)
+    scores = torch.zeros((1, 2, 32), device=DEV, requires_grad=True)
+    for call in (lambda: T.tkv_append(cache, x, x, table, lens), lambda: T.tkv_attend(cache, x, table, lens + 1),
+                 lambda: T.tkv_attend(cache, x.detach(), table, lens + 1, scores=scores, scores_out=scores.detach()),
+                 lambda: T.tkv_read(cache, table, lens, k=x, v=x),
+                 lambda: T.tkv_evict(cache, table, lens, scores, 5, 1, table)):
+        with pytest.raises(ValueError, match="gradient"):
+            call()
+    with torch.no_grad():
+        T.tkv_append(cache, x, x, table, lens)
+        out, _ = T.tkv_attend(cache, x, table, lens + 1)
+    assert torch.equal(out, torch.ones_like(out))

@@ -122,3 +122,21 @@ def test_rows_that_are_read_may_be_one():
     assert attend(q=one) == UNSUPPORTED_DEVICE
     alone = batch(n_seq=1, n_tokens=1, max_new=1)  # the stride of a single row is not looked at
     assert T.lib().tkv_read(r(c), r(tokens(ts=0)), r(tokens(ts=0)), r(alone), None) == UNSUPPORTED_DEVICE
+
+
+# ------------------------------------------------------------------ gradients
+
+def test_a_gradient_that_would_be_lost_is_refused():
+    st, c = encode()
+    calls = T._calls()
+    cache = calls.Cache(ctypes.addressof(c), torch.zeros(16, dtype=torch.uint8), 4, 128, 64)
+    ints = torch.zeros((1, 1), dtype=torch.int32)
+    k = torch.zeros((1, 4, 128), dtype=torch.bfloat16)
+    asks = k.clone().requires_grad_()
+    for x, word in ((k, "GPU"), (asks, "requires a gradient"), (asks * 2, "requires a gradient")):
+        with pytest.raises(ValueError, match=word):
+            calls.append(cache, x, x, ints, ints[0], None, None, None)
+        with pytest.raises(ValueError, match=word):
+            calls.attend(cache, x, ints, ints[0], None, None, None, None, True, None, None, None, None, None, None)
+    with torch.no_grad(), pytest.raises(ValueError, match="GPU"):  # on to the next check
+        calls.append(cache, asks, asks, ints, ints[0], None, None, None)

@@ -7,6 +7,7 @@
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/utils/pybind.h>
 
+#include <ATen/core/grad_mode.h>
 #include <ATen/ops/empty.h>
 #include <c10/hip/HIPGuard.h>
 #include <c10/hip/HIPStream.h>
@@ -46,6 +47,9 @@ const char *name_of(at::ScalarType t) {
 }
 
 void on_gpu(const Tensor &t, const char *what, const Cache &c) {
+    // nothing here has a backward pass: a gradient that is asked for would be lost without a word
+    TKV_CHECK(!(t.requires_grad() && at::GradMode::is_enabled()), what,
+              " requires a gradient, and these operators give none: call them under torch.no_grad()");
     TKV_CHECK(t.is_cuda(), what, " must be a GPU tensor");
     TKV_CHECK(t.device() == c.pool.device(), what, " is on ", t.device(), ", the cache on ", c.pool.device());
 }
@@ -138,14 +142,13 @@ Batch batch(const Cache &c, const Tensor &table, const Tensor &lens, const Maybe
 // that was queued before the memory was given back.
 struct Stream {
     std::optional<c10::hip::HIPStreamGuard> guard;
-    void *handle;
     Stream(const Cache &c, std::optional<int64_t> given) {
         if (given) {
             on_current_device(c);
             guard.emplace(c10::hip::getStreamFromExternal((hipStream_t)*given, c.pool.device().index()));
         }
-        handle = (void *)c10::hip::getCurrentHIPStream().stream();
     }
+    void *handle() const { return (void *)c10::hip::getCurrentHIPStream().stream(); }
 };
 
 Tensor made(at::IntArrayRef size, at::ScalarType type, const Cache &c) {
@@ -159,7 +162,7 @@ int do_append(const Cache &c, const Tensor &k, const Tensor &v, const Tensor &ta
     const tkv_tokens vt = tokens(v, "v", c.heads, n, false, c);
     const Batch b = batch(c, table, lens, starts, n, max_new);
     const Stream on(c, stream);
-    return tkv_append(&c.described, &kt, &vt, &b.b, on.handle);
+    return tkv_append(&c.described, &kt, &vt, &b.b, on.handle());
 }
 
 py::tuple do_read(const Cache &c, const Tensor &table, const Tensor &lens, const Maybe &starts,
@@ -181,7 +184,7 @@ py::tuple do_read(const Cache &c, const Tensor &table, const Tensor &lens, const
     apart(kt, "k", k);
     apart(vt, "v", v);
     const Batch b = batch(c, table, lens, starts, k.size(0), max_new);
-    const int st = tkv_read(&c.described, &kt, &vt, &b.b, on.handle);
+    const int st = tkv_read(&c.described, &kt, &vt, &b.b, on.handle());
     return py::make_tuple(st, k, v);
 }
 
@@ -245,7 +248,7 @@ py::tuple do_attend(const Cache &c, const Tensor &q, const Tensor &table, const 
         a.workspace = room.data_ptr();
         a.workspace_bytes = (uint64_t)room.numel();
     }
-    if (st == TMAP_SUCCESS) st = tkv_attend(&c.described, &a, &b.b, on.handle);
+    if (st == TMAP_SUCCESS) st = tkv_attend(&c.described, &a, &b.b, on.handle());
     return py::make_tuple(st, out, lse);
 }
 
@@ -279,7 +282,7 @@ py::tuple do_evict(const Cache &c, const Tensor &table, const Tensor &lens, cons
     a.dst_width = t.width;
     a.budget = (int32_t)budget;
     a.recent = (int32_t)recent;
-    const int st = tkv_evict(&c.described, &a, &b.b, on.handle);
+    const int st = tkv_evict(&c.described, &a, &b.b, on.handle());
     return py::make_tuple(st, kept, lens_out, scores_out);
 }
 

@@ -9,7 +9,8 @@ Names match the C ABI.  Tensors lie on the current GPU; work goes to `stream`
 workspace are allocated with torch where they are not given, from the memory
 of that stream; outputs are kept for torch's current stream too.  A caller who
 names a stream orders it after the work that makes the inputs, and keeps these
-until it is done with them, as everywhere in torch.
+until it is done with them, as everywhere in torch.  There is no backward pass:
+a tensor that requires a gradient is refused outside torch.no_grad().
 
     pool  = torch.empty(n_pages * tkv_page_bytes_of(heads, dim, page, group), dtype=torch.uint8, device="cuda")
     cache = tkv_encode(pool, heads, dim, page, group)
