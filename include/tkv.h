@@ -44,6 +44,8 @@
  *   - A row of the table holds fewer than 2^31 - 2^17 positions.  A call is
  *     refused whose sequences and heads have together more records, rows or
  *     positions than launches of 2^32 threads hold.
+ *   - A length below 0 counts as 0 to attention and eviction; append and read
+ *     leave such a sequence alone.
  *   - Positions whose page is outside the pool (< 0 or >= n_pages), or past
  *     the table's width, do not exist: they are never read or written.
  *   - No two sequences may name the same page where a call writes to it.
@@ -134,7 +136,8 @@ tmap_status tkv_read(const tkv_cache *cache, const tkv_tokens *k, const tkv_toke
  *
  * Products of q with codes are exact up to their fp32 sum; softmax, sums and
  * K's scales are fp32; a weight, and a V element's scale * (code - 8), are
- * rounded to fp16 once each on their way into the matrix unit.
+ * rounded to fp16 once each on their way into the matrix unit.  A row whose
+ * logarithms to base 2 all lie below -10^30 counts as one that sees nothing.
  */
 typedef struct tkv_attend_args {
     tkv_tokens q, out;        /* [n_tokens][q_heads][head_dim], fp16 or bf16, one type  */

@@ -1,7 +1,8 @@
 // tkv_move.hip -- new tokens into the cache (append) and positions out of it
 // (read).
 //
-// A wave takes one record: 32 positions of one head of one sequence.  A K
+// A record, 32 positions of one head of one sequence, has two waves, one for
+// its keys and one for its values; of a few new tokens one wave takes both.  A K
 // word belongs to one position, but a V word holds 8 positions of a channel,
 // so one wave owns a record's V words: where some of a word's positions are not
 // new, it reads the word, replaces the new nibbles and writes it back, with no
@@ -10,9 +11,13 @@
 //
 // What bounds them: memory, at two bytes of input (or four of output) for each
 // half byte of cache, and in append next to it the vector units, which take some
-// 17 instructions to quantise an element.  8 prompts of up to 4001 tokens, 25
+// 17 instructions to quantise an element, and the code's size: the exact
+// comparison is there for every word, 39 KB in all with 128 channels, and 75 with
+// 256, where the instruction cache holds 64 for two compute units.  8 prompts of up to 4001 tokens, 25
 // thousand in all, 8 heads of 128 channels: append 47 us for 131 MB, 2.8 TB/s, of
-// which the instructions alone are 29; read into fp32 50 us for 234 MB, 4.7 TB/s,
+// which the instructions alone are 29; read into fp32 42 us for 234 MB, 5.5 TB/s.
+// 4 heads of 256 channels, as many bytes: append 56 us (242 registers, two
+// waves a SIMD), read 49; 8 heads of 96: 33 and 31.
 #include "tkv_format.h"
 
 namespace tkv {
