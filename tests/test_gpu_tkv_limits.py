@@ -363,3 +363,60 @@ def test_gradients_are_refused_and_not_needed_under_no_grad():
         T.tkv_append(cache, x, x, table, lens)
         out, _ = T.tkv_attend(cache, x, table, lens + 1)
     assert torch.equal(out, torch.ones_like(out))
+
+
+# ------------------------------------------------------------------ offsets past 32 bits
+
+def test_offsets_past_32_bits():
+    """Pages, token rows and scores that lie past 2^32 bytes, and 2^31 elements, of their tensors: the same answers as
+    near their beginnings."""
+    say("offsets")
+    heads, gh, dim, page, group = 2, 2, 128, 1024, 32
+    each = T.tkv_page_bytes_of(heads, dim, page, group)
+    many = (9 << 30) // each
+    n, new = 2, 40  # tokens before and now, of two sequences
+    gen = torch.Generator(device=DEV).manual_seed(9)
+    rows = torch.randn((3, n * new, heads * gh, dim), device=DEV, generator=gen).half()
+    far = torch.empty((n * new, 1 << 26), dtype=torch.float16, device=DEV)  # 2^26 elements between tokens
+    wide = 1 << 30
+    results = []
+    for high in (False, True):
+        pool = torch.empty((many if high else 4) * each, dtype=torch.uint8, device=DEV)
+        cache = T.tkv_encode(pool, heads, dim, page, group)
+        last = cache.n_pages - 1
+        table, dst = ints([[last], [last - 2]]), ints([[last - 1], [last - 3]])
+        for p in (last, last - 1, last - 2, last - 3):
+            pool[p * each:(p + 1) * each].zero_()
+
+        def place(x, column=0):
+            if not high:
+                return x
+            y = far[:, column:column + x.shape[1] * dim].unflatten(1, (x.shape[1], dim))
+            y.copy_(x)
+            return y
+
+        lens = ints([0, 3])
+        T.tkv_append(cache, place(rows[0][:, :heads]), rows[1][:, :heads], table, lens)
+        T.tkv_append(cache, rows[0][:2, :heads], place(rows[1][:, :heads])[-2:], table, lens + new)
+        lens += new + 1
+        got = []
+        cap = wide if high else page
+        so = torch.empty((n, heads, cap), device=DEV)
+        si = so.new_zeros((n, heads, 50)) + torch.arange(50, device=DEV) / 8
+        so[:, :, :50] = si
+        for q in (rows[2][:n], rows[2]):  # kept logarithms, and computed again
+            q = place(torch.cat((q, rows[2]))[:n * new])[-q.shape[0]:]
+            got += T.tkv_attend(cache, q, table, lens, max_len=50, scores=so, scores_out=so)
+            out = place(torch.zeros_like(rows[2]), 4096)[-q.shape[0]:]  # beside q
+            T.tkv_attend(cache, q, table, lens, max_len=50, out=out)
+            got.append(out.clone())
+        got.append(so[:, :, :41].clone())
+        kept, left, ks = T.tkv_evict(cache, table, lens, so, 20, 4, dst, max_len=50)
+        k, v = place(torch.zeros_like(rows[0][:, :heads])), torch.zeros_like(rows[0][:, :heads])
+        T.tkv_read(cache, dst, ints([0, 0]), starts=ints([40, 60, 80]), max_new=20, k=k, v=v)
+        got += [kept, left, ks, k[40:].clone(), v[40:].clone()]
+        results.append(got)
+        del pool, cache, so
+    for i, (x, y) in enumerate(zip(*results)):
+        assert torch.equal(x, y), i
+    assert results[1][-1].any() and (results[1][-5] >= 0).all()
