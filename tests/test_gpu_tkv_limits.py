@@ -1,5 +1,6 @@
-"""The operators on the 4-bit cache at the edges of their batches: lengths past what a table holds, lengths shrunk in place,
-streams other than the current one.  The plain implementation is tests/tkv_ref.py, asked for one new token at a time;
+"""The operators on the 4-bit cache at the edges of their calls: lengths past what a table holds, lengths shrunk and outputs
+written in place, streams other than the current one, batches with nothing new, a workspace made once, errors of others,
+gradients, offsets past 32 bits.  The plain implementation is tests/tkv_ref.py, asked for one new token at a time;
 tolerances are those of tests/test_gpu_tkv.py, and what is not a number fails."""
 import numpy as np
 import pytest

@@ -1,4 +1,5 @@
-"""What libtkv refuses beyond tests/test_tkv_boundary.py: overlaps, and sizes that no launch has.  Without a GPU, with pointers that nothing reads;
+"""What libtkv refuses beyond tests/test_tkv_boundary.py: overlaps, sizes that no
+launch has, gradients.  Without a GPU, with pointers that nothing reads;
 what is not refused stops at the device."""
 import ctypes
 
