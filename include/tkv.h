@@ -1,6 +1,6 @@
 /*
- * tkv.h -- C ABI of libtkv: a paged key/value cache held in 4 bits, and the
- * operators of a language model's decoding loop on it, on AMD Instinct
+ * tkv.h -- C ABI of libtkv: a paged key/value cache held in 4 or 8 bits, and
+ * the operators of a language model's decoding loop on it, on AMD Instinct
  * MI355X (gfx950).
  *
  * A pool holds pages; a page holds `page_tokens` positions of every key/value
@@ -10,11 +10,15 @@
  * A table names the pages of each sequence: position p of sequence b lies in
  * page table[b][p / page_tokens].
  *
- * Numbers.  A key or value element is scale * code + zero: code in 0..15,
- * scale and zero fp16, one pair for each position and each group of `group`
- * neighbouring channels.
+ * Numbers, 4 bits.  A key or value element is scale * code + zero: code in
+ * 0..15, scale and zero fp16, one pair for each position and each group of
+ * `group` neighbouring channels.
  *
- * Record of 32 positions (dim = head_dim, W = dim / 32 words, groups =
+ * Numbers, 8 bits.  An element is 2^(E - 127) * code: code an e4m3 number (OCP,
+ * largest 448), E a byte, one for the keys and one for the values of a record;
+ * E = 0 stands for 0.
+ *
+ * Record of 32 positions, 4 bits (dim = head_dim, W = dim / 32 words, groups =
  * dim / group; S = 2 where W > 4, else 1, and w = W / S):
  *   byte 0                    K codes, uint32 [2 halves][S][64 lanes][w]
  *   16 * dim                  V codes, the same shape
@@ -27,6 +31,14 @@
  * and slot 8 * g + j of the V pairs is that same position.  This is the order
  * in which v_mfma_f32_16x16x32_f16 takes its operands: attention reads words in
  * whole wave-wide runs, and a lane's words are its part of the operand.
+ *
+ * Record of 32 positions, 8 bits (64 * dim + 128 bytes), the same order:
+ *   byte 0                    K codes [2 halves][W][64 lanes][8]
+ *   32 * dim                  V codes [dim / 16][64 lanes][8]
+ *   64 * dim                  E of the keys, E of the values; the rest is unused
+ *   K: position 16 * half + m, channel 32 * i + 8 * g + j
+ *   V: channel 16 * i + m, position 4 * g + (j & 3) + 16 * (j >> 2)
+ * where byte j of lane 16 * g + m is in run i.
  *
  * Conventions for every call:
  *   - Pointers are HIP device pointers, unless they are `tkv_cache *`.  The
@@ -76,8 +88,13 @@ typedef struct __attribute__((aligned(64))) tkv_cache {
 tmap_status tkv_encode(tkv_cache *cache, void *pool, int64_t n_pages, uint32_t n_heads, uint32_t head_dim,
                        uint32_t page_tokens, uint32_t group);
 
-/* Bytes of one page (all heads): n_heads * page_tokens / 32 *
- * (32 * head_dim + 256 * head_dim / group).  0 for a cache never encoded. */
+/* The same of a pool in 8 bits. */
+tmap_status tkv_encode8(tkv_cache *cache, void *pool, int64_t n_pages, uint32_t n_heads, uint32_t head_dim,
+                        uint32_t page_tokens);
+
+/* Bytes of one page (all heads): n_heads * page_tokens / 32 * the record's
+ * bytes, 32 * head_dim + 256 * head_dim / group or 64 * head_dim + 128.
+ * 0 for a cache never encoded. */
 uint64_t tkv_page_bytes(const tkv_cache *cache);
 
 /* A strided tensor of 16- or 32-bit elements [tokens][heads][head_dim], the
@@ -107,9 +124,42 @@ typedef struct tkv_batch {
  *   code   = (x - zero) / scale to the nearest whole number, ties to even,
  *            within 0..15 (decided exactly); 0 where scale is 0
  * k and v are fp16 or bf16, of the same type.  What is cached is finite.
+ *
+ * In 8 bits, with x as above: E is the smallest one of at least 27 with |x| <=
+ * 448 * 2^(E - 127) for all of a record's new positions (of a head's keys, or
+ * values), and at least what the record has if positions below lens[b] lie in
+ * it; code = x / 2^(E - 127) to the nearest e4m3 number, ties to even.  Where
+ * E grows, the codes of those earlier positions are rounded to it in the same
+ * manner: by a power of two, so exactly but where they become subnormal.
  */
 tmap_status tkv_append(const tkv_cache *cache, const tkv_tokens *k, const tkv_tokens *v, const tkv_batch *batch,
                        void *hip_stream);
+
+/*
+ * tkv_append_rotated -- the same, with the keys turned by their positions on the
+ * way, and queries beside them.  A token at position p turns its pairs (a, b) of
+ * channels into (a * c - b * s, b * c + a * s) with c and s from row p of a
+ * table, each product and sum rounded to fp32; what comes is quantised as above
+ * (NaN and the limits after the turn).  Values are as they are.  Queries are
+ * turned in the same manner and rounded to their type.
+ *   p is lens[b] + i for a sequence's i-th new token, or positions[row].  A
+ *   token whose p is not in the table is left alone: neither its key nor its
+ *   value is cached, and its query is not written.
+ */
+typedef struct tkv_rotation {
+    const float *cos_sin;     /* [n_positions][rot_dim]: the pairs' cosines, then their sines  */
+    int64_t stride;           /* floats from one position to the next, at least rot_dim        */
+    int64_t n_positions;      /* below 2^31                                                    */
+    const int32_t *positions; /* [n_tokens], or NULL                                           */
+    int32_t rot_dim;          /* channels that turn, the first ones: a multiple of 16, at most
+                                 head_dim                                                      */
+    int32_t neighbours;       /* 0: pairs (i, i + rot_dim / 2);  1: pairs (2 i, 2 i + 1)       */
+    tkv_tokens q, q_out;      /* [n_tokens][q_heads][head_dim], fp16 or bf16, one type; q_out
+                                 may be q                                                      */
+    int32_t q_heads;          /* 0: no queries                                                 */
+} tkv_rotation;
+tmap_status tkv_append_rotated(const tkv_cache *cache, const tkv_tokens *k, const tkv_tokens *v,
+                               const tkv_rotation *rotation, const tkv_batch *batch, void *hip_stream);
 
 /*
  * tkv_read -- the reverse: positions lens[b], lens[b] + 1, .. of each
@@ -138,6 +188,9 @@ tmap_status tkv_read(const tkv_cache *cache, const tkv_tokens *k, const tkv_toke
  * K's scales are fp32; a weight, and a V element's scale * (code - 8), are
  * rounded to fp16 once each on their way into the matrix unit.  A row whose
  * logarithms to base 2 all lie below -10^30 counts as one that sees nothing.
+ * In 8 bits K's and V's numbers enter as they are, V's in units of the largest
+ * power of two that a wave has met: what is 2^-31 of it is lost.  Scores are
+ * of caches in 4 bits.
  */
 typedef struct tkv_attend_args {
     tkv_tokens q, out;        /* [n_tokens][q_heads][head_dim], fp16 or bf16, one type  */
@@ -155,6 +208,21 @@ typedef struct tkv_attend_args {
 tmap_status tkv_attend(const tkv_cache *cache, const tkv_attend_args *args, const tkv_batch *batch,
                        void *hip_stream);
 
+/*
+ * tkv_attend_window -- the same where a row whose border is e (it sees positions
+ * below e) sees of these only the last `window`, and those below `sinks`.  Only
+ * their records are read: the pages between may have been given away.  Scores
+ * are not kept.  window == NULL: all positions.
+ */
+typedef struct tkv_window {
+    int32_t window; /* at least 1 */
+    int32_t sinks;  /* at least 0 */
+} tkv_window;
+tmap_status tkv_attend_window(const tkv_cache *cache, const tkv_attend_args *args, const tkv_window *window,
+                              const tkv_batch *batch, void *hip_stream);
+tmap_status tkv_attend_window_workspace(const tkv_cache *cache, const tkv_attend_args *args, const tkv_window *window,
+                                        const tkv_batch *batch, uint64_t *bytes);
+
 /* Workspace that tkv_attend needs for these arguments (pointers are not
  * read; a gfx950 device must be current, as the split of the work goes by
  * its number of compute units).  Smaller sizes may need more, since fewer
@@ -164,7 +232,8 @@ tmap_status tkv_attend_workspace(const tkv_cache *cache, const tkv_attend_args *
 
 /* Enough for these arguments and for every call with no more sequences, new
  * tokens (n_tokens and max_new) and positions (max_len and what the table
- * holds), with scores if these have them: to allocate once. */
+ * holds), with scores if these have them, and with any window: to allocate
+ * once. */
 tmap_status tkv_attend_workspace_bound(const tkv_cache *cache, const tkv_attend_args *args, const tkv_batch *batch,
                                        uint64_t *bytes);
 
@@ -182,7 +251,7 @@ tmap_status tkv_attend_workspace_bound(const tkv_cache *cache, const tkv_attend_
  *   lens_out    int32 [n_seq]: min(lens[b], budget); may be lens, and else
  *               may not overlap it
  * scores_out and scores may not overlap.  batch: table, lens and n_seq are
- * used.
+ * used.  Of caches in 4 bits.
  */
 typedef struct tkv_evict_args {
     const float *scores;

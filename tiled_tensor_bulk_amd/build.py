@@ -4,7 +4,7 @@
 
 Each translation unit is compiled in parallel into tiled_tensor_bulk_amd/_build
 and linked into tiled_tensor_bulk_amd/libtmap.so (the tile copies) or
-libtkv.so (the 4-bit cache and its operators); _tkv.so is libtkv's calls on torch
+libtkv.so (the 4- and 8-bit cache and its operators); _tkv.so is libtkv's calls on torch
 tensors.  Cross-compiles without a GPU.
 """
 from __future__ import annotations
@@ -28,8 +28,9 @@ SOURCES = (["tmap_host.cpp"] + [f"tmap_{m}_r{r}.hip" for m in ("load", "store", 
            + [f"tmap_band_{m}.hip" for m in ("load", "store", "roundtrip")]
            + [f"tmap_corner_{m}.hip" for m in ("load", "store", "roundtrip")]
            + [f"tmap_corner4_{m}.hip" for m in ("load", "store", "roundtrip")] + ["tmap_noalloc.hip"])
-TKV_SOURCES = (["tkv_host.cpp"] + [f"tkv_attend_d{d}.hip" for d in (256, 128, 96, 64)]
-               + ["tkv_combine.hip", "tkv_evict.hip", "tkv_move.hip"])
+TKV_SOURCES = (["tkv_host.cpp"] + [f"tkv_attend_d{d}.hip" for d in (256, 128, 96, 64)] + ["tkv_move.hip"]
+               + [f"tkv_attend8_d{d}.hip" for d in (256, 128, 96, 64)]
+               + ["tkv_move8.hip", "tkv_combine.hip", "tkv_evict.hip"])
 ARCH = "gfx950"
 
 

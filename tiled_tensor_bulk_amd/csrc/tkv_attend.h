@@ -94,10 +94,83 @@ struct Extent {
     __device__ __forceinline__ int limit(const AttendArgs &a, int i) const {
         return a.causal && sees + i < len ? sees + i : len;
     }
+    // the same by the length before it is cut: a window counts from here
+    __device__ __forceinline__ int border(const AttendArgs &a, int i) const { return sees + (a.causal ? i : n - 1); }
 };
 
-// A sequence's chunks: as few as the launch's chunk allows, of equal length up
-// to whole steps of the workgroup.
+// What of a sequence some rows see, and in which order it is gone over.  With a
+// window, rows of the tokens i0 .. i1 see positions below gap_at, the first ones
+// that stay visible, and from gap_at + gap on: places 0, 1, .. below `span` count
+// these.  gap and gap_at are whole records.  Without a window a place is a
+// position.
+template <bool WIN>
+struct View : Extent {
+    __device__ __forceinline__ View(const AttendArgs &a, int seq) : Extent(a, seq) {}
+    __device__ __forceinline__ int span() const { return len; }
+    __device__ __forceinline__ int position(int place) const { return place; }
+    __device__ __forceinline__ int place(int position) const { return position; }
+    __device__ __forceinline__ void narrow_to_block(const AttendArgs &, int) {}
+    __device__ __forceinline__ bool windowed(const AttendArgs &, int, int) const { return false; }
+};
+
+constexpr int kManyRowShift = 6;  // of a workgroup whose waves have rows of their own
+
+template <>
+struct View<true> : Extent {
+    int gap_at, gap, all;
+    __device__ __forceinline__ View(const AttendArgs &a, int seq) : Extent(a, seq) {
+        gap_at = gap = 0;
+        all = len;
+        if (a.window) narrow(a, 0, n - 1);
+    }
+    __device__ __forceinline__ int span() const { return all; }
+    __device__ __forceinline__ void narrow(const AttendArgs &a, int i0, int i1) {
+        const int64_t from = (int64_t)border(a, i0) - a.window;
+        const int low = from > 0 ? (int)from & -kTile : 0, high = limit(a, i1), first = (a.sinks + kTile - 1) & -kTile;
+        gap_at = gap = 0;
+        all = high;
+        if (low > first) {
+            gap_at = first;
+            gap = low - first;
+            all = place(high);
+        }
+    }
+    __device__ __forceinline__ int position(int place) const { return place + (place < gap_at ? 0 : gap); }
+    // of the first position from `position` on that has one
+    __device__ __forceinline__ int place(int position) const {
+        return position < gap_at ? position : position - gap > gap_at ? position - gap : gap_at;
+    }
+    // to the tokens of a block of rows, where a workgroup has many rows: few stay with all of the sequence's tokens
+    __device__ __forceinline__ void narrow_to_block(const AttendArgs &a, int block) {
+        if (!a.window || a.row_shift < kManyRowShift) return;
+        const int first = block << a.row_shift, last = first + (1 << a.row_shift) < rows ? first + (1 << a.row_shift) : rows;
+        narrow(a, divided(first, a.by_group_heads), divided(last - 1, a.by_group_heads));
+    }
+    // whether one of some rows, the last of which is of token i1, does not see a record for its window
+    __device__ __forceinline__ bool windowed(const AttendArgs &a, int i1, int record) const {
+        return a.window && border(a, i1) - record > a.window && record + kTile > a.sinks;
+    }
+};
+
+// What a row sees: positions below its limit, and with a window only the last of
+// those below its border and the first ones.
+template <bool WIN>
+struct Sight {
+    int until;  // the limit, or with a window the border
+    __device__ __forceinline__ void load(const AttendArgs &a, const Extent &e, int row) {
+        const int i = divided(row, a.by_group_heads);
+        until = row >= e.rows ? 0 : WIN ? e.border(a, i) : e.limit(a, i);
+    }
+    // (the difference counts where the border is above the position)
+    __device__ __forceinline__ bool sees(const AttendArgs &a, const Extent &e, int position) const {
+        if (!WIN) return position < until;
+        const bool out = a.window && (int)((uint32_t)until - (uint32_t)position) > a.window && position >= a.sinks;
+        return position < until && position < e.len && !out;
+    }
+};
+
+// The chunks of so many places: as few as the launch's chunk allows, of equal
+// length up to whole steps of the workgroup.
 constexpr int kStep = kTile * kAttendWaves;
 struct Chunks {
     int size, n;
@@ -130,19 +203,24 @@ struct Even {
     static constexpr int kLead = 1;
     int first[kSeqs];  // steps of the sequences before each
     int total, share;
-    static __device__ __forceinline__ int steps(const Extent &e) { return e.len > kStep ? (e.len + kStep - 1) / kStep : 1; }
+    template <bool WIN>
+    static __device__ __forceinline__ int steps(const View<WIN> &e) {
+        return e.span() > kStep ? (e.span() + kStep - 1) / kStep : 1;
+    }
     static __device__ __forceinline__ int blocks(const AttendArgs &a, const Extent &e) {
         return (e.rows + (1 << a.row_shift) - 1) >> a.row_shift;
     }
-    static __device__ __forceinline__ int all(const AttendArgs &a, const Extent &e) {
+    template <bool WIN>
+    static __device__ __forceinline__ int all(const AttendArgs &a, const View<WIN> &e) {
         return (int)a.c.heads * blocks(a, e) * (steps(e) + kLead);
     }
+    template <bool WIN>
     __device__ __forceinline__ void load(const AttendArgs &a, int lane) {
         int sum = 0, most = 0, mine[kSeqs];
 #pragma unroll
         for (int k = 0; k < kSeqs; ++k) {
             const int seq = kSeqs * lane + k;
-            const Extent e(a, seq < a.b.n_seq ? seq : a.b.n_seq - 1);
+            const View<WIN> e(a, seq < a.b.n_seq ? seq : a.b.n_seq - 1);
             mine[k] = seq < a.b.n_seq ? all(a, e) : 0;
             most = most > steps(e) ? most : steps(e);
         }
@@ -201,6 +279,27 @@ struct Pages {
         return __builtin_amdgcn_readlane(mine, index - base);
     }
 };
+
+// The 8-bit format's: of codes alone.
+template <int D, int NT>
+__device__ __forceinline__ void products8(const char *rec, int lane, const h8 (&q)[NT][D / 32], float (&x)[NT][8]) {
+    using F = Format<D, 0>;
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+        f4 acc[NT];
+#pragma unroll
+        for (int c = 0; c < F::W; ++c) {
+            const h8 key = codes8(*reinterpret_cast<const uint2 *>(rec + codes8_at(half * F::W + c, lane)), 1.0f);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+                acc[nt] = __builtin_amdgcn_mfma_f32_16x16x32_f16(key, q[nt][c], c ? acc[nt] : (f4){0, 0, 0, 0}, 0, 0, 0);
+        }
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) x[nt][4 * half + i] = acc[nt][i];
+    }
+}
 
 // Products of a record's 32 positions with the wave's rows, in fp32:
 // x[nt][4 * half + i] for position 16 half + 4 g + i.  first: -kPlus * qsum, four times.
@@ -303,7 +402,7 @@ struct Row {
     // logarithms to base 2: at least the smallest normal number, as masked
     // products are -inf.
     template <bool BF16>
-    __device__ __forceinline__ void operand(const AttendArgs &a, h8 (&q)[D / 32], float (&qsum)[D / GROUP],
+    __device__ __forceinline__ void operand(const AttendArgs &a, h8 (&q)[D / 32], float (&qsum)[Format<D, GROUP>::NG],
                                             float &factor) const {
         using F = Format<D, GROUP>;
         const uint32_t sign = a.scale_log2 < 0.0f ? 0x80008000u : 0;  // moves into q
@@ -326,14 +425,16 @@ struct Row {
         for (int c = 0; c < F::W; ++c)
 #pragma unroll
             for (int j = 0; j < 8; ++j) q[c][j] = (_Float16)(BF16 ? ldexpf(x[c][j], power) : x[c][j]);
-        const h8 ones = {1, 1, 1, 1, 1, 1, 1, 1};
+        if constexpr (GROUP != 0) {
+            const h8 ones = {1, 1, 1, 1, 1, 1, 1, 1};
 #pragma unroll
-        for (int grp = 0; grp < F::NG; ++grp) {
-            f4 sum = {0, 0, 0, 0};
+            for (int grp = 0; grp < F::NG; ++grp) {
+                f4 sum = {0, 0, 0, 0};
 #pragma unroll
-            for (int c = 0; c < F::KG; ++c)
-                sum = __builtin_amdgcn_mfma_f32_16x16x32_f16(ones, q[grp * F::KG + c], sum, 0, 0, 0);
-            qsum[grp] = sum[0];
+                for (int c = 0; c < F::KG; ++c)
+                    sum = __builtin_amdgcn_mfma_f32_16x16x32_f16(ones, q[grp * F::KG + c], sum, 0, 0, 0);
+                qsum[grp] = sum[0];
+            }
         }
     }
 };
@@ -422,10 +523,16 @@ struct Softmax {
         }
         l += sum;
     }
-    // after the last position: l whole in every lane, o what a division by l makes the output
-    __device__ __forceinline__ void finish(int lane) {
+    // after the last position: l whole in every lane, o what a division by l makes the output.  power: the 8-bit
+    // format's o are in units of it
+    __device__ __forceinline__ void finish(int lane, float power = 1.0f) {
         using F = Format<D, GROUP>;
         l = over_groups_sum(l);
+        if constexpr (GROUP == 0) {
+            const float ratio = z[0] > 0.0f ? l / z[0] * power : power;
+#pragma unroll
+            for (int c = 0; c < D / 16; ++c) o[c] *= ratio;
+        } else {
         float ratio = 1.0f;
         if constexpr (kOnes<D, GROUP>) {
             const float rounded = __shfl(z[(2 * F::NG) & 3], 16 * (2 * F::NG / 4) + (lane & 15));
@@ -438,6 +545,12 @@ struct Softmax {
 #pragma unroll
             for (int c = grp * F::VG; c < (grp + 1) * F::VG; ++c) o[c] = (o[c] + zero) * ratio;
         }
+        }
+    }
+    // o in units of a power of two of its own
+    __device__ __forceinline__ void rescale(float f) {
+#pragma unroll
+        for (int c = 0; c < D / 16; ++c) o[c] *= f;
     }
 };
 
@@ -453,7 +566,7 @@ __device__ __forceinline__ void place(const AttendArgs &a, int &block, int &spli
 // has a ring of two records in LDS, which its loads fill without passing
 // through registers: while it works on one, the other is on its way, and the
 // registers leave room for four waves on a SIMD.
-template <int D, int GROUP, int NT>
+template <int D, int GROUP, int NT, bool WIN>
 struct FewRows {
     using F = Format<D, GROUP>;
     static constexpr int kLoads = (F::REC + 1023) / 1024;  // of a record
@@ -464,31 +577,61 @@ struct FewRows {
     static constexpr int kRounds = 2 * F::W * NT * 1024 <= kJoinM ? 1 : 2;
     static constexpr int CH = 2 * F::W / kRounds;
     static_assert(CH * kRounds == 2 * F::W && CH * NT * 1024 <= kJoinM, "rounds cover the channels, and fit");
-    static constexpr int kRegs = NT * (12 * F::W + 4 * F::NG + 20) + 8 * F::NG + 2 * F::W + 28;
+    static constexpr int kRegs = NT * (12 * F::W + 4 * F::NG + 20) + (GROUP ? 8 * F::NG + 2 * F::W : 4 * F::W) + 28 +
+                                 (WIN ? 24 : 0);
     static constexpr int kWaves = kRegs <= 128 ? 4 : kRegs <= 168 ? 3 : kRegs <= 256 ? 2 : 1;
     static constexpr int kFit = 163840 / (kAttendWaves * kRing);
     static constexpr int kResident = kFit < kWaves ? kFit : kWaves;  // workgroups of a compute unit
     static_assert(kResident >= 1 && kResident <= kMostResident, "the workspace has room for no more parts");
 };
 
-// Rows block * R .. of one (sequence, head) at positions t0 .. t1 - 1.  part:
+// The 8-bit format's sums of weights times values, and of weights.  power: of
+// the values in the units of the sums.  live: positions of the record that the
+// sequence has; what lies past its end may be anything.
+template <int D, int NT>
+__device__ __forceinline__ void values8(const char *rec, int lane, float power, int live, const h8 (&p)[NT][1],
+                                        Softmax<D, 0> (&s)[NT]) {
+    using F = Format<D, 0>;
+    const h8 ones = {1, 1, 1, 1, 1, 1, 1, 1};
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) s[nt].z = __builtin_amdgcn_mfma_f32_16x16x32_f16(ones, p[nt][0], s[nt].z, 0, 0, 0);
+    const auto add = [&](uint2 mask, bool whole) {
+#pragma unroll
+        for (int c = 0; c < 2 * F::W; ++c) {
+            uint2 w = *reinterpret_cast<const uint2 *>(rec + F::VC + codes8_at(c, lane));
+            if (!whole) w.x &= mask.x, w.y &= mask.y;
+            const h8 value = codes8(w, power);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+                s[nt].o[c] = __builtin_amdgcn_mfma_f32_16x16x32_f16(value, p[nt][0], s[nt].o[c], 0, 0, 0);
+        }
+    };
+    if (live >= kTile)
+        add(make_uint2(0, 0), true);
+    else
+        add(live_codes(live, lane), false);
+}
+
+// Rows block * R .. of one (sequence, head) at places t0 .. t1 - 1.  part:
 // where the partial sums go, or -1 where these are all of the rows' positions.
-template <int D, int GROUP, int NT, bool BF16, bool EVEN>
-__device__ __forceinline__ void attend_piece(const AttendArgs &a, char *ring, int wave, int tid, const Extent &e, int seq,
+template <int D, int GROUP, int NT, bool BF16, bool EVEN, bool WIN>
+__device__ __forceinline__ void attend_piece(const AttendArgs &a, char *ring, int wave, int tid, const View<WIN> &e, int seq,
                                              int head, int block, int t0, int t1, int64_t part) {
     using F = Format<D, GROUP>;
-    using K = FewRows<D, GROUP, NT>;
+    using K = FewRows<D, GROUP, NT, WIN>;
     constexpr int R = 16 * NT;
+    constexpr bool k8 = GROUP == 0;
     const int lane = tid & 63, g = lane >> 4, n = lane & 15;
     const int shift = a.c.page_shift;
     const int32_t *table = a.b.table + seq * a.b.table_stride;
     const int r0 = block * R;
     Pages pages;
-    pages.load(a, table, t0 >> shift, lane);
+    pages.load(a, table, e.position(t0) >> shift, lane);
 
     const int rows_here = e.rows - r0 < R ? e.rows - r0 : R;
-    const int all_see = e.limit(a, divided(r0, a.by_group_heads));                  // below this no row is masked
-    int end = e.limit(a, divided(r0 + rows_here - 1, a.by_group_heads));            // at this and above every row is
+    const int i1 = divided(r0 + rows_here - 1, a.by_group_heads);
+    const int all_see = e.limit(a, divided(r0, a.by_group_heads));  // below this no row is masked, but for a window
+    int end = e.place(e.limit(a, i1));                              // at this and above every row is
     end = end < t1 ? end : t1;
 
     Row<D, GROUP> raw[NT];
@@ -500,7 +643,8 @@ __device__ __forceinline__ void attend_piece(const AttendArgs &a, char *ring, in
     char *const mine = ring + wave * K::kRing;
     const uint32_t mine_at = lds_address(mine);
     int missing = 0;  // bit s: the record in slot s has no page
-    const auto fetch = [&](int pos, int slot) {
+    const auto fetch = [&](int place, int slot) {
+        const int pos = e.position(place);
         const int page = pages.get(a, table, pos >> shift, lane);
         const char *rec = record_at(a.c, page < 0 ? 0 : page, head, pos / kTile);
         missing = (missing & ~(1 << slot)) | ((page < 0 ? 1 : 0) << slot);
@@ -514,24 +658,27 @@ __device__ __forceinline__ void attend_piece(const AttendArgs &a, char *ring, in
     h8 q[NT][F::W];
     float qsum[NT][F::NG], factor[NT];
     f4 first[NT][F::NG];
-    int limit[NT];
+    Sight<WIN> sight[NT];
     Softmax<D, GROUP> s[NT];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-        const int r = r0 + 16 * nt + n;
-        limit[nt] = r < e.rows ? e.limit(a, divided(r, a.by_group_heads)) : 0;
+        sight[nt].load(a, e, r0 + 16 * nt + n);
         raw[nt].template operand<BF16>(a, q[nt], qsum[nt], factor[nt]);
+        if constexpr (!k8) {
 #pragma unroll
-        for (int grp = 0; grp < F::NG; ++grp) {
-            const float f = -kPlus * qsum[nt][grp];
-            first[nt][grp] = (f4){f, f, f, f};
+            for (int grp = 0; grp < F::NG; ++grp) {
+                const float f = -kPlus * qsum[nt][grp];
+                first[nt][grp] = (f4){f, f, f, f};
+            }
         }
         s[nt].clear();
-        if (a.row_info && t0 == 0 && wave == 0 && r0 / 16 + nt < a.row_tiles)
-            keep_rows<D, GROUP>(a, ((int64_t)seq * a.c.heads + head) * a.row_tiles + r0 / 16 + nt, lane, q[nt],
-                                sum_parts<D, GROUP>(qsum[nt], g), sums_factor(factor[nt]));
+        if constexpr (!k8)
+            if (a.row_info && t0 == 0 && wave == 0 && r0 / 16 + nt < a.row_tiles)
+                keep_rows<D, GROUP>(a, ((int64_t)seq * a.c.heads + head) * a.row_tiles + r0 / 16 + nt, lane, q[nt],
+                                    sum_parts<D, GROUP>(qsum[nt], g), sums_factor(factor[nt]));
     }
 
+    int units = 0;  // of o: 2^(units - 127)
     for (int slot = 0; p0 < end; p0 += kStep, slot ^= 1) {
         static_assert(K::kDepth == 2, "slots alternate");
         if (p0 + kStep < end)
@@ -540,19 +687,37 @@ __device__ __forceinline__ void attend_piece(const AttendArgs &a, char *ring, in
             wait_loads<0>();
         const char *rec = mine + slot * K::kSlot;
         const bool gone = (missing >> slot) & 1;
-        float x[NT][8];
-        products<D, GROUP, NT>(rec, lane, q, qsum, first, x);
-        const bool masked = p0 + kTile > all_see || gone;  // some position is not seen by some row
+        const int at = e.position(p0);
+        float x[NT][8], scaled[NT];
+        const float(&f)[NT] = k8 ? scaled : factor;
+        int power = 0;  // E of the values
+        if constexpr (k8) {
+            const uint32_t ex = (uint32_t)__builtin_amdgcn_readfirstlane(*reinterpret_cast<const int *>(rec + F::EX));
+            products8<D, NT>(rec, lane, q, x);
+            power = (ex >> 8) & 255;
+            const float of_keys = power_of(ex & 255);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) scaled[nt] = fminf(fmaxf(factor[nt] * of_keys, 0x1p-126f), 0x1.fffffep127f);
+            if (power > units) {
+                const float shrunk = units ? __builtin_amdgcn_ldexpf(1.0f, units - power) : 1.0f;
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) s[nt].rescale(shrunk);
+                units = power;
+            }
+        } else {
+            products<D, GROUP, NT>(rec, lane, q, qsum, first, x);
+        }
+        const bool masked = at + kTile > all_see || gone || e.windowed(a, i1, at);  // some position is not seen by some row
         if (masked) {
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-                const int pos = p0 + 16 * (j >> 2) + 4 * g + (j & 3);
+                const int pos = at + 16 * (j >> 2) + 4 * g + (j & 3);
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
-                    if (pos >= limit[nt] || gone) x[nt][j] = -__builtin_inff();
+                    if (!sight[nt].sees(a, e, pos) || gone) x[nt][j] = -__builtin_inff();
             }
         }
-        if (NT == 1 && a.logits && n < a.rows) {
+        if (!k8 && NT == 1 && a.logits && n < a.rows) {
             float *to = a.logits + (((int64_t)(seq * (int)a.c.heads + head) * ((a.max_len + kTile - 1) / kTile) + p0 / kTile) *
                                         a.rows + n) * kTile + 4 * g;
 #pragma unroll
@@ -564,7 +729,7 @@ __device__ __forceinline__ void attend_piece(const AttendArgs &a, char *ring, in
         float top[NT];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-            top[nt] = Softmax<D, GROUP>::top(x[nt]) * factor[nt];
+            top[nt] = Softmax<D, GROUP>::top(x[nt]) * f[nt];
             grown |= top[nt] > s[nt].m + kSlack;
         }
         if (__any(grown)) {
@@ -573,7 +738,10 @@ __device__ __forceinline__ void attend_piece(const AttendArgs &a, char *ring, in
         }
         h8 p[NT][1];
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) s[nt].weights(x[nt], factor[nt], p[nt]);
+        for (int nt = 0; nt < NT; ++nt) s[nt].weights(x[nt], f[nt], p[nt]);
+        if constexpr (k8) {
+            values8<D, NT>(rec, lane, power_of(power - units + 127), masked ? e.len - at : kTile, p, s);
+        } else {
         h8 scale[F::NG];  // of the lane's 8 positions
 #pragma unroll
         for (int grp = 0; grp < F::NG; ++grp)
@@ -583,7 +751,7 @@ __device__ __forceinline__ void attend_piece(const AttendArgs &a, char *ring, in
         if (masked) {  // what lies past the sequence's end may be anything
 #pragma unroll
             for (int j = 0; j < 8; ++j)
-                if (p0 + 16 * (j >> 2) + 4 * g + (j & 3) >= e.len) {
+                if (at + 16 * (j >> 2) + 4 * g + (j & 3) >= e.len) {
 #pragma unroll
                     for (int grp = 0; grp < F::NG; ++grp) scale[grp][j] = (_Float16)0.0f;
                     row[j] = (_Float16)0.0f;
@@ -605,6 +773,7 @@ __device__ __forceinline__ void attend_piece(const AttendArgs &a, char *ring, in
                     s[nt].o[c] = __builtin_amdgcn_mfma_f32_16x16x32_f16(value, p[nt][0], s[nt].o[c], 0, 0, 0);
             }
         }
+        }
         if (p0 + K::kDepth * kStep < end) {
             wait_lds();  // the slot has been read
             fetch(p0 + K::kDepth * kStep, slot);
@@ -619,7 +788,7 @@ __device__ __forceinline__ void attend_piece(const AttendArgs &a, char *ring, in
     const auto o_of = [&](int w, int item) -> f4 & { return reinterpret_cast<f4 *>(ring + w * K::kRing)[item]; };
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-        s[nt].finish(lane);
+        s[nt].finish(lane, k8 ? power_of(units) : 1.0f);
         if (g == 0) m_of(wave, 16 * nt + n) = s[nt].m, l_of(wave, 16 * nt + n) = s[nt].l;
     }
     const int part_rows = EVEN && a.rows > R ? R : a.rows;
@@ -658,16 +827,16 @@ __device__ __forceinline__ void attend_piece(const AttendArgs &a, char *ring, in
     }
 }
 
-template <int D, int GROUP, int NT, bool BF16, bool EVEN>
-__global__ void __launch_bounds__(64 * kAttendWaves, (FewRows<D, GROUP, NT>::kWaves)) attend_kernel(const AttendArgs a) {
-    __shared__ __attribute__((aligned(1024))) char ring[kAttendWaves * FewRows<D, GROUP, NT>::kRing];
+template <int D, int GROUP, int NT, bool BF16, bool EVEN, bool WIN>
+__global__ void __launch_bounds__(64 * kAttendWaves, (FewRows<D, GROUP, NT, WIN>::kWaves)) attend_kernel(const AttendArgs a) {
+    __shared__ __attribute__((aligned(1024))) char ring[kAttendWaves * FewRows<D, GROUP, NT, WIN>::kRing];
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     if constexpr (EVEN) {
         int seq, at, left;  // a step of the sequence's line, and how many are to do
         {
             const int lane = threadIdx.x & 63;
             Even even;
-            even.load(a, lane);
+            even.load<WIN>(a, lane);
             if (blockIdx.x == 0 && wave == 0) even.store(a, lane);
             at = (int)blockIdx.x * even.share;
             left = even.total - at < even.share ? even.total - at : even.share;
@@ -678,7 +847,7 @@ __global__ void __launch_bounds__(64 * kAttendWaves, (FewRows<D, GROUP, NT>::kWa
         for (;;) {
             int tid = threadIdx.x;
             asm volatile("" : "+v"(tid));  // or what comes of it would be kept from one piece for the next
-            const Extent e(a, seq);
+            const View<WIN> e(a, seq);
             const int steps = Even::steps(e), line = steps + Even::kLead, blocks = Even::blocks(a, e);
             const int unit = (int)((uint32_t)at / (uint32_t)line);
             int from = at - unit * line, to = from + left < line ? from + left : line;
@@ -689,19 +858,19 @@ __global__ void __launch_bounds__(64 * kAttendWaves, (FewRows<D, GROUP, NT>::kWa
             if (to <= from) break;  // no more than a row block's lead was left
             const int head = (int)((uint32_t)unit / (uint32_t)blocks), block = unit - head * blocks;
             const int64_t part = ((int64_t)seq * a.c.heads + head) * a.row_blocks + block + blockIdx.x;
-            attend_piece<D, GROUP, NT, BF16, EVEN>(a, ring, wave, tid, e, seq, head, block, from * kStep, to * kStep,
+            attend_piece<D, GROUP, NT, BF16, EVEN, WIN>(a, ring, wave, tid, e, seq, head, block, from * kStep, to * kStep,
                                                    to - from < steps ? part : -1);
             if (left <= 0) break;
-            for (int all = Even::all(a, e); at >= all; all = Even::all(a, Extent(a, seq))) at -= all, ++seq;
+            for (int all = Even::all(a, e); at >= all; all = Even::all(a, View<WIN>(a, seq))) at -= all, ++seq;
             __syncthreads();  // the ring is read no longer
         }
     } else {
         int block, split, head, seq;
         place(a, block, split, head, seq);
-        const Extent e(a, seq);
-        const Chunks chunks(a, e.len);
+        const View<WIN> e(a, seq);
+        const Chunks chunks(a, e.span());
         if (block * 16 * NT >= e.rows || split >= chunks.n) return;
-        attend_piece<D, GROUP, NT, BF16, EVEN>(
+        attend_piece<D, GROUP, NT, BF16, EVEN, WIN>(
             a, ring, wave, threadIdx.x, e, seq, head, block, split * chunks.size, (split + 1) * chunks.size,
             a.n_split > 1 ? ((int64_t)seq * a.c.heads + head) * a.n_split + split : -1);
     }

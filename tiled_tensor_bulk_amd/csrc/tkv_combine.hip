@@ -20,7 +20,11 @@ constexpr int kCombineThreads = kBlockThreads;
 struct Parts {
     int n, stride;  // n 0: the row has been written where it was computed
     int64_t first;
-    __device__ __forceinline__ Parts(const AttendArgs &a, const Extent &e, int unit, int seq, int head, int row) {
+    static __device__ __forceinline__ int chunks(const AttendArgs &a, View<true> e, int row) {
+        e.narrow_to_block(a, row >> a.row_shift);
+        return Chunks(a, e.span()).n;
+    }
+    __device__ __forceinline__ Parts(const AttendArgs &a, const View<true> &e, int unit, int seq, int head, int row) {
         if (a.even) {
             const int rows = 1 << a.row_shift, steps = Even::steps(e), block = row >> a.row_shift;
             const uint32_t share = (uint32_t)a.dealt[kEvenSeqs];
@@ -32,7 +36,7 @@ struct Parts {
             stride = a.rows < rows ? a.rows : rows;
             first = ((int64_t)unit * a.row_blocks + block + part) * stride + (row & (rows - 1));
         } else {
-            n = Chunks(a, e.len).n;
+            n = chunks(a, e, row);
             stride = a.rows;
             first = (int64_t)unit * a.n_split * a.rows + row;
         }
@@ -48,7 +52,7 @@ __device__ __forceinline__ void combine_few(const AttendArgs &a, int workgroup) 
     int head = unit;
     const int seq = divide(head, (int)a.c.heads, a.by_heads);
     if (which >= AT_ONCE || seq >= a.b.n_seq) return;
-    const Extent e(a, seq);
+    const View<true> e(a, seq);
     if (row >= e.rows) return;
     const Parts parts(a, e, unit, seq, head, row);
     if (parts.n == 0) return;
@@ -95,9 +99,9 @@ __global__ void __launch_bounds__(kCombineThreads) combine_kernel(const AttendAr
     const int unit = divide(row, a.rows, a.by_rows);
     int head = unit;
     const int seq = divide(head, (int)a.c.heads, a.by_heads);
-    const Extent e(a, seq);
+    const View<true> e(a, seq);
     if (row >= e.rows) return;
-    const int parts = Chunks(a, e.len).n;
+    const int parts = Parts::chunks(a, e, row);
     const int64_t first = ((int64_t)unit * a.n_split) * a.rows + row;
     float best = kFar, sum = 0.0f;
     f4 y = (f4){0, 0, 0, 0};
@@ -138,7 +142,7 @@ __device__ __forceinline__ void weigh(const AttendArgs &a, int workgroup, int bl
     const int unit = workgroup / blocks, block = workgroup % blocks;
     int head = unit;
     const int seq = divide(head, (int)a.c.heads, a.by_heads);
-    const Extent e(a, seq);
+    const View<true> e(a, seq);
     if (block * kWeighPositions >= e.len) return;
     const int pos = block * kWeighPositions + (int)threadIdx.x * 4;
     const int64_t records = (a.max_len + kTile - 1) / kTile;

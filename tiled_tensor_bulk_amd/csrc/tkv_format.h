@@ -26,6 +26,16 @@ struct Format {
     static constexpr int REC = 32 * D + 256 * NG;
 };
 
+// The 8-bit format: words of a lane come in pairs, 8 codes each.
+template <int D>
+struct Format<D, 0> {
+    static constexpr int W = D / 32;            // pairs of a lane in half a record's K (or V) codes
+    static constexpr int NG = 1;                // one scale
+    static constexpr int VC = 32 * D;           // byte offsets in a record
+    static constexpr int EX = 64 * D;           // E of the keys, E of the values
+    static constexpr int REC = 64 * D + 128;
+};
+
 // N consecutive words (2, 3 or 4), 4-byte aligned at least.
 template <int N>
 struct __attribute__((packed, aligned(4))) Words {
@@ -95,6 +105,30 @@ __device__ __forceinline__ h8 codes_plus(uint32_t w) {
     return __builtin_bit_cast(h8, (u4){((w << 4) & mask) | magic, (w & mask) | magic, ((w >> 4) & mask) | magic,
                                        ((w >> 8) & mask) | magic});
 }
+
+// 8 codes of the 8-bit format times a power of two as fp16: exactly, but for
+// what becomes subnormal.
+__device__ __forceinline__ h8 codes8(uint2 w, float power) {
+    const h2 a = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w.x, power, false);
+    const h2 b = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w.x, power, true);
+    const h2 c = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w.y, power, false);
+    const h2 d = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w.y, power, true);
+    return (h8){a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
+}
+
+// 2^(e - 127), and 0 for e of 0 or less.
+__device__ __forceinline__ float power_of(int e) { return __builtin_bit_cast(float, (e > 0 ? e : 0) << 23); }
+
+// Bytes of a lane's 8 V codes whose positions are below `live`: 4 g .. 4 g + 3 in
+// the first word, and 16 more in the second.
+__device__ __forceinline__ uint32_t first_bytes(int n) { return n >= 4 ? ~0u : n <= 0 ? 0u : (1u << (8 * n)) - 1; }
+__device__ __forceinline__ uint2 live_codes(int live, int lane) {
+    const int n = live - 4 * (lane >> 4);
+    return make_uint2(first_bytes(n), first_bytes(n - 16));
+}
+
+// Where 8 codes of a lane are (tkv.h): bytes from the record's beginning.
+__device__ __forceinline__ int codes8_at(int pair, int lane) { return (pair * 64 + lane) * 8; }
 
 // The nibble of code j in its word.
 __device__ __forceinline__ constexpr int nibble_of(int j) { return (j >> 1) + 4 * (j & 1); }

@@ -230,11 +230,28 @@ constexpr int kLongForOne = 1 << 14;
 constexpr int kBlocksPerCu = 8;
 constexpr int kRowBlocksPerCu = 2;
 
-Split plan(const Cache &c, int64_t n_seq, int64_t rows, int64_t max_len, bool scores, int cus) {
+//
+// With a window the same of what a block of rows may see of a sequence.
+int64_t seen_at_most(const tkv::AttendArgs &a, int row_tile) {
+    if (!a.window) return a.max_len;
+    int64_t tokens = a.b.max_new;
+    if (row_tile > 32) {
+        const int64_t block = (row_tile + 2 * (int64_t)a.group_heads - 2) / a.group_heads;
+        tokens = block < tokens ? block : tokens;
+    }
+    const int64_t n = (int64_t)a.sinks + a.window + tokens + 2 * tkv::kTile;  // both ends in whole records
+    return n < a.max_len ? n : a.max_len;
+}
+
+Split plan(const tkv::AttendArgs &a, int cus) {
+    const Cache &c = a.c;
+    const int64_t n_seq = a.b.n_seq, rows = a.rows;
+    const bool scores = a.scores_out;
     Split s{};
     s.row_tile = rows <= 16 || (c.dim > 128 && rows <= 48) ? 16 : rows <= 32 ? 32 : rows <= 64 || c.dim > 128 ? 64 : 128;
     s.row_blocks = (int)((rows + s.row_tile - 1) / s.row_tile);
     s.row_tiles = (int)((rows + 15) / 16);
+    const int64_t max_len = seen_at_most(a, s.row_tile);
     const int64_t units = n_seq * c.heads * s.row_blocks;
     s.chunk = kLeastChunk;
     const int64_t most = (int64_t)cus * (s.row_tile <= 32 ? kBlocksPerCu : kRowBlocksPerCu);
@@ -298,8 +315,8 @@ uint64_t most_workspace(const Cache &c, int64_t n_seq, int64_t rows, int64_t max
     return total;
 }
 
-tmap_status attend_args(const tkv_cache *cache, const tkv_attend_args *in, const tkv_batch *batch, bool pointers,
-                        tkv::AttendArgs &a) {
+tmap_status attend_args(const tkv_cache *cache, const tkv_attend_args *in, const tkv_window *window,
+                        const tkv_batch *batch, bool pointers, tkv::AttendArgs &a) {
     TKV_REQUIRE(decode(cache, a.c), "cache was never encoded");
     TKV_REQUIRE(in, "args is NULL");
     TKV_TRY(check_batch(a.c, batch, a.b, true));
@@ -316,8 +333,16 @@ tmap_status attend_args(const tkv_cache *cache, const tkv_attend_args *in, const
     if (in->scores_out) {
         TKV_REQUIRE(aligned(in->scores_out, 4) && aligned(in->scores_in, 4), "scores are not 4-byte aligned");
         TKV_REQUIRE(in->score_stride >= in->max_len, "score_stride is less than max_len");
+        TKV_REQUIRE(a.c.group, "scores are kept of a cache in 4 bits, and this one has 8");
+        TKV_REQUIRE(!window, "scores are not kept with a window");
     } else {
         TKV_REQUIRE(!in->scores_in, "scores_in without scores_out");
+    }
+    if (window) {
+        TKV_REQUIRE(window->window >= 1, "window is less than 1");
+        TKV_REQUIRE(window->sinks >= 0, "sinks is negative");
+        a.window = window->window;
+        a.sinks = window->sinks < kMostPositions ? window->sinks : (int32_t)kMostPositions;
     }
     a.lse = in->lse;
     a.scale_log2 = in->scale * 1.44269504089f;
@@ -338,12 +363,8 @@ tmap_status attend_args(const tkv_cache *cache, const tkv_attend_args *in, const
     return TMAP_SUCCESS;
 }
 
-}  // namespace
-
-extern "C" {
-
-tmap_status tkv_encode(tkv_cache *cache, void *pool, int64_t n_pages, uint32_t n_heads, uint32_t head_dim,
-                       uint32_t page_tokens, uint32_t group) {
+tmap_status check_pool(const tkv_cache *cache, const void *pool, int64_t n_pages, uint32_t n_heads, uint32_t head_dim,
+                       uint32_t page_tokens) {
     TKV_REQUIRE(cache, "cache is NULL");
     TKV_REQUIRE(pool && aligned(pool, 16), "pool is NULL or not 16-byte aligned");
     TKV_REQUIRE(n_pages >= 1 && n_pages < 0x7FFFFFFF, "n_pages must be in [1, 2^31 - 1)");
@@ -352,8 +373,11 @@ tmap_status tkv_encode(tkv_cache *cache, void *pool, int64_t n_pages, uint32_t n
                 "head_dim must be 64, 96, 128 or 256");
     TKV_REQUIRE(page_tokens >= 32 && page_tokens <= 1024 && (page_tokens & (page_tokens - 1)) == 0,
                 "page_tokens must be a power of two in [32, 1024]");
-    TKV_REQUIRE((group == 32 || group == 64 || group == 128) && head_dim % group == 0,
-                "group must be 32, 64 or 128 and divide head_dim");
+    return TMAP_SUCCESS;
+}
+
+void describe(tkv_cache *cache, void *pool, int64_t n_pages, uint32_t n_heads, uint32_t head_dim, uint32_t page_tokens,
+              uint32_t group, uint32_t record) {
     Cache c{};
     c.pool = (uint64_t)(uintptr_t)pool;
     c.n_pages = (uint32_t)n_pages;
@@ -361,11 +385,74 @@ tmap_status tkv_encode(tkv_cache *cache, void *pool, int64_t n_pages, uint32_t n
     c.dim = head_dim;
     c.group = group;
     while ((1u << c.page_shift) < page_tokens) ++c.page_shift;
-    c.record = 32 * head_dim + 256 * (head_dim / group);
+    c.record = record;
     c.head_bytes = c.record * (page_tokens / tkv::kTile);
     c.page_bytes = (uint64_t)c.head_bytes * n_heads;
     c.magic = tkv::kMagic;
     std::memcpy(cache, &c, sizeof c);
+}
+
+tmap_status rotation_args(const tkv_rotation *in, tkv::MoveArgs &a) {
+    TKV_REQUIRE(in, "rotation is NULL");
+    const bool empty = a.b.n_tokens == 0;
+    tkv::Rotation &r = a.rot;
+    TKV_REQUIRE(in->rot_dim >= 16 && in->rot_dim % 16 == 0 && (uint32_t)in->rot_dim <= a.c.dim,
+                "rot_dim must be a multiple of 16 and at most head_dim");
+    TKV_REQUIRE(in->neighbours == 0 || in->neighbours == 1, "neighbours must be 0 or 1");
+    TKV_REQUIRE(in->n_positions >= 0 && in->n_positions <= 0x7FFFFFFF, "n_positions must be in [0, 2^31)");
+    TKV_REQUIRE(in->stride >= in->rot_dim, "the table's stride is less than rot_dim");
+    TKV_REQUIRE(empty || in->n_positions == 0 || (in->cos_sin && aligned(in->cos_sin, 4)),
+                "cos_sin is NULL or not 4-byte aligned");
+    TKV_REQUIRE(aligned(in->positions, 4), "positions is not 4-byte aligned");
+    TKV_REQUIRE(in->q_heads >= 0, "q_heads is negative");
+    r.table = in->cos_sin;
+    r.stride = in->stride;
+    r.positions = in->positions;
+    r.n_positions = (int32_t)in->n_positions;
+    r.dim = in->rot_dim;
+    r.neighbours = in->neighbours;
+    r.wide = aligned(in->cos_sin, 16) && in->stride % 4 == 0 && in->rot_dim % 8 == 0;
+    r.q_heads = in->q_heads;
+    if (!r.q_heads) return TMAP_SUCCESS;
+    TKV_TRY(check_tokens(in->q, "q", false, empty, r.q));
+    TKV_TRY(check_tokens(in->q_out, "q_out", false, empty, r.q_out));
+    TKV_REQUIRE(in->q.dtype == in->q_out.dtype, "q and q_out must have one type");
+    TKV_TRY(check_written(in->q_out, "q_out", a.b.n_tokens, in->q_heads, a.c.dim));
+    r.same = in->q.data == in->q_out.data && in->q.token_stride == in->q_out.token_stride &&
+             in->q.head_stride == in->q_out.head_stride;
+    TKV_REQUIRE(r.same || in->q.data != in->q_out.data || empty, "q_out is q with other strides");
+    // a wave for each token
+    const int64_t blocks = over((int64_t)a.b.n_seq * a.b.max_new, tkv::kBlockThreads / 64);
+    const int64_t records = a.b.max_new <= tkv::kFewTokens ? over((int64_t)a.tiles * a.b.n_seq * a.c.heads, 2) : 0;
+    TKV_REQUIRE(launchable(a.b.n_seq, a.b.max_new) && fits(blocks + records), "too many sequences and new tokens");
+    return TMAP_SUCCESS;
+}
+
+tmap_status append(tkv::MoveArgs &a, void *hip_stream) {
+    int cus = 0;
+    TKV_TRY(device(cus));
+    if (a.tiles == 0 || a.b.n_seq == 0) return ok();
+    return launched(tkv::launch_append(a, hip_stream));
+}
+
+}  // namespace
+
+extern "C" {
+
+tmap_status tkv_encode(tkv_cache *cache, void *pool, int64_t n_pages, uint32_t n_heads, uint32_t head_dim,
+                       uint32_t page_tokens, uint32_t group) {
+    TKV_TRY(check_pool(cache, pool, n_pages, n_heads, head_dim, page_tokens));
+    TKV_REQUIRE((group == 32 || group == 64 || group == 128) && head_dim % group == 0,
+                "group must be 32, 64 or 128 and divide head_dim");
+    describe(cache, pool, n_pages, n_heads, head_dim, page_tokens, group,
+             32 * head_dim + 256 * (head_dim / group));
+    return ok();
+}
+
+tmap_status tkv_encode8(tkv_cache *cache, void *pool, int64_t n_pages, uint32_t n_heads, uint32_t head_dim,
+                        uint32_t page_tokens) {
+    TKV_TRY(check_pool(cache, pool, n_pages, n_heads, head_dim, page_tokens));
+    describe(cache, pool, n_pages, n_heads, head_dim, page_tokens, 0, 64 * head_dim + 128);
     return ok();
 }
 
@@ -378,10 +465,15 @@ tmap_status tkv_append(const tkv_cache *cache, const tkv_tokens *k, const tkv_to
                        void *hip_stream) {
     tkv::MoveArgs a{};
     TKV_TRY(move_args(cache, k, v, batch, true, a));
-    int cus = 0;
-    TKV_TRY(device(cus));
-    if (a.tiles == 0 || a.b.n_seq == 0) return ok();
-    return launched(tkv::launch_append(a, hip_stream));
+    return append(a, hip_stream);
+}
+
+tmap_status tkv_append_rotated(const tkv_cache *cache, const tkv_tokens *k, const tkv_tokens *v,
+                               const tkv_rotation *rotation, const tkv_batch *batch, void *hip_stream) {
+    tkv::MoveArgs a{};
+    TKV_TRY(move_args(cache, k, v, batch, true, a));
+    TKV_TRY(rotation_args(rotation, a));
+    return append(a, hip_stream);
 }
 
 tmap_status tkv_read(const tkv_cache *cache, const tkv_tokens *k, const tkv_tokens *v, const tkv_batch *batch,
@@ -394,22 +486,27 @@ tmap_status tkv_read(const tkv_cache *cache, const tkv_tokens *k, const tkv_toke
     return launched(tkv::launch_read(a, hip_stream));
 }
 
-tmap_status tkv_attend_workspace(const tkv_cache *cache, const tkv_attend_args *args, const tkv_batch *batch,
-                                 uint64_t *bytes) {
+tmap_status tkv_attend_window_workspace(const tkv_cache *cache, const tkv_attend_args *args, const tkv_window *window,
+                                        const tkv_batch *batch, uint64_t *bytes) {
     tkv::AttendArgs a{};
     TKV_REQUIRE(bytes, "bytes is NULL");
-    TKV_TRY(attend_args(cache, args, batch, false, a));
+    TKV_TRY(attend_args(cache, args, window, batch, false, a));
     int cus = 0;
     TKV_TRY(device(cus));
-    *bytes = a.rows > 0 && a.b.n_seq > 0 ? plan(a.c, a.b.n_seq, a.rows, a.max_len, a.scores_out, cus).total : 0;
+    *bytes = a.rows > 0 && a.b.n_seq > 0 ? plan(a, cus).total : 0;
     return ok();
+}
+
+tmap_status tkv_attend_workspace(const tkv_cache *cache, const tkv_attend_args *args, const tkv_batch *batch,
+                                 uint64_t *bytes) {
+    return tkv_attend_window_workspace(cache, args, nullptr, batch, bytes);
 }
 
 tmap_status tkv_attend_workspace_bound(const tkv_cache *cache, const tkv_attend_args *args, const tkv_batch *batch,
                                        uint64_t *bytes) {
     tkv::AttendArgs a{};
     TKV_REQUIRE(bytes, "bytes is NULL");
-    TKV_TRY(attend_args(cache, args, batch, false, a));
+    TKV_TRY(attend_args(cache, args, nullptr, batch, false, a));
     int cus = 0;
     TKV_TRY(device(cus));
     *bytes = a.rows > 0 && a.b.n_seq > 0 ? most_workspace(a.c, a.b.n_seq, a.rows, a.max_len, a.scores_out, cus) : 0;
@@ -417,8 +514,13 @@ tmap_status tkv_attend_workspace_bound(const tkv_cache *cache, const tkv_attend_
 }
 
 tmap_status tkv_attend(const tkv_cache *cache, const tkv_attend_args *args, const tkv_batch *batch, void *hip_stream) {
+    return tkv_attend_window(cache, args, nullptr, batch, hip_stream);
+}
+
+tmap_status tkv_attend_window(const tkv_cache *cache, const tkv_attend_args *args, const tkv_window *window,
+                              const tkv_batch *batch, void *hip_stream) {
     tkv::AttendArgs a{};
-    TKV_TRY(attend_args(cache, args, batch, true, a));
+    TKV_TRY(attend_args(cache, args, window, batch, true, a));
     int cus = 0;
     TKV_TRY(device(cus));
     if (a.b.n_seq == 0) return ok();
@@ -429,7 +531,7 @@ tmap_status tkv_attend(const tkv_cache *cache, const tkv_attend_args *args, cons
         a.by_heads = divisor(a.c.heads);
         return launched(tkv::launch_weigh(a, hip_stream));
     }
-    const Split s = plan(a.c, a.b.n_seq, a.rows, a.max_len, a.scores_out, cus);
+    const Split s = plan(a, cus);
     // every launch of the call, so that none is refused after another has begun
     const int64_t heads = (int64_t)a.b.n_seq * a.c.heads;
     int64_t joining = 0, weighing = 0;
@@ -481,6 +583,7 @@ tmap_status tkv_evict(const tkv_cache *cache, const tkv_evict_args *args, const 
     tkv::EvictArgs a{};
     TKV_REQUIRE(decode(cache, a.c), "cache was never encoded");
     TKV_REQUIRE(args, "args is NULL");
+    TKV_REQUIRE(a.c.group, "eviction is of a cache in 4 bits, and this one has 8");
     TKV_TRY(check_batch(a.c, batch, a.b, false));
     TKV_REQUIRE(args->budget >= 0 && args->recent >= 0, "budget or recent is negative");
     TKV_REQUIRE(args->max_len >= 0 && args->score_stride >= args->max_len, "score_stride is less than max_len");

@@ -24,6 +24,7 @@ constexpr int kEvenSeqs = 256;            // most sequences of an even split
 // the second, 69 with the first.
 constexpr int kLogitRows = 8;
 constexpr float kLimit = 32000.0f;        // largest magnitude quantised: 15 * scale stays inside fp16
+constexpr int kLeastPower = 27;           // smallest E of the 8-bit format: 2^-100
 
 // The decoded form of tkv_cache.
 struct Cache {
@@ -31,7 +32,7 @@ struct Cache {
     uint64_t page_bytes;
     uint32_t n_pages;
     uint32_t heads;
-    uint32_t dim, group;
+    uint32_t dim, group;   // group 0: the 8-bit format
     uint32_t page_shift;   // log2(page_tokens)
     uint32_t record;       // bytes of 32 positions of one head
     uint32_t head_bytes;   // bytes of one head's positions of a page
@@ -66,11 +67,26 @@ struct Divisor {
     int32_t shift;
 };
 
+struct Rotation {
+    const float *table;
+    int64_t stride;
+    const int32_t *positions;  // nullptr: the tokens' places in their sequences
+    int32_t n_positions;
+    int32_t dim;               // channels turned; 0: none
+    int32_t neighbours;
+    int32_t wide;              // every 4 floats of the table can be read at once
+    Tokens q, q_out;
+    int32_t q_heads;           // 0: no queries
+    int32_t same;              // q_out is q: what is not turned stays
+};
+
 struct MoveArgs {  // append and read
     Cache c;
     Tokens k, v;
     Batch b;
-    int32_t tiles;  // records that a sequence's new tokens can touch
+    int32_t tiles;        // records that a sequence's new tokens can touch
+    int32_t move_blocks;  // workgroups of the first part of a launch; the others take the queries
+    Rotation rot;
 };
 
 struct AttendArgs {
@@ -84,6 +100,7 @@ struct AttendArgs {
     int32_t rows;          // max_new * group_heads
     int32_t row_blocks;
     int32_t max_len;
+    int32_t window, sinks; // window 0: every position below a row's border is seen
     int32_t chunk_shift;   // a workgroup has at most 1 << chunk_shift positions
     int32_t n_split;
     int32_t even;          // the steps of all sequences are dealt evenly (Even), not in chunks
@@ -118,15 +135,22 @@ struct EvictArgs {
     int32_t dst_width, budget, recent, max_len;
 };
 
-// Launchers, one translation unit each; they return a hipError_t as int.
+// Launchers, one translation unit each; they return a hipError_t as int.  A
+// cache in 8 bits (group 0) goes on to those whose names say so.
 int launch_append(const MoveArgs &a, void *stream);
 int launch_read(const MoveArgs &a, void *stream);
+int launch_append8(const MoveArgs &a, void *stream);
+int launch_read8(const MoveArgs &a, void *stream);
 // row_tile: rows of a workgroup, 16 or 32 (its waves share the positions), 64
 // or 128 (its waves share the rows)
 int launch_attend_d64(const AttendArgs &a, int row_tile, void *stream);
 int launch_attend_d96(const AttendArgs &a, int row_tile, void *stream);
 int launch_attend_d128(const AttendArgs &a, int row_tile, void *stream);
 int launch_attend_d256(const AttendArgs &a, int row_tile, void *stream);
+int launch_attend8_d64(const AttendArgs &a, int row_tile, void *stream);
+int launch_attend8_d96(const AttendArgs &a, int row_tile, void *stream);
+int launch_attend8_d128(const AttendArgs &a, int row_tile, void *stream);
+int launch_attend8_d256(const AttendArgs &a, int row_tile, void *stream);
 int launch_combine(const AttendArgs &a, void *stream);
 int launch_weigh(const AttendArgs &a, void *stream);  // of sequences without rows: the scores as they are
 int launch_evict(const EvictArgs &a, void *stream);

@@ -18,11 +18,9 @@
 // which the instructions alone are 29; read into fp32 42 us for 234 MB, 5.5 TB/s.
 // 4 heads of 256 channels, as many bytes: append 56 us (242 registers, two
 // waves a SIMD), read 49; 8 heads of 96: 33 and 31.
-#include "tkv_format.h"
+#include "tkv_rotate.h"
 
 namespace tkv {
-
-constexpr int kMoveWaves = kBlockThreads / 64;
 
 // Nearest whole numbers to (x - z) / s within 0..15, ties to even.  The
 // quotient in fp32 is within 1e-5 of the true one, so only one that close to a
@@ -90,8 +88,6 @@ __device__ __forceinline__ void quantise(const float *x, _Float16 *scale, _Float
     }
 }
 
-__device__ __forceinline__ float limited(float y) { return y != y ? 0.0f : fminf(fmaxf(y, -kLimit), kLimit); }
-
 // A row's channels 32 i + 8 g .. as they lie.
 template <int D>
 __device__ __forceinline__ void load_row(const Tokens &t, int64_t row, int head, int g, uint4 (&raw)[D / 32]) {
@@ -100,33 +96,47 @@ __device__ __forceinline__ void load_row(const Tokens &t, int64_t row, int head,
     for (int i = 0; i < D / 32; ++i) raw[i] = load8_raw(t, at + 32 * i);
 }
 
-struct Unit {
-    int seq, head, tile;   // record: positions 32 * tile ..
-    int first, n;          // the sequence's first new position and their number
-    int64_t start;         // row of the first
-    char *rec;             // nullptr where the position's page does not exist
-};
-
-__device__ __forceinline__ bool unit_of(const MoveArgs &a, int unit, Unit &u) {
-    u.head = unit % (int)a.c.heads;
-    const int rest = unit / (int)a.c.heads;
-    u.seq = rest / a.tiles;
-    if (u.seq >= a.b.n_seq) return false;
-    new_tokens(a.b, u.seq, u.start, u.n);
-    u.first = a.b.lens[u.seq];
-    if (u.first < 0 || u.n <= 0) return false;
-    u.tile = u.first / kTile + rest % a.tiles;
-    if ((int64_t)u.tile * kTile >= (int64_t)u.first + u.n) return false;
-    const int page = page_at(a.b.table + u.seq * a.b.table_stride, a.b.table_width, a.c.n_pages,
-                             u.tile >> (a.c.page_shift - 5));
-    u.rec = page < 0 ? nullptr : record_at(a.c, page, u.head, u.tile);
-    return true;
+// A row's channels 32 i + 8 g .. turned; the other members of pairs i and i +
+// dim / 2 are read once more.
+template <int D>
+__device__ __forceinline__ void turn_row(const MoveArgs &a, int64_t row, int head, int64_t turn_at, int g,
+                                         float (&x)[D / 4]) {
+    const Rotation &r = a.rot;
+    const float *turn = r.table + turn_at;
+    const int half = r.dim / 2;
+    const int64_t at = row * a.k.token_stride + head * a.k.head_stride;
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i) {
+        const int ch = 32 * i + 8 * g;
+        if (ch >= r.dim) continue;
+        float *y = x + 8 * i, c[8], s[8];
+        if (r.neighbours) {
+            load_floats<4>(turn + ch / 2, r.wide, c);
+            load_floats<4>(turn + half + ch / 2, r.wide, s);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) turn_pair(y[2 * j], y[2 * j + 1], c[j], s[j]);
+        } else {
+            const bool second = ch >= half;
+            const int pair = second ? ch - half : ch;
+            float other[8];
+            load8(a.k, at + (second ? ch - half : ch + half), other);
+            load_floats<8>(turn + pair, r.wide, c);
+            load_floats<8>(turn + half + pair, r.wide, s);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                float first = second ? other[j] : y[j], last = second ? y[j] : other[j];
+                turn_pair(first, last, c[j], s[j]);
+                y[j] = second ? last : first;
+            }
+        }
+    }
 }
 
-// Codes, scales and zeros of one position's channels, from its row.
-template <int D, int GROUP>
-__device__ __forceinline__ void quantise_row(const uint4 (&raw)[D / 32], int type, _Float16 *scale, _Float16 *zero,
-                                             float *code) {
+// Codes, scales and zeros of one position's channels, from its row; turned by
+// the table's row where there is one.
+template <int D, int GROUP, bool ROT>
+__device__ __forceinline__ void quantise_row(const MoveArgs &a, const uint4 (&raw)[D / 32], int type, int64_t row, int head,
+                                             int64_t turn, int g, _Float16 *scale, _Float16 *zero, float *code) {
     float x[D / 4];
 #pragma unroll
     for (int i = 0; i < D / 32; ++i) {
@@ -135,6 +145,8 @@ __device__ __forceinline__ void quantise_row(const uint4 (&raw)[D / 32], int typ
         else
             raw_to_float<false>(raw[i], x + 8 * i);
     }
+    if constexpr (ROT)
+        if (turn >= 0) turn_row<D>(a, row, head, turn, g, x);
 #pragma unroll
     for (int j = 0; j < D / 4; ++j) x[j] = limited(x[j]);
     quantise<D, GROUP>(x, scale, zero, code);
@@ -143,7 +155,7 @@ __device__ __forceinline__ void quantise_row(const uint4 (&raw)[D / 32], int typ
 // Many new tokens: of two waves on a record one takes the keys and one the
 // values.  Each asks for all its rows before it works on the first: with both
 // in one wave and one row at a time a prompt waited for memory four times over.
-template <int D, int GROUP>
+template <int D, int GROUP, bool ROT>
 __global__ void __launch_bounds__(64 * kMoveWaves) append_kernel(const MoveArgs a) {
     using F = Format<D, GROUP>;
     constexpr int PITCH = D + 4;  // bytes of a row in LDS, off a multiple of the banks
@@ -157,18 +169,25 @@ __global__ void __launch_bounds__(64 * kMoveWaves) append_kernel(const MoveArgs 
     const Tokens &from = keys ? a.k : a.v;
     uint4 raw[2][F::W];
     bool live[2];
+    int64_t row[2];
+    int64_t turn[2] = {-1, -1};
 #pragma unroll
     for (int half = 0; half < 2; ++half) {
         const int i = p0 + 16 * half + m - u.first;
         live[half] = i >= 0 && i < u.n;  // the four lanes of a position are live together
-        load_row<D>(from, u.start + (live[half] ? i : 0), u.head, g, raw[half]);
+        row[half] = u.start + (live[half] ? i : 0);
+        load_row<D>(from, row[half], u.head, g, raw[half]);
+        if constexpr (ROT) {
+            turn[half] = turn_of(a.rot, row[half], p0 + 16 * half + m);
+            live[half] = live[half] && turn[half] >= 0;
+        }
     }
     _Float16 scale[F::NG], zero[F::NG];
     if (keys) {
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
             float code[D / 4];
-            quantise_row<D, GROUP>(raw[half], from.type, scale, zero, code);
+            quantise_row<D, GROUP, ROT>(a, raw[half], from.type, row[half], u.head, turn[half], g, scale, zero, code);
             if (!live[half]) continue;
             uint32_t word[F::W];
 #pragma unroll
@@ -189,7 +208,7 @@ __global__ void __launch_bounds__(64 * kMoveWaves) append_kernel(const MoveArgs 
 #pragma unroll
     for (int half = 0; half < 2; ++half) {
         float code[D / 4];
-        quantise_row<D, GROUP>(raw[half], from.type, scale, zero, code);
+        quantise_row<D, GROUP, false>(a, raw[half], from.type, 0, 0, -1, g, scale, zero, code);
         if (live[half] && g == 0) {
             const int slot = 8 * (m >> 2) + 4 * half + (m & 3);
 #pragma unroll
@@ -215,8 +234,15 @@ __global__ void __launch_bounds__(64 * kMoveWaves) append_kernel(const MoveArgs 
     uint32_t mask = 0;
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-        const int i = p0 + 4 * g + (j & 3) + 16 * (j >> 2) - u.first;
-        if (i >= 0 && i < u.n) mask |= 0xFu << (4 * nibble_of(j));
+        const int t = 4 * g + (j & 3) + 16 * (j >> 2);
+        bool there;
+        if constexpr (ROT) {
+            there = __shfl((int)live[j >> 2], t & 15);
+        } else {
+            const int i = p0 + t - u.first;
+            there = i >= 0 && i < u.n;
+        }
+        if (there) mask |= 0xFu << (4 * nibble_of(j));
     }
     if (mask == 0) return;
 #pragma unroll
@@ -242,11 +268,16 @@ __global__ void __launch_bounds__(64 * kMoveWaves) append_kernel(const MoveArgs 
 // token or so for each sequence and latency is what counts.  32 sequences of 8
 // heads: 3.6 us for one token each, 6.6 for 4 and 8.6 for 6, where the kernel
 // above takes 7.1, 7.2 and 7.4; so it is used up to kFewTokens.
-template <int D, int GROUP>
+template <int D, int GROUP, bool ROT>
 __global__ void __launch_bounds__(64 * kMoveWaves) append_few_kernel(const MoveArgs a) {
     using F = Format<D, GROUP>;
     constexpr int E = D <= 128 ? 2 : 4;
     const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+    if constexpr (ROT)
+        if ((int)blockIdx.x >= a.move_blocks) {
+            rotate_queries<D>(a, (blockIdx.x - a.move_blocks) * kMoveWaves + wave, lane);
+            return;
+        }
     Unit u;
     if (!unit_of(a, blockIdx.x * kMoveWaves + wave, u) || !u.rec) return;
     const int ch = E * lane;
@@ -265,9 +296,16 @@ __global__ void __launch_bounds__(64 * kMoveWaves) append_few_kernel(const MoveA
         float x[2][E];
 #pragma unroll
         for (int e = 0; e < E; ++e) {
-            x[0][e] = limited(elem_to_float(((const uint16_t *)a.k.data)[ka + e], a.k.type));
+            x[0][e] = elem_to_float(((const uint16_t *)a.k.data)[ka + e], a.k.type);
             x[1][e] = limited(elem_to_float(((const uint16_t *)a.v.data)[va + e], a.v.type));
         }
+        if constexpr (ROT) {
+            const int64_t turn = turn_of(a.rot, row, pos);
+            if (turn < 0) continue;
+            turn_few<E>(a, turn, ka - ch, ch, x[0]);
+        }
+#pragma unroll
+        for (int e = 0; e < E; ++e) x[0][e] = limited(x[0][e]);
         // a V code is half a byte of its word; the other half may be another position's
         const int nibble = nibble_of((t & 3) + 4 * half);
         uint8_t *byte[E], old[E];
@@ -315,6 +353,12 @@ __global__ void __launch_bounds__(64 * kMoveWaves) append_few_kernel(const MoveA
             v[0] = scale[1], v[32] = zero[1];
         }
     }
+}
+
+// The queries of many tokens: a wave for each.
+template <int D>
+__global__ void __launch_bounds__(64 * kMoveWaves) queries_kernel(const MoveArgs a) {
+    rotate_queries<D>(a, blockIdx.x * kMoveWaves + (threadIdx.x >> 6), threadIdx.x & 63);
 }
 
 // Positions out of the cache, keys and values by a wave each: V codes go through
@@ -397,10 +441,19 @@ static int launch_move(const MoveArgs &a, bool append, void *stream) {
     const int64_t units = (int64_t)a.b.n_seq * a.tiles * a.c.heads;
     const dim3 grid((uint32_t)((units + kMoveWaves - 1) / kMoveWaves)), block(64 * kMoveWaves);
     const dim3 two_waves((uint32_t)((units * 2 + kMoveWaves - 1) / kMoveWaves));  // for a record
-    if (append && a.b.max_new <= kFewTokens)
-        append_few_kernel<D, GROUP><<<grid, block, 0, (hipStream_t)stream>>>(a);
+    hipStream_t s = (hipStream_t)stream;
+    if (append && a.b.max_new <= kFewTokens && a.rot.dim) {
+        MoveArgs both = a;  // and the queries
+        both.move_blocks = (int)grid.x;
+        const int64_t tokens = a.rot.q_heads ? (int64_t)a.b.n_seq * a.b.max_new : 0;
+        const dim3 all((uint32_t)(grid.x + (tokens + kMoveWaves - 1) / kMoveWaves));
+        append_few_kernel<D, GROUP, true><<<all, block, 0, s>>>(both);
+    } else if (append && a.b.max_new <= kFewTokens)
+        append_few_kernel<D, GROUP, false><<<grid, block, 0, s>>>(a);
+    else if (append && a.rot.dim)
+        append_kernel<D, GROUP, true><<<two_waves, block, 0, s>>>(a);
     else if (append)
-        append_kernel<D, GROUP><<<two_waves, block, 0, (hipStream_t)stream>>>(a);
+        append_kernel<D, GROUP, false><<<two_waves, block, 0, s>>>(a);
     else
         read_kernel<D, GROUP><<<two_waves, block, 0, (hipStream_t)stream>>>(a);
     return (int)hipGetLastError();
@@ -421,7 +474,23 @@ static int move(const MoveArgs &a, bool append, void *stream) {
     return (int)hipErrorInvalidValue;
 }
 
-int launch_append(const MoveArgs &a, void *stream) { return move(a, true, stream); }
-int launch_read(const MoveArgs &a, void *stream) { return move(a, false, stream); }
+static int launch_queries(const MoveArgs &a, void *stream) {
+    const dim3 grid((uint32_t)(((int64_t)a.b.n_seq * a.b.max_new + kMoveWaves - 1) / kMoveWaves)), block(64 * kMoveWaves);
+    hipStream_t s = (hipStream_t)stream;
+    switch (a.c.dim) {
+        case 64: queries_kernel<64><<<grid, block, 0, s>>>(a); break;
+        case 96: queries_kernel<96><<<grid, block, 0, s>>>(a); break;
+        case 128: queries_kernel<128><<<grid, block, 0, s>>>(a); break;
+        default: queries_kernel<256><<<grid, block, 0, s>>>(a);
+    }
+    return (int)hipGetLastError();
+}
+
+int launch_append(const MoveArgs &a, void *stream) {
+    const int rc = a.c.group ? move(a, true, stream) : launch_append8(a, stream);
+    return rc || !a.rot.q_heads || a.b.max_new <= kFewTokens ? rc : launch_queries(a, stream);
+}
+
+int launch_read(const MoveArgs &a, void *stream) { return a.c.group ? move(a, false, stream) : launch_read8(a, stream); }
 
 }  // namespace tkv

@@ -106,16 +106,18 @@ struct Share {
 template <int RECS>
 struct StepPages {
     int page[RECS];
-    __device__ __forceinline__ void load(const AttendArgs &a, const int32_t *table, Pages &pages, int pos, int end,
-                                         int lane) {
+    template <bool WIN>
+    __device__ __forceinline__ void load(const AttendArgs &a, const View<WIN> &e, const int32_t *table, Pages &pages,
+                                         int place, int end, int lane) {
 #pragma unroll
         for (int i = 0; i < RECS; ++i)
-            page[i] = pos + kTile * i < end ? pages.get(a, table, (pos + kTile * i) >> a.c.page_shift, lane) : -1;
+            page[i] = place + kTile * i < end
+                          ? pages.get(a, table, e.position(place + kTile * i) >> a.c.page_shift, lane) : -1;
     }
     __device__ __forceinline__ int of(int rec) const { return RECS == 1 || rec == 0 ? page[0] : page[RECS - 1]; }
 };
 
-template <int D, int GROUP, int NT, bool BF16>
+template <int D, int GROUP, int NT, bool BF16, bool WIN>
 __global__ void __launch_bounds__(64 * kAttendWaves, 2) rows_kernel(const AttendArgs a) {
     using F = Format<D, GROUP>;
     constexpr int R = 16 * NT * kAttendWaves;
@@ -128,20 +130,23 @@ __global__ void __launch_bounds__(64 * kAttendWaves, 2) rows_kernel(const Attend
     int block, split, head, seq;
     place(a, block, split, head, seq);
     const int32_t *table = a.b.table + seq * a.b.table_stride;
-    const Extent e(a, seq);
-    const Chunks chunks(a, e.len);
-    if (block * R >= e.rows || split >= chunks.n) return;
+    View<WIN> e(a, seq);
+    if (block * R >= e.rows) return;
+    e.narrow_to_block(a, block);
+    const Chunks chunks(a, e.span());
+    if (split >= chunks.n) return;
     const int t0 = split * chunks.size;
     Pages pages;
-    pages.load(a, table, t0 >> a.c.page_shift, lane);
+    pages.load(a, table, e.position(t0) >> a.c.page_shift, lane);
     const int r0 = block * R + wave * 16 * NT;
 
     // positions that some row of the workgroup sees, and of the wave
     const int last = block * R + R < e.rows ? block * R + R - 1 : e.rows - 1;
-    int end = e.limit(a, divided(last, a.by_group_heads));
+    int end = e.place(e.limit(a, divided(last, a.by_group_heads)));
     end = end < t0 + chunks.size ? end : t0 + chunks.size;
     const int wave_last = r0 + 16 * NT < e.rows ? r0 + 16 * NT - 1 : e.rows - 1;
-    const int wave_end = r0 < e.rows ? e.limit(a, divided(wave_last, a.by_group_heads)) : 0;
+    const int wave_i1 = divided(wave_last, a.by_group_heads);
+    const int wave_end = r0 < e.rows ? e.place(e.limit(a, wave_i1)) : 0;
     const int all_see = r0 < e.rows ? e.limit(a, divided(r0, a.by_group_heads)) : 0;
 
     Row<D, GROUP> raw[NT];
@@ -150,17 +155,16 @@ __global__ void __launch_bounds__(64 * kAttendWaves, 2) rows_kernel(const Attend
     const int rec = wave / (2 * F::S), hs = wave % (2 * F::S);
     Share<D, GROUP> share;
     StepPages<RECS> step_now, step_next;
-    step_now.load(a, table, pages, t0, end, lane);
-    share.load(a, step_now.of(rec), head, t0 + rec * kTile, hs, lane);
+    step_now.load(a, e, table, pages, t0, end, lane);
+    share.load(a, step_now.of(rec), head, e.position(t0 + rec * kTile), hs, lane);
 
     h8 q[NT][F::W], sums[NT];
     float factor[NT];
-    int limit[NT];
+    Sight<WIN> sight[NT];
     Softmax<D, GROUP> s[NT];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-        const int r = r0 + 16 * nt + n;
-        limit[nt] = r < e.rows ? e.limit(a, divided(r, a.by_group_heads)) : 0;
+        sight[nt].load(a, e, r0 + 16 * nt + n);
         float qsum[F::NG], f;
         raw[nt].template operand<BF16>(a, q[nt], qsum, f);
         sums[nt] = sum_parts<D, GROUP>(qsum, g);
@@ -174,13 +178,20 @@ __global__ void __launch_bounds__(64 * kAttendWaves, 2) rows_kernel(const Attend
         stage[i / (RECS * kTile)].kz[i / kTile % RECS][i % kTile] = (h8){0, 0, 0, 0, 0, 0, 0, 0};
     __syncthreads();
     share.unpack(stage[0], rec, hs, lane, e.len);
-    step_next.load(a, table, pages, t0 + STEP, end, lane);
-    share.load(a, step_next.of(rec), head, t0 + STEP + rec * kTile, hs, lane);
+    step_next.load(a, e, table, pages, t0 + STEP, end, lane);
+    share.load(a, step_next.of(rec), head, e.position(t0 + STEP + rec * kTile), hs, lane);
     __syncthreads();
 
     int now = 0;
     for (int p0 = t0; p0 < end; p0 += STEP, now ^= 1) {
         const Stage<D, GROUP, RECS> &from = stage[now];
+        int at[RECS];  // positions of the step's records
+        bool windowed = false;
+#pragma unroll
+        for (int i = 0; i < RECS; ++i) {
+            at[i] = e.position(p0 + kTile * i);
+            windowed |= e.windowed(a, wave_i1, at[i]);
+        }
         if (p0 < wave_end) {
             float x[NT][8 * RECS];
 #pragma unroll
@@ -216,13 +227,13 @@ __global__ void __launch_bounds__(64 * kAttendWaves, 2) rows_kernel(const Attend
             bool missing = false;
 #pragma unroll
             for (int i = 0; i < RECS; ++i) missing |= step_now.page[i] < 0;
-            if (p0 + STEP > all_see || missing) {  // some position is not seen by some row
+            if (at[RECS - 1] + kTile > all_see || missing || windowed) {  // some position is not seen by some row
 #pragma unroll
                 for (int j = 0; j < 8 * RECS; ++j) {
-                    const int pos = p0 + kTile * (j >> 3) + 16 * ((j >> 2) & 1) + 4 * g + (j & 3);
+                    const int pos = at[j >> 3] + 16 * ((j >> 2) & 1) + 4 * g + (j & 3);
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt)
-                        if (pos >= limit[nt] || step_now.page[j >> 3] < 0) x[nt][j] = -__builtin_inff();
+                        if (step_now.page[j >> 3] < 0 || !sight[nt].sees(a, e, pos)) x[nt][j] = -__builtin_inff();
                 }
             }
             bool grown = false;
@@ -257,8 +268,8 @@ __global__ void __launch_bounds__(64 * kAttendWaves, 2) rows_kernel(const Attend
         }
         share.unpack(stage[now ^ 1], rec, hs, lane, e.len);
         step_now = step_next;
-        step_next.load(a, table, pages, p0 + 2 * STEP, end, lane);
-        share.load(a, step_next.of(rec), head, p0 + 2 * STEP + rec * kTile, hs, lane);
+        step_next.load(a, e, table, pages, p0 + 2 * STEP, end, lane);
+        share.load(a, step_next.of(rec), head, e.position(p0 + 2 * STEP + rec * kTile), hs, lane);
         __syncthreads();
     }
 

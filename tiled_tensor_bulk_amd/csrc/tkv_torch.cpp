@@ -168,6 +168,46 @@ int do_append(const Cache &c, const Tensor &k, const Tensor &v, const Tensor &ta
     return tkv_append(&c.described, &kt, &vt, &b.b, on.handle());
 }
 
+py::tuple do_append_rotated(const Cache &c, const Tensor &k, const Tensor &v, const Tensor &table, const Tensor &lens,
+                            const Maybe &starts, std::optional<int64_t> max_new, const Tensor &cos_sin,
+                            const Maybe &positions, bool neighbours, const Maybe &q, const Maybe &q_out_,
+                            std::optional<int64_t> stream) {
+    const tkv_tokens kt = tokens(k, "k", c.heads, -1, false, c);
+    const int64_t n = k.size(0);
+    const tkv_tokens vt = tokens(v, "v", c.heads, n, false, c);
+    const Batch b = batch(c, table, lens, starts, n, max_new);
+    const Stream on(c, stream);
+    tkv_rotation r{};
+    typed(cos_sin, "cos_sin", at::kFloat, c);
+    TKV_CHECK(cos_sin.dim() == 2, "cos_sin must be a tensor [positions, channels]");
+    TKV_CHECK(cos_sin.stride(1) == 1 || cos_sin.numel() == 0, "cos_sin's rows must be contiguous");
+    TKV_CHECK(cos_sin.size(1) <= c.dim, "cos_sin turns ", cos_sin.size(1), " channels, the cache has ", c.dim);
+    r.cos_sin = cos_sin.data_ptr<float>();
+    r.n_positions = cos_sin.size(0);
+    r.rot_dim = (int32_t)cos_sin.size(1);
+    r.stride = r.n_positions < 2 ? r.rot_dim : cos_sin.stride(0);
+    r.neighbours = neighbours;
+    if (positions) {
+        typed(*positions, "positions", at::kInt, c);
+        TKV_CHECK(positions->dim() == 1 && positions->size(0) == n && (n < 2 || positions->stride(0) == 1),
+                  "positions must be a contiguous vector of the ", n, " tokens");
+        r.positions = positions->data_ptr<int32_t>();
+    }
+    TKV_CHECK(q || !q_out_, "q_out is only written where q is given");
+    Tensor q_out;
+    if (q) {
+        r.q = tokens(*q, "q", -1, n, false, c);
+        TKV_CHECK(q->size(1) > 0 && q->size(1) <= INT32_MAX, "q has no heads, or too many");
+        r.q_heads = (int32_t)q->size(1);
+        q_out = q_out_ ? *q_out_ : made({n, q->size(1), c.dim}, q->scalar_type(), c);
+        r.q_out = tokens(q_out, "q_out", q->size(1), n, false, c);
+        apart(r.q_out, "q_out", q_out);
+        TKV_CHECK(q_out.scalar_type() == q->scalar_type(), "q_out must be ", name_of(q->scalar_type()));
+    }
+    const int st = tkv_append_rotated(&c.described, &kt, &vt, &r, &b.b, on.handle());
+    return py::make_tuple(st, q ? py::cast(q_out) : py::none());
+}
+
 py::tuple do_read(const Cache &c, const Tensor &table, const Tensor &lens, const Maybe &starts,
                std::optional<int64_t> max_new, std::optional<int64_t> n_tokens, at::ScalarType dtype, const Maybe &k_,
                const Maybe &v_, std::optional<int64_t> stream) {
@@ -204,11 +244,21 @@ int64_t bound(std::optional<int64_t> max_len, int64_t held) {
     return std::max<int64_t>(n, -1);
 }
 
-py::tuple do_attend(const Cache &c, const Tensor &q, const Tensor &table, const Tensor &lens, const Maybe &starts,
-                 std::optional<int64_t> max_new, std::optional<int64_t> max_len, std::optional<double> scale, bool causal,
-                 const Maybe &scores, const Maybe &scores_out, const Maybe &out_, const Maybe &lse_,
-                 const Maybe &workspace, std::optional<int64_t> stream) {
+py::tuple do_attend_window(const Cache &c, const Tensor &q, const Tensor &table, const Tensor &lens, const Maybe &starts,
+                           std::optional<int64_t> max_new, std::optional<int64_t> max_len, std::optional<double> scale,
+                           bool causal, const Maybe &scores, const Maybe &scores_out, const Maybe &out_, const Maybe &lse_,
+                           const Maybe &workspace, std::optional<int64_t> stream, std::optional<int64_t> window, int64_t
+                           sinks) {
     const Stream on(c, stream);
+    TKV_CHECK(window || sinks == 0, "sinks are only apart from the others where a window is given");
+    tkv_window seen{};
+    if (window) {
+        TKV_CHECK(*window >= 1, "window is less than 1");
+        TKV_CHECK(sinks >= 0, "sinks is negative");
+        seen.window = (int32_t)std::min<int64_t>(*window, INT32_MAX);
+        seen.sinks = (int32_t)std::min<int64_t>(sinks, INT32_MAX);
+    }
+    const tkv_window *const w = window ? &seen : nullptr;
     tkv_attend_args a{};
     a.q = tokens(q, "q", -1, -1, false, c);
     const int64_t n = q.size(0), heads = q.size(1);
@@ -238,7 +288,7 @@ py::tuple do_attend(const Cache &c, const Tensor &q, const Tensor &table, const 
     a.scale = (float)(scale ? *scale : 1.0 / std::sqrt((double)c.dim));
     a.causal = causal;
     uint64_t need = 0;
-    int st = tkv_attend_workspace(&c.described, &a, &b.b, &need);
+    int st = tkv_attend_window_workspace(&c.described, &a, w, &b.b, &need);
     Tensor room;
     if (st == TMAP_SUCCESS && need) {
         if (workspace) {
@@ -251,8 +301,16 @@ py::tuple do_attend(const Cache &c, const Tensor &q, const Tensor &table, const 
         a.workspace = room.data_ptr();
         a.workspace_bytes = (uint64_t)room.numel();
     }
-    if (st == TMAP_SUCCESS) st = tkv_attend(&c.described, &a, &b.b, on.handle());
+    if (st == TMAP_SUCCESS) st = tkv_attend_window(&c.described, &a, w, &b.b, on.handle());
     return py::make_tuple(st, out, lse);
+}
+
+py::tuple do_attend(const Cache &c, const Tensor &q, const Tensor &table, const Tensor &lens, const Maybe &starts,
+                 std::optional<int64_t> max_new, std::optional<int64_t> max_len, std::optional<double> scale, bool causal,
+                 const Maybe &scores, const Maybe &scores_out, const Maybe &out, const Maybe &lse, const Maybe &workspace,
+                 std::optional<int64_t> stream) {
+    return do_attend_window(c, q, table, lens, starts, max_new, max_len, scale, causal, scores, scores_out, out, lse,
+                            workspace, stream, std::nullopt, 0);
 }
 
 py::tuple do_evict(const Cache &c, const Tensor &table, const Tensor &lens, const Tensor &scores, int64_t budget,
@@ -294,7 +352,9 @@ py::tuple do_evict(const Cache &c, const Tensor &table, const Tensor &lens, cons
 PYBIND11_MODULE(_tkv, m) {
     py::class_<Cache>(m, "Cache").def(py::init<int64_t, Tensor, int64_t, int64_t, int64_t>());
     m.def("append", torch::wrap_pybind_function(do_append));
+    m.def("append_rotated", torch::wrap_pybind_function(do_append_rotated));
     m.def("read", torch::wrap_pybind_function(do_read));
     m.def("attend", torch::wrap_pybind_function(do_attend));
+    m.def("attend_window", torch::wrap_pybind_function(do_attend_window));
     m.def("evict", torch::wrap_pybind_function(do_evict));
 }
