@@ -161,6 +161,30 @@ struct Sight {
         const int i = divided(row, a.by_group_heads);
         until = row >= e.rows ? 0 : WIN ? e.border(a, i) : e.limit(a, i);
     }
+    // The products of a record that the row does not see become -inf: of a lane's 16 positions 4 h + 0..3 of each 8.  Of a
+    // record that is gone no row sees anything.
+    template <class X>
+    __device__ __forceinline__ void mask(const AttendArgs &a, const Extent &e, int at, bool gone, int h, X &x) const {
+        static_assert(WIN, "of a border");
+        const int first = at + 4 * h, limit = until < e.len ? until : e.len;
+        uint32_t seen = gone ? 0 : below(limit - first);
+        if (a.window) {
+            const int64_t low = (int64_t)until - a.window - first;
+            seen &= ~below(low < 0 ? 0 : low > kTile ? kTile : (int)low) | below(a.sinks - first);
+        }
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {
+            const uint32_t all = (uint32_t)((int32_t)(seen << (31 - j)) >> 31);  // of bit j
+            const float y = x[j];  // a bit cast of a vector's element would be one of its first
+            x[j] = __builtin_bit_cast(float, (__builtin_bit_cast(uint32_t, y) & all) | (0xFF800000u & ~all));
+        }
+    }
+    // which of the 16 are less than n from the first one
+    static __device__ __forceinline__ uint32_t below(int n) {
+        n = n < 0 ? 0 : n > kTile ? kTile : n;
+        const int part = n & 7;
+        return (1u << (4 * (n >> 3) + (part < 4 ? part : 4))) - 1;
+    }
     // (the difference counts where the border is above the position)
     __device__ __forceinline__ bool sees(const AttendArgs &a, const Extent &e, int position) const {
         if (!WIN) return position < until;

@@ -248,7 +248,7 @@ Split plan(const tkv::AttendArgs &a, int cus) {
     const int64_t n_seq = a.b.n_seq, rows = a.rows;
     const bool scores = a.scores_out;
     Split s{};
-    s.row_tile = rows <= 16 || (c.dim > 128 && rows <= 48) ? 16 : rows <= 32 ? 32 : rows <= 64 || c.dim > 128 ? 64 : 128;
+    s.row_tile = rows <= 16 || (c.dim > 128 && rows <= 48) ? 16 : rows <= 32 ? 32 : rows <= 64 || (c.dim > 128 && c.group) ? 64 : 128;
     s.row_blocks = (int)((rows + s.row_tile - 1) / s.row_tile);
     s.row_tiles = (int)((rows + 15) / 16);
     const int64_t max_len = seen_at_most(a, s.row_tile);
