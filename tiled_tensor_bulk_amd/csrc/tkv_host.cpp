@@ -202,7 +202,10 @@ uint64_t up(uint64_t v, uint64_t to) { return (v + to - 1) / to * to; }
 // manner, and that reads each record for every 16 rows, which pays up to 48 of
 // them: 8 sequences of up to 1500 positions, 34 rows, 22 us, with 64 rows of the
 // second manner 31; 4 of up to 8192, 32 rows 38 us, 48 rows 46 and 42, 64 rows
-// 60 and 44.
+// 60 and 44.  The 8-bit format's many rows come in blocks of 128 only, and it
+// takes tiles of 16 or 32 up to 64 rows: 128 channels, 8 heads, 48 rows, 8
+// sequences of up to 1500 positions 20 us, in a block of 64 that was 25; 4 of up
+// to 8192 34 and 33; 256 channels, 4 heads, 64 rows, 31 and 46, 60 and 49.
 //
 // Chunks: as long as they leave 8 workgroups of few rows for a compute unit, 2
 // of many (512 new tokens over 8192 positions, 2 sequences: 217 us with 2, 307
@@ -230,7 +233,6 @@ constexpr int kLongForOne = 1 << 14;
 constexpr int kBlocksPerCu = 8;
 constexpr int kRowBlocksPerCu = 2;
 
-//
 // With a window the same of what a block of rows may see of a sequence.
 int64_t seen_at_most(const tkv::AttendArgs &a, int row_tile) {
     if (!a.window) return a.max_len;
@@ -243,12 +245,16 @@ int64_t seen_at_most(const tkv::AttendArgs &a, int row_tile) {
     return n < a.max_len ? n : a.max_len;
 }
 
+// Rows up to which the waves of a workgroup share the positions.
+int64_t most_few_rows(const Cache &c) { return c.group == 0 ? 64 : c.dim > 128 ? 48 : 32; }
+
 Split plan(const tkv::AttendArgs &a, int cus) {
     const Cache &c = a.c;
     const int64_t n_seq = a.b.n_seq, rows = a.rows;
     const bool scores = a.scores_out;
     Split s{};
-    s.row_tile = rows <= 16 || (c.dim > 128 && rows <= 48) ? 16 : rows <= 32 ? 32 : rows <= 64 || (c.dim > 128 && c.group) ? 64 : 128;
+    const bool few = rows <= most_few_rows(c);
+    s.row_tile = rows <= 16 || (few && c.dim > 128) ? 16 : few ? 32 : c.group && (rows <= 64 || c.dim > 128) ? 64 : 128;
     s.row_blocks = (int)((rows + s.row_tile - 1) / s.row_tile);
     s.row_tiles = (int)((rows + 15) / 16);
     const int64_t max_len = seen_at_most(a, s.row_tile);
@@ -296,13 +302,13 @@ Split plan(const tkv::AttendArgs &a, int cus) {
 uint64_t most_workspace(const Cache &c, int64_t n_seq, int64_t rows, int64_t max_len, bool scores, int cus) {
     const auto least = [](uint64_t a, uint64_t b) { return a < b ? a : b; };
     const auto most = [](uint64_t a, uint64_t b) { return a > b ? a : b; };
-    const uint64_t heads = (uint64_t)n_seq * c.heads, few = least(rows, 48);
+    const uint64_t heads = (uint64_t)n_seq * c.heads, few = least(rows, c.group ? 48 : 64);
     const auto chunks = [&](int64_t chunk) { return (uint64_t)((max_len + chunk - 1) / chunk); };
     // rows of partial sums.  In chunks shorter than kMostChunk: the workgroups, kBlocksPerCu for a
     // compute unit of 32 rows or kRowBlocksPerCu of 128, and no more than chunks of 256 make
     uint64_t parts = least((uint64_t)cus * most(kBlocksPerCu * 32, kRowBlocksPerCu * 128), heads * rows * chunks(256));
     if (chunks(kMostChunk) > 1) parts = most(parts, heads * rows * chunks(kMostChunk));
-    if (max_len > kLeastChunk)  // an even split: tiles of 16 rows up to 48 of them, or of 32
+    if (max_len > kLeastChunk)  // an even split: tiles of 16 rows up to 48 of them (64 in 8 bits), or of 32
         parts = most(parts, least(n_seq, tkv::kEvenSeqs) * c.heads * (few + 15) +
                                 (uint64_t)cus * tkv::kMostResident * least(rows, 32));
     uint64_t total = 0;

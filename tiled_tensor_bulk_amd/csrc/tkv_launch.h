@@ -25,14 +25,14 @@ static int launch_type(const AttendArgs &a, int row_tile, void *stream) {
             attend_kernel<D, GROUP, 2, BF16, false, WIN><<<grid, block, 0, s>>>(a);
     } else if (row_tile == 64) {
         if constexpr (GROUP == 0)
-            rows8_kernel<D, 2, BF16><<<grid, dim3(128), 0, s>>>(a);
+            return (int)hipErrorInvalidValue;
         else
             rows_kernel<D, GROUP, 1, BF16, WIN><<<grid, block, 0, s>>>(a);
     } else {
         if constexpr (D > 128 && GROUP != 0)
             return (int)hipErrorInvalidValue;
         else if constexpr (GROUP == 0)
-            rows8_kernel<D, 4, BF16><<<grid, dim3(256), 0, s>>>(a);
+            rows8_kernel<D, BF16><<<grid, block, 0, s>>>(a);
         else
             rows_kernel<D, GROUP, 2, BF16, WIN><<<grid, block, 0, s>>>(a);
     }

@@ -1,8 +1,8 @@
 // tkv_rows8.h -- attention of many rows over the 8-bit cache: a chunk of a
 // prompt, or all of a decoder's tokens over an encoder's states.
 //
-// A workgroup's waves, two or four, hold 32 rows each and go over all positions
-// of the chunk, a record at a time.  Each wave converts its part of the next
+// A workgroup's four waves hold 32 rows each and go over all positions of the
+// chunk, a record at a time.  Each wave converts its part of the next
 // record's words into LDS, as fp16 numbers in the order in which the matrix unit
 // takes them, and all read all of it back; there are two stages and one barrier
 // a record, and a word is asked for a record before it is converted.
@@ -26,6 +26,8 @@
 // 512 new tokens each over 2 sequences of up to 8192 positions 141 us, 676 TFLOP/s,
 // where the longer one's workgroups are the last ones; 6000 tokens through a window
 // of 1024 137 us, 686 TFLOP/s.  Tiles of 16 rows, as with 4 bits, took 143 and 171.
+// 256 channels (304 TFLOP/s, 4 heads of 2 rows, the first of these) leave one wave
+// on a SIMD, and the products' sums in accumulation registers.
 #pragma once
 
 #include "tkv_rows.h"
@@ -65,15 +67,15 @@ struct Record8 {
     __device__ __forceinline__ int values() const { return there ? (int)(ex >> 8) : 0; }
 };
 
-// What a wave brings of a record's keys, or values: words wave, wave + WAVES, ..
+// What a wave brings of a record's keys, or values: words wave, wave + 4, ..
 // of the record's 2 * (D / 32); past the last one, that again.
-template <int D, int WAVES>
+template <int D>
 struct Share8 {
-    static constexpr int WORDS = 2 * (D / 32), COUNT = (WORDS + WAVES - 1) / WAVES;
+    static constexpr int WORDS = 2 * (D / 32), COUNT = (WORDS + kAttendWaves - 1) / kAttendWaves;
     uint2 w[COUNT];
     static __device__ __forceinline__ int which(int i, int wave) {
-        const int word = wave + i * WAVES;
-        return WORDS % WAVES && word >= WORDS ? WORDS - 1 : word;
+        const int word = wave + i * kAttendWaves;
+        return WORDS % kAttendWaves && word >= WORDS ? WORDS - 1 : word;
     }
     __device__ __forceinline__ void load(const char *codes, int wave, int lane) {
 #pragma unroll
@@ -141,7 +143,17 @@ __device__ __forceinline__ float wide_operand(const AttendArgs &a, const uint4 (
 }
 
 // Waves of a SIMD that the registers are to suffice for.
-constexpr int rows8_waves(int d, int waves) { return d > 128 ? 1 : d == 128 && waves == 2 ? 2 : d > 64 ? 3 : 4; }
+constexpr int rows8_waves(int d) { return d > 128 ? 1 : d > 64 ? 3 : 4; }
+
+// Sums that are made by here, and not later.  A kernel of more than 256
+// registers has products in the accumulation registers.
+template <int D>
+__device__ __forceinline__ void here(f16v &x) {
+    if constexpr (rows8_waves(D) == 1)
+        asm volatile("" : "+a"(x));
+    else
+        asm volatile("" : "+v"(x));
+}
 
 // 4 numbers rounded to 16 bits.
 template <bool BF16>
@@ -154,11 +166,11 @@ __device__ __forceinline__ uint2 packed(f4 x) {
     }
 }
 
-template <int D, int WAVES, bool BF16>
-__global__ void __launch_bounds__(64 * WAVES, rows8_waves(D, WAVES)) rows8_kernel(const AttendArgs a) {
+template <int D, bool BF16>
+__global__ void __launch_bounds__(64 * kAttendWaves, rows8_waves(D)) rows8_kernel(const AttendArgs a) {
     using F = Format<D, 0>;
-    using Share = Share8<D, WAVES>;
-    constexpr int R = 32 * WAVES, W = F::W;
+    using Share = Share8<D>;
+    constexpr int R = 32 * kAttendWaves, W = F::W;
     constexpr int FRAGS = 2 * W;  // operands of a record's keys, of 16 channels, and of its values
     __shared__ Stage8<D> stage;
 
@@ -266,7 +278,7 @@ __global__ void __launch_bounds__(64 * WAVES, rows8_waves(D, WAVES)) rows8_kerne
 #pragma unroll
         for (int c = 0; c < FRAGS; ++c) {
             x = __builtin_amdgcn_mfma_f32_32x32x16_f16(frag[c], q[c], x, 0, 0, 0);
-            asm volatile("" : "+v"(x));
+            here<D>(x);
             ask(c + AHEAD, odd);
             // a word is asked for again where it has been unpacked: it has a step to come
 #pragma unroll
@@ -316,7 +328,7 @@ __global__ void __launch_bounds__(64 * WAVES, rows8_waves(D, WAVES)) rows8_kerne
             for (int b = 0; b < W; ++b) {
                 const int c = FRAGS + s * W + b;
                 o[b] = __builtin_amdgcn_mfma_f32_32x32x16_f16(frag[c], p, o[b], 0, 0, 0);
-                asm volatile("" : "+v"(o[b]));
+                here<D>(o[b]);
                 ask(c + AHEAD, odd);
                 __builtin_amdgcn_sched_barrier(0);
             }
