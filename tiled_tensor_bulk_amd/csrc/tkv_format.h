@@ -249,8 +249,13 @@ __device__ __forceinline__ void store8(const Tokens &t, int64_t offset, const fl
     }
     uint16_t *p = (uint16_t *)t.data + offset;
     uint16_t e[8];
+    if (t.type == kBf16) {  // asked once
 #pragma unroll
-    for (int i = 0; i < 8; ++i) e[i] = float_to_elem(in[i], t.type);
+        for (int i = 0; i < 8; ++i) e[i] = float_to_elem(in[i], kBf16);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) e[i] = float_to_elem(in[i], kF16);
+    }
     if (t.wide) {
         uint32_t w[4];
 #pragma unroll

@@ -176,7 +176,7 @@ tmap_status move_args(const tkv_cache *cache, const tkv_tokens *k, const tkv_tok
     constexpr int kWaves = tkv::kBlockThreads / 64;
     TKV_REQUIRE(launchable(a.tiles, a.b.n_seq, a.c.heads) &&
                     fits(over((int64_t)a.tiles * a.b.n_seq * a.c.heads,
-                              append && a.b.max_new <= tkv::kFewTokens ? kWaves : kWaves / 2)),
+                              append && a.b.max_new <= tkv::kFewTokens && a.c.group ? kWaves : kWaves / 2)),
                 "too many sequences, heads and new tokens");
     return TMAP_SUCCESS;
 }
@@ -308,8 +308,8 @@ uint64_t most_workspace(const Cache &c, int64_t n_seq, int64_t rows, int64_t max
     // compute unit of 32 rows or kRowBlocksPerCu of 128, and no more than chunks of 256 make
     uint64_t parts = least((uint64_t)cus * most(kBlocksPerCu * 32, kRowBlocksPerCu * 128), heads * rows * chunks(256));
     if (chunks(kMostChunk) > 1) parts = most(parts, heads * rows * chunks(kMostChunk));
-    if (max_len > kLeastChunk)  // an even split: tiles of 16 rows up to 48 of them (64 in 8 bits), or of 32
-        parts = most(parts, least(n_seq, tkv::kEvenSeqs) * c.heads * (few + 15) +
+    if (max_len > kLeastChunk)  // an even split: tiles of 16 rows up to 48 of them, or one of 32; in 8 bits several
+        parts = most(parts, least(n_seq, tkv::kEvenSeqs) * c.heads * (few + (c.group ? 15 : 31)) +
                                 (uint64_t)cus * tkv::kMostResident * least(rows, 32));
     uint64_t total = 0;
     if (max_len > 256) total = up(parts * c.dim * 4, 256) + up(parts * 8, 256) + up((tkv::kEvenSeqs + 1) * 4, 256);
@@ -427,8 +427,9 @@ tmap_status rotation_args(const tkv_rotation *in, tkv::MoveArgs &a) {
     r.same = in->q.data == in->q_out.data && in->q.token_stride == in->q_out.token_stride &&
              in->q.head_stride == in->q_out.head_stride;
     TKV_REQUIRE(r.same || in->q.data != in->q_out.data || empty, "q_out is q with other strides");
-    // a wave for each token
-    const int64_t blocks = over((int64_t)a.b.n_seq * a.b.max_new, tkv::kBlockThreads / 64);
+    // a wave for each token, or more of them for few
+    const int64_t tokens = (int64_t)a.b.n_seq * a.b.max_new;
+    const int64_t blocks = over(tokens > tkv::kQueryTokens ? tokens : tkv::kQueryTokens * tkv::kQueryWaves, tkv::kBlockThreads / 64);
     const int64_t records = a.b.max_new <= tkv::kFewTokens ? over((int64_t)a.tiles * a.b.n_seq * a.c.heads, 2) : 0;
     TKV_REQUIRE(launchable(a.b.n_seq, a.b.max_new) && fits(blocks + records), "too many sequences and new tokens");
     return TMAP_SUCCESS;

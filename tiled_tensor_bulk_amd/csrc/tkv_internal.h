@@ -80,12 +80,16 @@ struct Rotation {
     int32_t same;              // q_out is q: what is not turned stays
 };
 
+constexpr int64_t kQueryTokens = 1024;  // up to which a token's queries may have several waves
+constexpr int kQueryWaves = 64;         // at most
+
 struct MoveArgs {  // append and read
     Cache c;
     Tokens k, v;
     Batch b;
     int32_t tiles;        // records that a sequence's new tokens can touch
     int32_t move_blocks;  // workgroups of the first part of a launch; the others take the queries
+    int32_t query_waves;  // of a token's queries there
     Rotation rot;
 };
 

@@ -275,7 +275,8 @@ __global__ void __launch_bounds__(64 * kMoveWaves) append_few_kernel(const MoveA
     const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
     if constexpr (ROT)
         if ((int)blockIdx.x >= a.move_blocks) {
-            rotate_queries<D>(a, (blockIdx.x - a.move_blocks) * kMoveWaves + wave, lane);
+            const int w = (blockIdx.x - a.move_blocks) * kMoveWaves + wave;
+            rotate_queries<D, 1>(a, w / a.query_waves, w % a.query_waves, a.query_waves, lane);
             return;
         }
     Unit u;
@@ -358,7 +359,7 @@ __global__ void __launch_bounds__(64 * kMoveWaves) append_few_kernel(const MoveA
 // The queries of many tokens: a wave for each.
 template <int D>
 __global__ void __launch_bounds__(64 * kMoveWaves) queries_kernel(const MoveArgs a) {
-    rotate_queries<D>(a, blockIdx.x * kMoveWaves + (threadIdx.x >> 6), threadIdx.x & 63);
+    rotate_queries<D, 4>(a, blockIdx.x * kMoveWaves + (threadIdx.x >> 6), 0, 1, threadIdx.x & 63);
 }
 
 // Positions out of the cache, keys and values by a wave each: V codes go through
@@ -446,7 +447,8 @@ static int launch_move(const MoveArgs &a, bool append, void *stream) {
         MoveArgs both = a;  // and the queries
         both.move_blocks = (int)grid.x;
         const int64_t tokens = a.rot.q_heads ? (int64_t)a.b.n_seq * a.b.max_new : 0;
-        const dim3 all((uint32_t)(grid.x + (tokens + kMoveWaves - 1) / kMoveWaves));
+        both.query_waves = query_waves(a, tokens, kQueryHeads<D>);
+        const dim3 all((uint32_t)(grid.x + (tokens * both.query_waves + kMoveWaves - 1) / kMoveWaves));
         append_few_kernel<D, GROUP, true><<<all, block, 0, s>>>(both);
     } else if (append && a.b.max_new <= kFewTokens)
         append_few_kernel<D, GROUP, false><<<grid, block, 0, s>>>(a);

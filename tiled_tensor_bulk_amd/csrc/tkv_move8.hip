@@ -300,7 +300,8 @@ __global__ void __launch_bounds__(64 * kMoveWaves) append8_few_kernel(const Move
     const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
     if constexpr (ROT)
         if ((int)blockIdx.x >= a.move_blocks) {
-            rotate_queries<D>(a, (blockIdx.x - a.move_blocks) * kMoveWaves + wave, lane);
+            const int w = (blockIdx.x - a.move_blocks) * kMoveWaves + wave;
+            rotate_queries<D, 1>(a, w / a.query_waves, w % a.query_waves, a.query_waves, lane);
             return;
         }
     const bool keys = __builtin_amdgcn_readfirstlane(wave & 1) == 0;
@@ -399,7 +400,8 @@ static int launch_move8(const MoveArgs &a, bool append, void *stream) {
         MoveArgs both = a;  // and the queries
         both.move_blocks = (int)two_waves.x;
         const int64_t tokens = a.rot.q_heads ? (int64_t)a.b.n_seq * a.b.max_new : 0;
-        const dim3 all((uint32_t)(two_waves.x + (tokens + kMoveWaves - 1) / kMoveWaves));
+        both.query_waves = query_waves(a, tokens, kQueryHeads<D>);
+        const dim3 all((uint32_t)(two_waves.x + (tokens * both.query_waves + kMoveWaves - 1) / kMoveWaves));
         append8_few_kernel<D, true><<<all, block, 0, s>>>(both);
     } else if (a.b.max_new <= kFewTokens) {
         append8_few_kernel<D, false><<<two_waves, block, 0, s>>>(a);

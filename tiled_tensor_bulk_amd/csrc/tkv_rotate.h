@@ -136,11 +136,21 @@ __device__ __forceinline__ void unit_floats(uint4 lo, uint4 hi, int type, float 
     }
 }
 
-// The queries of one token, by one wave.  `token` counts max_new for each sequence.
 template <int D>
-__device__ __forceinline__ void rotate_queries(const MoveArgs &a, int token, int lane) {
-    constexpr int U = D / 16, HEADS = 64 / U;  // units of a row, rows at once
-    constexpr int AHEAD = 4;
+constexpr int kQueryHeads = 64 / (D / 16);  // rows that a wave has at once
+
+// Waves of a token's queries in a launch of few tokens.
+inline int query_waves(const MoveArgs &a, int64_t tokens, int heads_at_once) {
+    return tokens > kQueryTokens || a.rot.q_heads > kQueryWaves * heads_at_once ? 1 : (a.rot.q_heads + heads_at_once - 1) / heads_at_once;
+}
+
+// The queries of one token by `waves` waves, of which this is one, AHEAD rows at a
+// time.  `token` counts max_new for each sequence.  One row each where a card has
+// more waves than tokens: with four of them in a wave a step of 32 sequences and
+// 32 heads took 15.1 us with its reading back, QQQ so.
+template <int D, int AHEAD>
+__device__ __forceinline__ void rotate_queries(const MoveArgs &a, int token, int wave, int waves, int lane) {
+    constexpr int U = D / 16, HEADS = kQueryHeads<D>;  // units of a row
     const Rotation &r = a.rot;
     const int seq = token / a.b.max_new, i = token % a.b.max_new;
     if (seq >= a.b.n_seq) return;
@@ -158,7 +168,7 @@ __device__ __forceinline__ void rotate_queries(const MoveArgs &a, int token, int
     int c0, c1;
     unit_channels(r, unit, c0, c1);
     const int64_t from = (start + i) * r.q.token_stride, to = (start + i) * r.q_out.token_stride;
-    for (int h0 = sub; h0 < r.q_heads; h0 += HEADS * AHEAD) {
+    for (int h0 = sub + wave * HEADS * AHEAD; h0 < r.q_heads; h0 += waves * HEADS * AHEAD) {
         uint4 lo[AHEAD], hi[AHEAD];
 #pragma unroll
         for (int k = 0; k < AHEAD; ++k) {
