@@ -10,6 +10,14 @@
 // Where a record has earlier positions, its power is at least theirs, and
 // where it grows their codes are rounded once more to it: exactly, but for
 // those that become subnormal.  Read goes the other way.
+//
+// Memory bounds both: 8 sequences of up to 4001 positions, 8 heads of 128
+// channels in fp16, 196 MB each way: append, turned, 47 us, 4.2 TB/s, read 36 us,
+// 5.4 TB/s, beside 4.9 TB/s of a large copy.  Two waves a record, as the keys'
+// and the values' powers and orders have nothing in common, leave a lane 32
+// numbers of 16 bits in registers at a time.  A few tokens (append8_few_kernel:
+// 32 sequences, one token each, 4.3 us) are a launch and four dependent loads:
+// lengths, table, power and rows, of which none can be left out.
 #include "tkv_rotate.h"
 
 namespace tkv {
