@@ -12,7 +12,7 @@
 // those that become subnormal.  Read goes the other way.
 //
 // Memory bounds both: 8 sequences of up to 4001 positions, 8 heads of 128
-// channels in fp16, 196 MB each way: append, turned, 47 us, 4.2 TB/s, read 36 us,
+// channels in fp16, 196 MB that move: append, turned, 47 us, 4.2 TB/s, read 36 us,
 // 5.4 TB/s, beside 4.9 TB/s of a large copy.  Two waves a record, as the keys'
 // and the values' powers and orders have nothing in common, leave a lane 32
 // numbers of 16 bits in registers at a time.  A few tokens (append8_few_kernel:

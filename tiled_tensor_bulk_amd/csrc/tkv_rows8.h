@@ -17,15 +17,17 @@
 // are held in units of a power of two that all waves raise alike when a record
 // with a larger one comes; a wave's sums follow when they take that record.
 //
-// What bounds it is the number of instructions that a SIMD's vector unit is
-// given: some 120 a wave and record beside 16 matrix instructions, of which the
-// 16 exponentials take four times an fma's time, 700 cycles of issue for 512 of
-// products; and a record's barrier and branches, which three waves on a SIMD (168
-// registers) hide better than two that make one record's products beside another's
-// softmax (137 us against 160).  128 channels, 8 heads of 4 rows, with the joining:
-// 512 new tokens each over 2 sequences of up to 8192 positions 141 us, 676 TFLOP/s,
-// where the longer one's workgroups are the last ones; 6000 tokens through a window
-// of 1024 137 us, 686 TFLOP/s.  Tiles of 16 rows, as with 4 bits, took 143 and 171.
+// What bounds it: by its counters a record takes a wave 124 vector instructions,
+// 630 cycles of issue (16 exponentials, at four times an fma's, are 256 of them),
+// and 512 cycles of matrix instructions, of 1500 that a SIMD has for them.  Of
+// what neither fills, a record's barrier and its branches are the cause, which
+// three waves on a SIMD (168 registers) hide better than two that make one
+// record's products beside another's softmax (137 us against 160).  128 channels,
+// 8 heads of 4 rows, with the joining: 512 new tokens each over 2 sequences of up
+// to 8192 positions 141 us, 676 TFLOP/s, where the longer one's workgroups are the
+// last ones; 6000 tokens through a window of 1024 137 us, 686 TFLOP/s.  Tiles of
+// 16 rows, as with 4 bits, took 143 and 171.
+//
 // 256 channels (304 TFLOP/s, 4 heads of 2 rows, the first of these) leave one wave
 // on a SIMD, and the products' sums in accumulation registers.
 #pragma once
