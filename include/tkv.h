@@ -16,7 +16,7 @@
  *
  * Numbers, 8 bits.  An element is 2^(E - 127) * code: code an e4m3 number (OCP,
  * largest 448), E a byte, one for the keys and one for the values of a record;
- * E = 0 stands for 0.
+ * E = 0 stands for 0, the codes being numbers.
  *
  * Record of 32 positions, 4 bits (dim = head_dim, W = dim / 32 words, groups =
  * dim / group; S = 2 where W > 4, else 1, and w = W / S):
@@ -155,7 +155,7 @@ typedef struct tkv_rotation {
                                  head_dim                                                      */
     int32_t neighbours;       /* 0: pairs (i, i + rot_dim / 2);  1: pairs (2 i, 2 i + 1)       */
     tkv_tokens q, q_out;      /* [n_tokens][q_heads][head_dim], fp16 or bf16, one type; q_out
-                                 may be q                                                      */
+                                 may be q, and else may not overlap it                         */
     int32_t q_heads;          /* 0: no queries                                                 */
 } tkv_rotation;
 tmap_status tkv_append_rotated(const tkv_cache *cache, const tkv_tokens *k, const tkv_tokens *v,
