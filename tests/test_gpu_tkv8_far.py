@@ -1,5 +1,6 @@
 """The 8-bit cache in a pool of more than 4 GiB: what lies in its last pages gives, bit for bit, what it gives in a small
-pool.  And calls on two streams, each with its own workspace, give what they give one after the other."""
+pool.  Calls on two streams, each with its own workspace, give what they give one after the other.  And a pool's description
+takes no account of groups."""
 import pytest
 
 pytestmark = pytest.mark.gpu
@@ -66,3 +67,17 @@ def test_calls_on_two_streams():
         torch.cuda.synchronize()
     for a, b in zip(want, got):
         assert all(torch.equal(x, y) for x, y in zip(a[:5], b[:5]))
+
+
+def test_groups_mean_nothing_in_8_bits():
+    say("groups")
+    size = T.tkv_page_bytes_of(2, 96, 32, bits=8)
+    pool = torch.zeros(3 * size, dtype=torch.uint8, device=DEV)
+    for group in (0, 64, 128):
+        cache = T.tkv_encode(pool, 2, 96, 32, group, bits=8)
+        assert (cache.n_pages, cache.group, cache.bits, T.tkv_page_bytes(cache)) == (3, 0, 8, size)
+    with pytest.raises(ValueError, match="multiple"):
+        T.tkv_encode(pool[:-16], 2, 96, 32, 0, bits=8)
+    for group in (0, 64):
+        with pytest.raises(ValueError, match="4 or 8"):
+            T.tkv_encode(pool, 2, 64, 32, group, bits=2)

@@ -576,18 +576,18 @@ struct Softmax {
 #pragma unroll
             for (int c = 0; c < D / 16; ++c) o[c] *= ratio;
         } else {
-        float ratio = 1.0f;
-        if constexpr (kOnes<D, GROUP>) {
-            const float rounded = __shfl(z[(2 * F::NG) & 3], 16 * (2 * F::NG / 4) + (lane & 15));
-            ratio = rounded > 0.0f ? l / rounded : 1.0f;
-        }
+            float ratio = 1.0f;
+            if constexpr (kOnes<D, GROUP>) {
+                const float rounded = __shfl(z[(2 * F::NG) & 3], 16 * (2 * F::NG / 4) + (lane & 15));
+                ratio = rounded > 0.0f ? l / rounded : 1.0f;
+            }
 #pragma unroll
-        for (int grp = 0; grp < F::NG; ++grp) {
-            const int from = 16 * (grp / 2) + (lane & 15);
-            const float zero = fmaf(8.0f, __shfl(z[(2 * grp) & 3], from), __shfl(z[(2 * grp + 1) & 3], from));
+            for (int grp = 0; grp < F::NG; ++grp) {
+                const int from = 16 * (grp / 2) + (lane & 15);
+                const float zero = fmaf(8.0f, __shfl(z[(2 * grp) & 3], from), __shfl(z[(2 * grp + 1) & 3], from));
 #pragma unroll
-            for (int c = grp * F::VG; c < (grp + 1) * F::VG; ++c) o[c] = (o[c] + zero) * ratio;
-        }
+                for (int c = grp * F::VG; c < (grp + 1) * F::VG; ++c) o[c] = (o[c] + zero) * ratio;
+            }
         }
     }
     // o in units of a power of two of its own

@@ -184,7 +184,7 @@ def tkv_encode(pool, n_heads: int, head_dim: int, page_tokens: int, group: int =
     if not pool.is_contiguous():
         raise ValueError("pool must be contiguous")
     c = tkv_cache()
-    each = tkv_page_bytes_of(n_heads, head_dim, page_tokens, group, bits) if group > 0 else 0
+    each = tkv_page_bytes_of(n_heads, head_dim, page_tokens, group, bits) if group > 0 or bits != 4 else 0
     n_pages = pool.numel() // each if each > 0 else 1
     if bits == 8:
         st = lib().tkv_encode8(ctypes.byref(c), pool.data_ptr(), n_pages, n_heads, head_dim, page_tokens)
@@ -193,9 +193,8 @@ def tkv_encode(pool, n_heads: int, head_dim: int, page_tokens: int, group: int =
     _check(st, "tkv_encode")
     if pool.numel() % each:
         raise ValueError(f"pool holds {pool.numel()} bytes, not a multiple of a page's {each}")
-    c.pool, c.n_heads, c.head_dim, c.page_tokens, c.group, c.n_pages = (pool, n_heads, head_dim, page_tokens, group,
-                                                                        n_pages)
-    c.bits = bits
+    c.pool, c.n_heads, c.head_dim, c.page_tokens, c.n_pages = pool, n_heads, head_dim, page_tokens, n_pages
+    c.group, c.bits = (group, 4) if bits == 4 else (0, 8)
     c.calls = _calls().Cache(ctypes.addressof(c), pool, n_heads, head_dim, page_tokens)
     return c
 
