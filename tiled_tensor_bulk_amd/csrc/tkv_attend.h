@@ -721,7 +721,7 @@ __device__ __forceinline__ void attend_piece(const AttendArgs &a, char *ring, in
                                     sum_parts<D, GROUP>(qsum[nt], g), sums_factor(factor[nt]));
     }
 
-    int units = 0;  // of o: 2^(units - 127)
+    int units = 0;  // of o: 2^(units - 127); 0: nothing but zeros has been summed
     for (int slot = 0; p0 < end; p0 += kStep, slot ^= 1) {
         static_assert(K::kDepth == 2, "slots alternate");
         if (p0 + kStep < end)
@@ -783,7 +783,7 @@ __device__ __forceinline__ void attend_piece(const AttendArgs &a, char *ring, in
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) s[nt].weights(x[nt], f[nt], p[nt]);
         if constexpr (k8) {
-            values8<D, NT>(rec, lane, power_of(power - units + 127), masked ? e.len - at : kTile, p, s);
+            values8<D, NT>(rec, lane, power_in(power, units), masked ? e.len - at : kTile, p, s);
         } else {
         h8 scale[F::NG];  // of the lane's 8 positions
 #pragma unroll

@@ -119,6 +119,11 @@ __device__ __forceinline__ h8 codes8(uint2 w, float power) {
 // 2^(e - 127), and 0 for e of 0 or less.
 __device__ __forceinline__ float power_of(int e) { return __builtin_bit_cast(float, (e > 0 ? e : 0) << 23); }
 
+// What the codes of a record of E = e are multiplied with in units of 2^(units -
+// 127).  E = 0 stands for 0, and not for the least of powers: units is 0 until
+// a record of another E has come, and what was summed by then is to be 0.
+__device__ __forceinline__ float power_in(int e, int units) { return e ? power_of(e - units + 127) : 0.0f; }
+
 // Bytes of a lane's 8 V codes whose positions are below `live`: 4 g .. 4 g + 3 in
 // the first word, and 16 more in the second.
 __device__ __forceinline__ uint32_t first_bytes(int n) { return n >= 4 ? ~0u : n <= 0 ? 0u : (1u << (8 * n)) - 1; }

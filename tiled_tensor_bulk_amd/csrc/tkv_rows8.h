@@ -221,13 +221,14 @@ __global__ void __launch_bounds__(64 * kAttendWaves, rows8_waves(D)) rows8_kerne
     keys.load(now.at, wave, lane);
     values.load(now.at + F::VC, wave, lane);
     now.settle(), next1.settle();
-    // sums are in units of 2^(units - 127), and values in those of the largest power up to them
+    // sums are in units of 2^(units - 127), 0 while nothing but zeros has been summed, and values in those of the
+    // largest power up to them
     int units = 0, units_now = now.values();
     drop_end(now);
 #pragma unroll
     for (int i = 0; i < Share::COUNT; ++i) {
         keys.unpack_keys(i, stage.k[0], wave, lane);
-        values.unpack_values(i, stage.v[0], wave, lane, 1.0f);
+        values.unpack_values(i, stage.v[0], wave, lane, power_in(units_now, units_now));
     }
     keys.load(next1.at, wave, lane);
     values.load(next1.at + F::VC, wave, lane);
@@ -269,7 +270,7 @@ __global__ void __launch_bounds__(64 * kAttendWaves, rows8_waves(D)) rows8_kerne
         find(next2, p0 + 2 * kTile);
         drop_end(next1);
         const int units_next = next1.values() > units_now ? next1.values() : units_now;
-        const float power = power_of(next1.values() - units_next + 127);
+        const float power = power_in(next1.values(), units_next);
         if (units_now > units) {
             if (units) scale_sums(__builtin_amdgcn_ldexpf(1.0f, units - units_now));
             units = units_now;
