@@ -144,7 +144,9 @@ tmap_status tkv_append(const tkv_cache *cache, const tkv_tokens *k, const tkv_to
  * turned in the same manner and rounded to their type.
  *   p is lens[b] + i for a sequence's i-th new token, or positions[row].  A
  *   token whose p is not in the table is left alone: neither its key nor its
- *   value is cached, and its query is not written.
+ *   value is cached, and its query is not written.  (In 8 bits a record none of
+ *   whose positions has been cached gets E = 0.  Attention takes every position
+ *   below lens[b] for a cached one.)
  */
 typedef struct tkv_rotation {
     const float *cos_sin;     /* [n_positions][rot_dim]: the pairs' cosines, then their sines  */

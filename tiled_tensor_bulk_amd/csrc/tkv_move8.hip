@@ -86,6 +86,11 @@ __device__ __forceinline__ uint32_t byte_mask(uint32_t bits) {
     return ((bits & 1) | (bits & 2) << 7 | (bits & 4) << 14 | (bits & 8) << 21) * 255u;
 }
 
+// Of a record that has no earlier positions and gets none, as the rotation's
+// table turns none of its new ones: later ones may count them, and would take
+// for its power what the byte was before.
+__device__ __forceinline__ void no_power_yet(char *ex) { *reinterpret_cast<uint8_t *>(ex) = 0; }
+
 template <int D, bool ROT>
 __global__ void __launch_bounds__(64 * kMoveWaves) append8_kernel(const MoveArgs a) {
     using F = Format<D, 0>;
@@ -143,7 +148,10 @@ __global__ void __launch_bounds__(64 * kMoveWaves) append8_kernel(const MoveArgs
     uint32_t fresh = mine_live;  // new positions, over the wave
 #pragma unroll
     for (int mask = 1; mask < 64; mask <<= 1) fresh |= __shfl_xor(fresh, mask);
-    if (!fresh) return;
+    if (!fresh) {  // all of them are left alone
+        if (!old && lane == 0) no_power_yet(ex);
+        return;
+    }
     int e = power_for(largest(top));
     e = e > had ? e : had;
     const float inverse = power_of(254 - e), shrunk = power_of(had - e + 127);
@@ -343,7 +351,10 @@ __global__ void __launch_bounds__(64 * kMoveWaves) append8_few_kernel(const Move
             top = fmaxf(top, fabsf(x[k][j]));
         }
     }
-    if (!live) return;
+    if (!live) {
+        if (!old && lane == 0) no_power_yet(ex);
+        return;
+    }
     int e = power_for(largest(top));
     e = e > had ? e : had;
     if (old && had < e) {
