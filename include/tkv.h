@@ -158,7 +158,7 @@ typedef struct tkv_rotation {
     int32_t neighbours;       /* 0: pairs (i, i + rot_dim / 2);  1: pairs (2 i, 2 i + 1)       */
     tkv_tokens q, q_out;      /* [n_tokens][q_heads][head_dim], fp16 or bf16, one type; q_out
                                  may be q, and else may not overlap it                         */
-    int32_t q_heads;          /* 0: no queries                                                 */
+    int32_t q_heads;          /* 0: no queries; at most 2^30                                   */
 } tkv_rotation;
 tmap_status tkv_append_rotated(const tkv_cache *cache, const tkv_tokens *k, const tkv_tokens *v,
                                const tkv_rotation *rotation, const tkv_batch *batch, void *hip_stream);

@@ -411,6 +411,7 @@ tmap_status rotation_args(const tkv_rotation *in, tkv::MoveArgs &a) {
                 "cos_sin is NULL or not 4-byte aligned");
     TKV_REQUIRE(aligned(in->positions, 4), "positions is not 4-byte aligned");
     TKV_REQUIRE(in->q_heads >= 0, "q_heads is negative");
+    TKV_REQUIRE(in->q_heads <= 1 << 30, "q_heads is more than 2^30");  // heads are counted in 31 bits, some past the last one
     r.table = in->cos_sin;
     r.stride = in->stride;
     r.positions = in->positions;
