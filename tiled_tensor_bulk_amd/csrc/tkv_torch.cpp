@@ -97,7 +97,7 @@ struct Table {
 Table table_of(const Tensor &t, const char *what, int64_t n_seq, const Cache &c) {
     typed(t, what, at::kInt, c);
     TKV_CHECK(t.dim() == 2 && t.size(0) == n_seq, what, " must be [", n_seq, ", pages]");
-    TKV_CHECK(t.stride(1) == 1 || t.numel() == 0, what, "'s rows must be contiguous");
+    TKV_CHECK(t.size(1) < 2 || t.stride(1) == 1 || t.numel() == 0, what, "'s rows must be contiguous");
     TKV_CHECK(n_seq < 2 || t.stride(0) >= t.size(1), what, "'s rows must not overlap");
     TKV_CHECK(t.size(1) <= INT32_MAX, what, " is too wide");
     return {t.data_ptr<int32_t>(), n_seq < 2 ? t.size(1) : t.stride(0), (int32_t)t.size(1)};
@@ -125,7 +125,7 @@ Batch batch(const Cache &c, const Tensor &table, const Tensor &lens, const Maybe
     const int32_t *first = nullptr;
     if (starts) {
         typed(*starts, "starts", at::kInt, c);
-        TKV_CHECK(starts->dim() == 1 && starts->size(0) == n_seq + 1 && starts->stride(0) == 1,
+        TKV_CHECK(starts->dim() == 1 && starts->size(0) == n_seq + 1 && (n_seq == 0 || starts->stride(0) == 1),
                   "starts must be a contiguous vector of sequences + 1");
         first = starts->data_ptr<int32_t>();
     } else {
