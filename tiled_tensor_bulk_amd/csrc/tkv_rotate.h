@@ -141,7 +141,9 @@ constexpr int kQueryHeads = 64 / (D / 16);  // rows that a wave has at once
 
 // Waves of a token's queries in a launch of few tokens.
 inline int query_waves(const MoveArgs &a, int64_t tokens, int heads_at_once) {
-    return tokens > kQueryTokens || a.rot.q_heads > kQueryWaves * heads_at_once ? 1 : (a.rot.q_heads + heads_at_once - 1) / heads_at_once;
+    if (tokens > kQueryTokens) return 1;
+    const int waves = (a.rot.q_heads + heads_at_once - 1) / heads_at_once;
+    return waves < kQueryWaves ? waves : kQueryWaves;
 }
 
 // The queries of one token by `waves` waves, of which this is one, AHEAD rows at a
