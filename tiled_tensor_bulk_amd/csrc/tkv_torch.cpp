@@ -244,11 +244,10 @@ int64_t bound(std::optional<int64_t> max_len, int64_t held) {
     return std::max<int64_t>(n, -1);
 }
 
-py::tuple do_attend_window(const Cache &c, const Tensor &q, const Tensor &table, const Tensor &lens, const Maybe &starts,
-                           std::optional<int64_t> max_new, std::optional<int64_t> max_len, std::optional<double> scale,
-                           bool causal, const Maybe &scores, const Maybe &scores_out, const Maybe &out_, const Maybe &lse_,
-                           const Maybe &workspace, std::optional<int64_t> stream, std::optional<int64_t> window, int64_t
-                           sinks) {
+py::tuple do_attend(const Cache &c, const Tensor &q, const Tensor &table, const Tensor &lens, const Maybe &starts,
+                    std::optional<int64_t> max_new, std::optional<int64_t> max_len, std::optional<double> scale, bool causal,
+                    const Maybe &scores, const Maybe &scores_out, const Maybe &out_, const Maybe &lse_, const Maybe &workspace,
+                    std::optional<int64_t> stream, std::optional<int64_t> window, int64_t sinks) {
     const Stream on(c, stream);
     TKV_CHECK(window || sinks == 0, "sinks are only apart from the others where a window is given");
     tkv_window seen{};
@@ -305,14 +304,6 @@ py::tuple do_attend_window(const Cache &c, const Tensor &q, const Tensor &table,
     return py::make_tuple(st, out, lse);
 }
 
-py::tuple do_attend(const Cache &c, const Tensor &q, const Tensor &table, const Tensor &lens, const Maybe &starts,
-                 std::optional<int64_t> max_new, std::optional<int64_t> max_len, std::optional<double> scale, bool causal,
-                 const Maybe &scores, const Maybe &scores_out, const Maybe &out, const Maybe &lse, const Maybe &workspace,
-                 std::optional<int64_t> stream) {
-    return do_attend_window(c, q, table, lens, starts, max_new, max_len, scale, causal, scores, scores_out, out, lse,
-                            workspace, stream, std::nullopt, 0);
-}
-
 py::tuple do_evict(const Cache &c, const Tensor &table, const Tensor &lens, const Tensor &scores, int64_t budget,
                 int64_t recent, const Tensor &dst_table, std::optional<int64_t> max_len, const Maybe &kept_,
                 const Maybe &lens_out_, const Maybe &scores_out_, std::optional<int64_t> stream) {
@@ -354,7 +345,9 @@ PYBIND11_MODULE(_tkv, m) {
     m.def("append", torch::wrap_pybind_function(do_append));
     m.def("append_rotated", torch::wrap_pybind_function(do_append_rotated));
     m.def("read", torch::wrap_pybind_function(do_read));
-    m.def("attend", torch::wrap_pybind_function(do_attend));
-    m.def("attend_window", torch::wrap_pybind_function(do_attend_window));
+    using py::arg;
+    m.def("attend", torch::wrap_pybind_function(do_attend), arg("cache"), arg("q"), arg("table"), arg("lens"), arg("starts"),
+          arg("max_new"), arg("max_len"), arg("scale"), arg("causal"), arg("scores"), arg("scores_out"), arg("out"),
+          arg("lse"), arg("workspace"), arg("stream"), arg("window") = py::none(), arg("sinks") = 0);
     m.def("evict", torch::wrap_pybind_function(do_evict));
 }

@@ -254,8 +254,8 @@ def tkv_attend(cache: tkv_cache, q, table, lens, starts=None, max_new: Optional[
     heads; may be scores itself (caches in 4 bits, no window).  workspace: a uint8 tensor of at least
     tkv_attend_workspace bytes.  window: a query sees only the last so many of its positions, and the first `sinks`;
     the pages between are not read, and may be missing."""
-    st, o, ls = _torch.attend_window(cache.calls, q, table, lens, starts, max_new, max_len, scale, causal, scores,
-                                     scores_out, out, lse, workspace, _stream(stream), window, sinks)
+    st, o, ls = _torch.attend(cache.calls, q, table, lens, starts, max_new, max_len, scale, causal, scores, scores_out, out,
+                              lse, workspace, _stream(stream), window, sinks)
     if stream is not None:
         _keep(stream, cache.pool.device, o if out is None else None, ls if lse is None else None)
     _check(st, "tkv_attend")
