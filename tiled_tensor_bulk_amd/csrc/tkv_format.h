@@ -314,9 +314,11 @@ __device__ __forceinline__ void load_to_lds(const char *base, uint32_t bytes, ui
 #undef TKV_LOADS
 }
 
-// The same for up to 12 KiB.
+// The same for any number of KiB that a wait can count twice (a ring's two
+// slots): 17 are the most there are, of an 8-bit record of 256 channels.
 template <int N>
 __device__ __forceinline__ void load_run_to_lds(const char *base, uint32_t bytes, uint32_t lds, uint32_t lane16) {
+    static_assert(2 * N < 64, "the counter's range");
     load_to_lds<(N < 4 ? N : 4)>(base, bytes, lds, lane16);
     if constexpr (N > 4) load_run_to_lds<N - 4>(base + 4096, bytes ? bytes - 4096 : 0, lds + 4096, lane16);
 }

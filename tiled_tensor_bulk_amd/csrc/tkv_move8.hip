@@ -14,8 +14,9 @@
 // Memory bounds both: 8 sequences of up to 4001 positions, 8 heads of 128
 // channels in fp16, 196 MB that move: append, turned, 47 us, 4.2 TB/s, read 36 us,
 // 5.4 TB/s, beside 4.9 TB/s of a large copy.  Two waves a record, as the keys'
-// and the values' powers and orders have nothing in common, leave a lane 32
-// numbers of 16 bits in registers at a time.  A few tokens (append8_few_kernel:
+// and the values' powers and orders have nothing in common, leave a lane 64
+// numbers of 16 bits, 32 registers, at a time (of 128 channels; of 64 half as
+// many, of 256 twice).  A few tokens (append8_few_kernel:
 // 32 sequences, one token each, 4.3 us) are a launch and four dependent loads:
 // lengths, table, power and rows, of which none can be left out.
 #include "tkv_rotate.h"

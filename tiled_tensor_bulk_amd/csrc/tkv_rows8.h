@@ -24,8 +24,8 @@
 // three waves on a SIMD (168 registers) hide better than two that make one
 // record's products beside another's softmax (137 us against 160).  128 channels,
 // 8 heads of 4 rows, with the joining: 512 new tokens each over 2 sequences of up
-// to 8192 positions 141 us, 676 TFLOP/s, where the longer one's workgroups are the
-// last ones; 6000 tokens through a window of 1024 137 us, 686 TFLOP/s.  Tiles of
+// to 8192 positions 141 us, 675 TFLOP/s, where the longer one's workgroups are the
+// last ones; 6000 tokens through a window of 1024 138 us, 680 TFLOP/s.  Tiles of
 // 16 rows, as with 4 bits, took 143 and 171.
 //
 // 256 channels (304 TFLOP/s, 4 heads of 2 rows, the first of these) leave one wave
